@@ -1,0 +1,86 @@
+// kv_internal.h -- parameters of the rotary-position and quantised-cache kernels (rope.cu,
+// kv_cache.cu, kv_attend.cu) and their launchers, called by oq_cache.cpp.
+#pragma once
+
+#include "oq_internal.h"
+
+namespace oq {
+
+// Rotary positions of up to two tensors (queries and keys) of the same tokens.
+struct RopeParams {
+    const void *x[2];
+    void *y[2];
+    int heads[2];                 // heads[1] = 0: one tensor
+    long long x_stride[2], y_stride[2];   // elements between tokens
+    const long long *pos;         // [T]
+    const double *turns;          // [rot / 2] turns a position
+    float amplitude;
+    int T, d, rot;
+    int inverse;
+};
+cudaError_t launch_rope(const RopeParams &p, int dtype, int layout, cudaStream_t st, int num_sms,
+                        std::string *why);
+
+// The paged cache as the kernels see it: codes [pages, kv_heads, page, row_bytes], norms
+// [pages, kv_heads, page]; slot = page index * page + offset.
+struct KvView {
+    uint8_t *codes[2];            // keys, values
+    float *norms[2];
+    long long pages;
+    int page_log2;
+    int kv_heads, d, bits, row_bytes;
+};
+
+struct KvWriteParams {
+    KvView c;
+    const void *x[2];             // keys, values: [T, kv_heads, d]
+    long long x_stride[2];
+    const long long *slots;       // [T], -1: skip
+    int T, h;
+    const uint16_t *ent;          // [d] perm | sign bit << 15
+    const uint32_t *tbl;          // quantizer grid words (each `tbl_copies` times)
+    int tbl_copies;
+    float eps, K;                 // as K1Params
+    int G, F;
+};
+cudaError_t launch_kv_write(const KvWriteParams &p, int dtype, cudaStream_t st, int num_sms,
+                            std::string *why);
+
+struct KvReadParams {
+    KvView c;
+    void *y[2];
+    long long y_stride[2];
+    const long long *slots;
+    int T, h;
+    const uint16_t *ent;
+    const float *cent;            // fp32 unit centroids
+    float scale;                  // 1 / sqrt(d h): norms times this, on the unnormalised transform
+};
+cudaError_t launch_kv_read(const KvReadParams &p, int dtype, cudaStream_t st, int num_sms,
+                           std::string *why);
+
+struct KvAttendParams {
+    KvView c;
+    const void *q;
+    void *out;
+    long long q_stride, out_stride;
+    int q_heads, group;           // group = q_heads / kv_heads
+    long long q_rows;             // rows of q and out
+    const int *q_start;           // [B + 1]
+    const int *prefix;            // [B]
+    const int *table;             // [B, table_width]
+    const long long *mask;        // [q_rows] or null
+    int B, table_width, max_nodes;
+    const uint16_t *ent;
+    const float *cent;
+    int h;
+    float qk_scale;               // scale * log2(e) / (sqrt(d) sqrt(h))
+    float o_scale;                // 1 / (sqrt(d) sqrt(h))
+};
+cudaError_t launch_kv_attend(const KvAttendParams &p, int dtype, cudaStream_t st, int num_sms,
+                             std::string *why);
+
+cudaError_t read_and_clear_kv_error(unsigned *out, cudaStream_t st);
+cudaError_t read_and_clear_attend_error(unsigned *out, cudaStream_t st);
+
+}  // namespace oq

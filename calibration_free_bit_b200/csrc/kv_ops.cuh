@@ -1,0 +1,68 @@
+// kv_ops.cuh -- helpers shared by the rotary-position and quantised-cache kernels: element
+// types, 16-byte vectors of them as fp32, one row's rotation by a warp, code extraction.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+namespace oq {
+namespace kvops {
+
+template <class E> __device__ __forceinline__ float to_f32(E v);
+template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <> __device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+
+template <class E> __device__ __forceinline__ E from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+// 16 bytes of elements <-> fp32.
+template <class E> struct Vec {
+    static constexpr int n = 16 / sizeof(E);
+    union { uint4 u; E e[n]; };
+    __device__ __forceinline__ void load(const E *p) { u = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void store(E *p) const { *reinterpret_cast<uint4 *>(p) = u; }
+};
+
+// The unnormalised block Walsh-Hadamard transform (blocks of h) of a row of D held by a warp:
+// lane l has positions l*(D/32) .. l*(D/32) + D/32 - 1.  It is its own transpose.
+template <int D>
+__device__ __forceinline__ void warp_wht(float (&z)[D / 32], int h, int lane) {
+    constexpr int N = D / 32;
+#pragma unroll
+    for (int s = 1; s < N; s <<= 1)
+        if (s < h) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (!(i & s)) {
+                    const float a = z[i], b = z[i | s];
+                    z[i] = a + b;
+                    z[i | s] = a - b;
+                }
+        }
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1)
+        if (s * N < h) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float o = __shfl_xor_sync(0xffffffffu, z[i], s);
+                z[i] = (lane & s) ? o - z[i] : z[i] + o;
+            }
+        }
+}
+
+// Code k of an LSB-first stream of `bits`-wide codes (bits <= 8) at `row` (byte loads).
+__device__ __forceinline__ uint32_t code_at(const uint8_t *row, int k, int bits) {
+    const int bit = k * bits, at = bit >> 3, sh = bit & 7;
+    uint32_t w = row[at];
+    if (sh + bits > 8)
+        w |= (uint32_t)row[at + 1] << 8;
+    return (w >> sh) & ((1u << bits) - 1u);
+}
+
+}  // namespace kvops
+}  // namespace oq

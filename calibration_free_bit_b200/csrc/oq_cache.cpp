@@ -1,0 +1,408 @@
+// oq_cache.cpp -- host side of the rotary positions and the quantised key/value cache: the calls
+// oq_build_rope .. oq_kv_attend of include/oq.h (argument checks, tables, launches).
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <new>
+
+#include "kv_internal.h"
+#include "oq_handles.h"
+
+using namespace oq::host;
+
+namespace {
+
+constexpr double kTwoPi = 6.283185307179586476925286766559;
+
+int elem_size(int dtype) { return dtype == OQ_F32 ? 4 : 2; }
+
+// Rows [tokens, heads, d] of a tensor: base and token stride must keep 16-byte vectors aligned.
+int check_rows(const char *who, const char *name, const void *p, long long stride, int dtype) {
+    if (!p)
+        return fail(OQ_EINVAL, "%s: %s is NULL", who, name);
+    if (!aligned16(p) || stride < 0 || (stride * elem_size(dtype)) % 16 != 0)
+        return fail(OQ_EINVAL, "%s: %s must be 16-byte aligned, with a token stride (%lld "
+                               "elements) that is a non-negative multiple of 16 bytes", who, name,
+                    stride);
+    return OQ_OK;
+}
+
+// The same for a tensor that is written: tokens must not overlap.
+int check_out_rows(const char *who, const char *name, const void *p, long long stride, int dtype,
+                   long long row) {
+    const int rc = check_rows(who, name, p, stride, dtype);
+    if (rc != OQ_OK)
+        return rc;
+    if (stride < row)
+        return fail(OQ_EINVAL, "%s: %s has a token stride of %lld elements, less than its "
+                               "heads * d = %lld", who, name, stride, row);
+    return OQ_OK;
+}
+
+int check_cache(const char *who, const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache,
+                oq::KvView *v) {
+    if (!r || !c || !cache)
+        return fail(OQ_EINVAL, "%s: null handle or cache", who);
+    if (cache->d != 128 && cache->d != 256)
+        return fail(OQ_EINVAL, "%s: head dimension %d (128 or 256)", who, cache->d);
+    if (r->d != cache->d || c->d != cache->d)
+        return fail(OQ_EINVAL, "%s: the cache has d = %d but the rotation has d = %d and the "
+                               "codebook d = %d", who, cache->d, r->d, c->d);
+    if (c->bits != cache->bits)
+        return fail(OQ_EINVAL, "%s: the cache has %d-bit codes but the codebook %d bits", who,
+                    cache->bits, c->bits);
+    if (cache->page_size < 16 || cache->page_size > 1024 ||
+        (cache->page_size & (cache->page_size - 1)) != 0)
+        return fail(OQ_EINVAL, "%s: page_size = %d must be a power of two in [16, 1024]", who,
+                    cache->page_size);
+    if (cache->kv_heads < 1 || cache->kv_heads > OQ_KV_MAX_HEADS)
+        return fail(OQ_EINVAL, "%s: kv_heads = %d not in [1, %d]", who, cache->kv_heads,
+                    OQ_KV_MAX_HEADS);
+    if (cache->num_pages < 1 || cache->num_pages > 0x7fffffffll)
+        return fail(OQ_EINVAL, "%s: num_pages = %lld not in [1, 2^31)", who, cache->num_pages);
+    if (!cache->k_codes || !cache->v_codes || !cache->k_norms || !cache->v_norms)
+        return fail(OQ_EINVAL, "%s: null cache pointer", who);
+    if (!aligned16(cache->k_codes) || !aligned16(cache->v_codes) || !aligned16(cache->k_norms) ||
+        !aligned16(cache->v_norms))
+        return fail(OQ_EINVAL, "%s: the cache's arrays must be 16-byte aligned", who);
+    v->codes[0] = cache->k_codes;
+    v->codes[1] = cache->v_codes;
+    v->norms[0] = cache->k_norms;
+    v->norms[1] = cache->v_norms;
+    v->pages = cache->num_pages;
+    v->page_log2 = 0;
+    while ((1 << v->page_log2) < cache->page_size)
+        ++v->page_log2;
+    v->kv_heads = cache->kv_heads;
+    v->d = cache->d;
+    v->bits = cache->bits;
+    v->row_bytes = cache->d * cache->bits / 8;
+    return OQ_OK;
+}
+
+int check_slots(const char *who, const int64_t *slots) {
+    if (!slots || (reinterpret_cast<uintptr_t>(slots) & 7u))
+        return fail(OQ_EINVAL, "%s: slots must be a non-null, 8-byte aligned pointer", who);
+    return OQ_OK;
+}
+
+int upload_ent(oq_rpbh *r, int dev) {
+    return upload(r->mu, &r->dev_ent16[dev], r->ent16, "upload rotation entries");
+}
+
+}  // namespace
+
+extern "C" {
+
+int oq_build_rope(int rot_dim, int layout, double theta, int scaling, double factor,
+                  int original_len, oq_rope **out) {
+    const char *who = "oq_build_rope";
+    if (!out)
+        return fail(OQ_EINVAL, "%s: out is NULL", who);
+    *out = nullptr;
+    if (rot_dim < 16 || rot_dim > 512 || rot_dim % 16 != 0)
+        return fail(OQ_EINVAL, "%s: rot_dim = %d must be a multiple of 16 in [16, 512]", who,
+                    rot_dim);
+    if (layout != OQ_ROPE_HALF && layout != OQ_ROPE_INTERLEAVED)
+        return fail(OQ_EINVAL, "%s: layout = %d (OQ_ROPE_HALF or OQ_ROPE_INTERLEAVED)", who,
+                    layout);
+    if (!(theta > 1.0) || !std::isfinite(theta))
+        return fail(OQ_EINVAL, "%s: theta must be finite and above 1", who);
+    if (scaling < OQ_ROPE_PLAIN || scaling > OQ_ROPE_YARN)
+        return fail(OQ_EINVAL, "%s: scaling = %d (OQ_ROPE_PLAIN .. OQ_ROPE_YARN)", who, scaling);
+    if (scaling != OQ_ROPE_PLAIN && !(factor >= 1.0 && std::isfinite(factor)))
+        return fail(OQ_EINVAL, "%s: factor must be finite and at least 1", who);
+    if (scaling == OQ_ROPE_YARN && original_len < 1)
+        return fail(OQ_EINVAL, "%s: original_len = %d must be positive", who, original_len);
+    oq_rope *r = new (std::nothrow) oq_rope;
+    if (!r)
+        return fail(OQ_ENOMEM, "%s: out of host memory", who);
+    r->rot = rot_dim;
+    r->layout = layout;
+    const int half = rot_dim / 2;
+    const double base =
+        scaling == OQ_ROPE_NTK ? theta * std::pow(factor, (double)rot_dim / (rot_dim - 2)) : theta;
+    r->freq.resize(half);
+    for (int i = 0; i < half; ++i)
+        r->freq[i] = std::pow(base, -2.0 * i / rot_dim);
+    if (scaling == OQ_ROPE_LINEAR)
+        for (double &f : r->freq)
+            f /= factor;
+    if (scaling == OQ_ROPE_YARN) {
+        // the pair that makes `turns` turns over the original length
+        auto pair_at = [&](double turns) {
+            return rot_dim * std::log(original_len / (turns * kTwoPi)) / (2.0 * std::log(theta));
+        };
+        const double lo = std::max(std::floor(pair_at(32.0)), 0.0);
+        const double hi = std::min(std::ceil(pair_at(1.0)), rot_dim - 1.0);
+        for (int i = 0; i < half; ++i) {
+            const double ramp = std::min(std::max((i - lo) / std::max(hi - lo, 1e-3), 0.0), 1.0);
+            r->freq[i] = r->freq[i] / factor * ramp + r->freq[i] * (1.0 - ramp);
+        }
+        r->amplitude = 0.1 * std::log(factor) + 1.0;
+    }
+    r->turns.resize(half);
+    for (int i = 0; i < half; ++i)
+        r->turns[i] = r->freq[i] / kTwoPi;
+    *out = r;
+    return OQ_OK;
+}
+
+int oq_rope_values(const oq_rope *r, double *freq, double *amplitude) {
+    if (!r)
+        return fail(OQ_EINVAL, "oq_rope_values: null handle");
+    if (freq)
+        std::memcpy(freq, r->freq.data(), sizeof(double) * r->freq.size());
+    if (amplitude)
+        *amplitude = r->amplitude;
+    return OQ_OK;
+}
+
+void oq_free_rope(oq_rope *r) {
+    if (!r)
+        return;
+    int cur = -1;
+    cudaGetDevice(&cur);
+    for (int dev = 0; dev < oq::kMaxDevices; ++dev)
+        if (r->dev_turns[dev]) {
+            cudaSetDevice(dev);
+            cudaFree(r->dev_turns[dev]);
+        }
+    if (cur >= 0)
+        cudaSetDevice(cur);
+    delete r;
+}
+
+int oq_apply_rope(const oq_rope *r, const oq_rope_rows *rows, int num_rows, int dtype, int T, int d,
+                  const int64_t *positions, int inverse, void *stream) {
+    const char *who = "oq_apply_rope";
+    if (!r || !rows)
+        return fail(OQ_EINVAL, "%s: null handle or rows", who);
+    if (num_rows != 1 && num_rows != 2)
+        return fail(OQ_EINVAL, "%s: num_rows = %d (1 or 2 tensors)", who, num_rows);
+    if (dtype != OQ_F32 && dtype != OQ_BF16 && dtype != OQ_F16)
+        return fail(OQ_EINVAL, "%s: dtype must be OQ_F32, OQ_BF16 or OQ_F16", who);
+    if (d < r->rot || d > 1024 || d % 16 != 0)
+        return fail(OQ_EINVAL, "%s: d = %d must be a multiple of 16 from rot_dim = %d to 1024",
+                    who, d, r->rot);
+    if (T < 0)
+        return fail(OQ_EINVAL, "%s: negative row count %d", who, T);
+    for (int i = 0; i < num_rows; ++i)
+        if (rows[i].heads < 1 || rows[i].heads > OQ_KV_MAX_HEADS)
+            return fail(OQ_EINVAL, "%s: heads = %d not in [1, %d]", who, rows[i].heads,
+                        OQ_KV_MAX_HEADS);
+    if (T == 0)
+        return OQ_OK;
+    if (!positions || (reinterpret_cast<uintptr_t>(positions) & 7u))
+        return fail(OQ_EINVAL, "%s: positions must be a non-null, 8-byte aligned pointer", who);
+    oq::RopeParams p{};
+    for (int i = 0; i < num_rows; ++i) {
+        int rc = check_rows(who, i ? "x[1]" : "x[0]", rows[i].x, rows[i].x_stride, dtype);
+        if (rc == OQ_OK)
+            rc = check_out_rows(who, i ? "y[1]" : "y[0]", rows[i].y, rows[i].y_stride, dtype,
+                                (long long)rows[i].heads * d);
+        if (rc != OQ_OK)
+            return rc;
+        if (rows[i].x == rows[i].y && rows[i].x_stride != rows[i].y_stride)
+            return fail(OQ_EINVAL, "%s: in place, x and y need the same token stride", who);
+        p.x[i] = rows[i].x;
+        p.y[i] = rows[i].y;
+        p.heads[i] = rows[i].heads;
+        p.x_stride[i] = rows[i].x_stride;
+        p.y_stride[i] = rows[i].y_stride;
+    }
+    int dev;
+    DeviceInfo *di;
+    int rc = current_device(&dev, &di);
+    if (rc != OQ_OK)
+        return rc;
+    oq_rope *rw = const_cast<oq_rope *>(r);
+    if ((rc = upload(rw->mu, &rw->dev_turns[dev], rw->turns, "upload rotary frequencies")) != OQ_OK)
+        return rc;
+    p.pos = reinterpret_cast<const long long *>(positions);
+    p.turns = reinterpret_cast<const double *>(rw->dev_turns[dev]);
+    p.amplitude = (float)r->amplitude;
+    p.T = T;
+    p.d = d;
+    p.rot = r->rot;
+    p.inverse = inverse != 0;
+    cudaStream_t st = (cudaStream_t)stream;
+    std::string why;
+    cudaError_t e = timed(OQ_KERNEL_ROPE, st, [&] {
+        return oq::launch_rope(p, dtype, r->layout, st, di->sms, &why);
+    });
+    return e == cudaSuccess ? OQ_OK : fail_cuda(e, why.c_str());
+}
+
+int oq_kv_write(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache, const void *k,
+                long long k_stride, const void *v, long long v_stride, int dtype, int T,
+                const int64_t *slots, void *stream) {
+    const char *who = "oq_kv_write";
+    oq::KvWriteParams p{};
+    int rc = check_cache(who, r, c, cache, &p.c);
+    if (rc != OQ_OK)
+        return rc;
+    if (dtype != OQ_F32 && dtype != OQ_BF16 && dtype != OQ_F16)
+        return fail(OQ_EINVAL, "%s: dtype must be OQ_F32, OQ_BF16 or OQ_F16", who);
+    if (T < 0)
+        return fail(OQ_EINVAL, "%s: negative row count %d", who, T);
+    if (T == 0)
+        return OQ_OK;
+    if ((rc = check_rows(who, "k", k, k_stride, dtype)) != OQ_OK ||
+        (rc = check_rows(who, "v", v, v_stride, dtype)) != OQ_OK ||
+        (rc = check_slots(who, slots)) != OQ_OK)
+        return rc;
+    int dev;
+    DeviceInfo *di;
+    if ((rc = current_device(&dev, &di)) != OQ_OK)
+        return rc;
+    oq_rpbh *rw = const_cast<oq_rpbh *>(r);
+    oq_codebook *cw = const_cast<oq_codebook *>(c);
+    if ((rc = upload_ent(rw, dev)) != OQ_OK ||
+        (rc = upload(cw->mu, &cw->dev_tbl[dev], cw->tbl_img, "upload quantizer table")) != OQ_OK)
+        return rc;
+    p.x[0] = k;
+    p.x[1] = v;
+    p.x_stride[0] = k_stride;
+    p.x_stride[1] = v_stride;
+    p.slots = reinterpret_cast<const long long *>(slots);
+    p.T = T;
+    p.h = r->h;
+    p.ent = reinterpret_cast<const uint16_t *>(rw->dev_ent16[dev]);
+    p.tbl = cw->dev_tbl[dev];
+    p.tbl_copies = c->bits <= 4 ? 32 : 1;
+    p.eps = 1e-8f;
+    p.K = (float)(std::sqrt((double)r->d / r->h) / (c->G * c->delta));
+    p.G = c->G;
+    p.F = c->F;
+    cudaStream_t st = (cudaStream_t)stream;
+    std::string why;
+    cudaError_t e = timed(OQ_KERNEL_KV_WRITE, st, [&] {
+        return oq::launch_kv_write(p, dtype, st, di->sms, &why);
+    });
+    return e == cudaSuccess ? OQ_OK : fail_cuda(e, why.c_str());
+}
+
+int oq_kv_read(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache,
+               const int64_t *slots, int T, void *k, long long k_stride, void *v,
+               long long v_stride, int dtype, void *stream) {
+    const char *who = "oq_kv_read";
+    oq::KvReadParams p{};
+    int rc = check_cache(who, r, c, cache, &p.c);
+    if (rc != OQ_OK)
+        return rc;
+    if (dtype != OQ_F32 && dtype != OQ_BF16 && dtype != OQ_F16)
+        return fail(OQ_EINVAL, "%s: dtype must be OQ_F32, OQ_BF16 or OQ_F16", who);
+    if (T < 0)
+        return fail(OQ_EINVAL, "%s: negative row count %d", who, T);
+    if (T == 0)
+        return OQ_OK;
+    const long long row = (long long)cache->kv_heads * cache->d;
+    if ((rc = check_out_rows(who, "k", k, k_stride, dtype, row)) != OQ_OK ||
+        (rc = check_out_rows(who, "v", v, v_stride, dtype, row)) != OQ_OK ||
+        (rc = check_slots(who, slots)) != OQ_OK)
+        return rc;
+    int dev;
+    DeviceInfo *di;
+    if ((rc = current_device(&dev, &di)) != OQ_OK)
+        return rc;
+    oq_rpbh *rw = const_cast<oq_rpbh *>(r);
+    oq_codebook *cw = const_cast<oq_codebook *>(c);
+    if ((rc = upload_ent(rw, dev)) != OQ_OK ||
+        (rc = upload(cw->mu, &cw->dev_cent32[dev], cw->cent32, "upload centroids")) != OQ_OK)
+        return rc;
+    p.y[0] = k;
+    p.y[1] = v;
+    p.y_stride[0] = k_stride;
+    p.y_stride[1] = v_stride;
+    p.slots = reinterpret_cast<const long long *>(slots);
+    p.T = T;
+    p.h = r->h;
+    p.ent = reinterpret_cast<const uint16_t *>(rw->dev_ent16[dev]);
+    p.cent = reinterpret_cast<const float *>(cw->dev_cent32[dev]);
+    p.scale = (float)(1.0 / std::sqrt((double)r->d * r->h));
+    cudaStream_t st = (cudaStream_t)stream;
+    std::string why;
+    cudaError_t e = timed(OQ_KERNEL_KV_READ, st, [&] {
+        return oq::launch_kv_read(p, dtype, st, di->sms, &why);
+    });
+    return e == cudaSuccess ? OQ_OK : fail_cuda(e, why.c_str());
+}
+
+int oq_kv_attend(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache, const void *q,
+                 long long q_stride, void *out, long long out_stride, int dtype, int q_rows,
+                 int q_heads, const int32_t *q_start, const int32_t *prefix, int B, int max_nodes,
+                 const int32_t *page_table, int table_width, const int64_t *tree_mask,
+                 double scale, void *stream) {
+    const char *who = "oq_kv_attend";
+    oq::KvAttendParams p{};
+    int rc = check_cache(who, r, c, cache, &p.c);
+    if (rc != OQ_OK)
+        return rc;
+    if (dtype != OQ_BF16 && dtype != OQ_F16)
+        return fail(OQ_EINVAL, "%s: dtype must be OQ_BF16 or OQ_F16", who);
+    if (q_heads < 1 || q_heads > OQ_KV_MAX_HEADS || q_heads % cache->kv_heads != 0)
+        return fail(OQ_EINVAL, "%s: q_heads = %d must be a multiple of kv_heads = %d, at most %d",
+                    who, q_heads, cache->kv_heads, OQ_KV_MAX_HEADS);
+    if (q_rows < 0 || B < 0 || B > 65535)
+        return fail(OQ_EINVAL, "%s: q_rows = %d and B = %d must be non-negative, B at most 65535",
+                    who, q_rows, B);
+    if (max_nodes < 1 || max_nodes > OQ_KV_MAX_NODES)
+        return fail(OQ_EINVAL, "%s: max_nodes = %d not in [1, %d]", who, max_nodes,
+                    OQ_KV_MAX_NODES);
+    if (table_width < 1 || ((long long)table_width << p.c.page_log2) > 0x7fffffffll)
+        return fail(OQ_EINVAL, "%s: table_width = %d must be positive, and hold fewer than 2^31 "
+                               "tokens", who, table_width);
+    if (!(scale > 0.0) || !std::isfinite(scale))
+        return fail(OQ_EINVAL, "%s: scale must be positive and finite", who);
+    if (q_rows == 0 || B == 0)
+        return OQ_OK;
+    if ((rc = check_rows(who, "q", q, q_stride, dtype)) != OQ_OK ||
+        (rc = check_out_rows(who, "out", out, out_stride, dtype, (long long)q_heads * cache->d)) !=
+            OQ_OK)
+        return rc;
+    if (!q_start || !prefix || !page_table)
+        return fail(OQ_EINVAL, "%s: null q_start, prefix or page_table", who);
+    if (((reinterpret_cast<uintptr_t>(q_start) | reinterpret_cast<uintptr_t>(prefix) |
+          reinterpret_cast<uintptr_t>(page_table)) & 3u) ||
+        (reinterpret_cast<uintptr_t>(tree_mask) & 7u))
+        return fail(OQ_EINVAL, "%s: q_start, prefix and page_table must be 4-byte aligned, "
+                               "tree_mask 8-byte", who);
+    int dev;
+    DeviceInfo *di;
+    if ((rc = current_device(&dev, &di)) != OQ_OK)
+        return rc;
+    oq_rpbh *rw = const_cast<oq_rpbh *>(r);
+    oq_codebook *cw = const_cast<oq_codebook *>(c);
+    if ((rc = upload_ent(rw, dev)) != OQ_OK ||
+        (rc = upload(cw->mu, &cw->dev_cent32[dev], cw->cent32, "upload centroids")) != OQ_OK)
+        return rc;
+    p.q = q;
+    p.out = out;
+    p.q_stride = q_stride;
+    p.out_stride = out_stride;
+    p.q_heads = q_heads;
+    p.group = q_heads / cache->kv_heads;
+    p.q_rows = q_rows;
+    p.q_start = q_start;
+    p.prefix = prefix;
+    p.table = page_table;
+    p.mask = reinterpret_cast<const long long *>(tree_mask);
+    p.B = B;
+    p.table_width = table_width;
+    p.max_nodes = max_nodes;
+    p.ent = reinterpret_cast<const uint16_t *>(rw->dev_ent16[dev]);
+    p.cent = reinterpret_cast<const float *>(cw->dev_cent32[dev]);
+    p.h = r->h;
+    const double unit = 1.0 / std::sqrt((double)r->d * r->h);
+    p.qk_scale = (float)(scale * 1.4426950408889634 * unit);
+    p.o_scale = (float)unit;
+    cudaStream_t st = (cudaStream_t)stream;
+    std::string why;
+    cudaError_t e = timed(OQ_KERNEL_KV_ATTEND, st, [&] {
+        return oq::launch_kv_attend(p, dtype, st, di->sms, &why);
+    });
+    return e == cudaSuccess ? OQ_OK : fail_cuda(e, why.c_str());
+}
+
+}  // extern "C"

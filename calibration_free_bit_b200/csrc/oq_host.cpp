@@ -16,14 +16,21 @@
 #include <new>
 
 #include "decode4.cuh"
+#include "kv_internal.h"
+#include "oq_handles.h"
 #include "oq_internal.h"
 
-namespace {
+using namespace oq::host;
 
+namespace {
 thread_local std::string g_last_error = "no error";
+}  // namespace
+
+namespace oq {
+namespace host {
 
 int fail(int code, const char *fmt, ...) {
-    char buf[512];
+    char buf[1024];
     va_list ap;
     va_start(ap, fmt);
     vsnprintf(buf, sizeof buf, fmt, ap);
@@ -36,15 +43,20 @@ int fail_cuda(cudaError_t e, const char *what) {
     return fail(OQ_ECUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-// Optional per-kernel timing (oq_timing_enable / oq_timing_collect): events recorded on the
-// caller's stream around every kernel this thread launches through the C ABI.
-struct TimedLaunch {
-    int kernel;
-    cudaEvent_t start, stop;
-};
+}  // namespace host
+}  // namespace oq
+
+namespace {
 thread_local bool g_timing = false;
 thread_local std::vector<TimedLaunch> g_timed;
 thread_local std::vector<cudaEvent_t> g_event_pool;
+
+}  // namespace
+
+namespace oq {
+namespace host {
+
+bool timing_on() { return g_timing; }
 
 cudaEvent_t take_event() {
     if (!g_event_pool.empty()) {
@@ -58,27 +70,12 @@ cudaEvent_t take_event() {
     return e;
 }
 
-// Run `launch` (returning cudaError_t), bracketed by events when timing is on.  While the
-// stream is being captured into a CUDA graph the events are recorded as external event nodes,
-// so each replay of the graph re-records them and they stay readable afterwards.
-template <class F>
-cudaError_t timed(int kernel, cudaStream_t st, F &&launch) {
-    if (!g_timing)
-        return launch();
-    TimedLaunch t{kernel, take_event(), take_event()};
-    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-    cudaStreamIsCapturing(st, &cs);
-    const unsigned flags =
-        cs == cudaStreamCaptureStatusActive ? cudaEventRecordExternal : cudaEventRecordDefault;
-    if (t.start)
-        cudaEventRecordWithFlags(t.start, st, flags);
-    cudaError_t e = launch();
-    if (t.stop)
-        cudaEventRecordWithFlags(t.stop, st, flags);
-    if (t.start && t.stop)
-        g_timed.push_back(t);
-    return e;
-}
+void keep_timed(const TimedLaunch &t) { g_timed.push_back(t); }
+
+}  // namespace host
+}  // namespace oq
+
+namespace {
 
 // Armed test of the kernels' bounded waits (oq_debug_arm_wait_timeout): one-shot, per thread.
 thread_local int g_armed_kernel = 0;
@@ -319,35 +316,6 @@ uint16_t to_half_bits(double x) {
 
 }  // namespace
 
-// ---------------------------------------------------------------------------------------
-// Handles.
-// ---------------------------------------------------------------------------------------
-struct oq_rpbh {
-    int d = 0, h = 0;
-    uint64_t seed = 0;
-    std::vector<int32_t> perm;
-    std::vector<int8_t> sign;
-    std::vector<uint32_t> ent_img[2];             // K1 gather-entry images: [0] bf16, [1] fp32
-    std::vector<uint16_t> ent16;                  // tensor-core K1: perm[i] | sign bit << 15
-    std::mutex mu;
-    uint32_t *dev_ent[2][oq::kMaxDevices] = {};
-    uint32_t *dev_ent16[oq::kMaxDevices] = {};
-};
-
-struct oq_codebook {
-    int d = 0, bits = 0, marginal = OQ_MARGINAL_GAUSSIAN;
-    std::vector<double> c, t;                     // unit centroids / boundaries
-    uint16_t lut[256] = {};                       // unit centroids, fp16 bits
-    int G = 0, F = 0;
-    double delta = 0.0;
-    std::vector<uint32_t> grid;                   // G + 1 words
-    std::vector<uint32_t> tbl_img;                // K1 shared-memory image of the table
-    std::vector<uint32_t> dec_img;                // K1 fp16 output: byte -> centroids (b 2,4,8)
-    std::mutex mu;
-    uint32_t *dev_tbl[oq::kMaxDevices] = {};
-    uint32_t *dev_dec[oq::kMaxDevices] = {};
-};
-
 namespace {
 
 // Uniform grid over the unit axis with at most one boundary per cell; see include/oq.h.
@@ -406,16 +374,13 @@ bool build_grid(oq_codebook *cb) {
     return false;
 }
 
-struct DeviceInfo {
-    int checked = 0;       // 0 unknown, 1 ok, -1 unsupported
-    int sms = 0;
-    cudaMemPool_t pool = nullptr;
-    cudaStream_t side = nullptr;      // oq_quantized_linear: weight decode beside K1
-    cudaEvent_t fork = nullptr, join = nullptr;
-    uint32_t *gelu_tab = nullptr;     // the fused GELU's table (oq::gelu_table_image)
-};
 DeviceInfo g_dev[oq::kMaxDevices];
 std::mutex g_dev_mu;
+
+}  // namespace
+
+namespace oq {
+namespace host {
 
 int current_device(int *dev_out, DeviceInfo **info_out) {
     int dev = 0;
@@ -444,25 +409,10 @@ int current_device(int *dev_out, DeviceInfo **info_out) {
     return OQ_OK;
 }
 
-template <class T>
-int upload(std::mutex &mu, uint32_t **slot, const std::vector<T> &host, const char *what) {
-    std::lock_guard<std::mutex> lk(mu);
-    if (*slot)
-        return OQ_OK;
-    void *p = nullptr;
-    cudaError_t e = cudaMalloc(&p, host.size() * sizeof(T));
-    if (e != cudaSuccess)
-        return fail_cuda(e, what);
-    e = cudaMemcpy(p, host.data(), host.size() * sizeof(T), cudaMemcpyHostToDevice);
-    if (e != cudaSuccess) {
-        cudaFree(p);
-        return fail_cuda(e, what);
-    }
-    *slot = static_cast<uint32_t *>(p);
-    return OQ_OK;
-}
+}  // namespace host
+}  // namespace oq
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+namespace {
 
 // y rows are written by TMA tensor stores, whose global row stride must be a multiple of 16
 // bytes: out_features a multiple of 4 for fp32 y, of 8 for bf16 y.
@@ -1071,8 +1021,11 @@ int oq_lloyd_max_marginal(int d, int bits, int marginal, oq_codebook **out) {
     cb->t.resize(L - 1);
     for (int j = 0; j < L - 1; ++j)
         cb->t[j] = 0.5 * (cb->c[j] + cb->c[j + 1]);
-    for (int i = 0; i < L; ++i)
+    cb->cent32.resize((size_t)(L + 3) / 4 * 4);
+    for (int i = 0; i < L; ++i) {
         cb->lut[i] = to_half_bits(cb->c[i]);
+        cb->cent32[i] = (float)cb->c[i];
+    }
     if (!build_grid(cb)) {
         delete cb;
         return fail(OQ_EINVAL, "%s: could not build the quantizer grid", who);
@@ -1489,7 +1442,7 @@ int oq_check(void *stream) {
     cudaError_t e = cudaStreamSynchronize(st);
     if (e != cudaSuccess)
         return fail_cuda(e, "oq_check: stream synchronize");
-    unsigned w1 = 0, w2 = 0, w3 = 0, w4 = 0;
+    unsigned w1 = 0, w2 = 0, w3 = 0, w4 = 0, w5 = 0, w6 = 0;
     if ((e = oq::read_and_clear_k1_error(&w1, st)) != cudaSuccess)
         return fail_cuda(e, "oq_check: read k1 error word");
     if ((e = oq::read_and_clear_k3_error(&w4, st)) != cudaSuccess)
@@ -1498,6 +1451,17 @@ int oq_check(void *stream) {
         return fail_cuda(e, "oq_check: read k1 (tensor-core) error word");
     if ((e = oq::read_and_clear_k2_error(&w2, st)) != cudaSuccess)
         return fail_cuda(e, "oq_check: read k2 error word");
+    if ((e = oq::read_and_clear_kv_error(&w5, st)) != cudaSuccess)
+        return fail_cuda(e, "oq_check: read cache error word");
+    if ((e = oq::read_and_clear_attend_error(&w6, st)) != cudaSuccess)
+        return fail_cuda(e, "oq_check: read attention error word");
+    if (w5 || w6)
+        return fail(OQ_EDEVICE, "device error word: cache=0x%x attend=0x%x quantize=0x%x "
+                                "quantize_tc=0x%x linear=0x%x fused=0x%x (cache bit 1 = a slot "
+                                "outside the cache, 2 = a bounded wait gave up; attend bits "
+                                "1/2/4/8 = query ranges/lengths/page index/a bounded wait gave "
+                                "up; what such a row names was skipped)",
+                    w5, w6, w1, w3, w2, w4);
     if (w1 || w2 || w3 || w4)
         return fail(OQ_EDEVICE, "device error word: quantize=0x%x quantize_tc=0x%x linear=0x%x "
                                 "fused=0x%x (a bounded wait gave up; quantize bits 1/2 = row "
@@ -1544,6 +1508,10 @@ void oq_free_codebook(oq_codebook *cb) {
         if (cb->dev_dec[dev]) {
             cudaSetDevice(dev);
             cudaFree(cb->dev_dec[dev]);
+        }
+        if (cb->dev_cent32[dev]) {
+            cudaSetDevice(dev);
+            cudaFree(cb->dev_cent32[dev]);
         }
     }
     if (cur >= 0)

@@ -6,7 +6,9 @@ of the library (there is no CPU fallback): build it with ``python -m
 calibration_free_bit_b200.build`` or ``__graft_entry__.build()``.
 
 Names follow the C ABI: oq_build_rpbh, oq_lloyd_max, oq_quantize_weight, oq_quantize_act,
-oq_linear (plus oq_check and the introspection calls used by the tests).
+oq_linear, and for attention beside the quantized layers oq_build_rope, oq_apply_rope,
+oq_kv_write, oq_kv_read, oq_kv_attend (plus oq_check and the introspection calls used by the
+tests).
 """
 from __future__ import annotations
 
@@ -23,7 +25,7 @@ LIB_PATH = os.path.join(_PKG, "liboq.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "oq.h")
 
 OQ_OK, OQ_EINVAL, OQ_EUNSUPPORTED, OQ_ECUDA, OQ_EDEVICE, OQ_ENOMEM = 0, -1, -2, -3, -4, -5
-OQ_F32, OQ_BF16 = 0, 1
+OQ_F32, OQ_BF16, OQ_F16 = 0, 1, 2
 
 _lib = None
 
@@ -68,7 +70,18 @@ def lib():
     L.oq_timing_collect.argtypes = [vp, i32, C.POINTER(i32)]
     L.oq_last_error.restype = C.c_char_p
     L.oq_version.restype = C.c_char_p
-    for name in ("oq_build_rpbh", "oq_build_block_rht", "oq_rpbh_tables", "oq_lloyd_max", "oq_lloyd_max_marginal",
+    i64, f64 = C.c_longlong, C.c_double
+    L.oq_build_rope.argtypes = [i32, i32, f64, i32, f64, i32, C.POINTER(vp)]
+    L.oq_rope_values.argtypes = [vp, vp, C.POINTER(f64)]
+    L.oq_free_rope.argtypes = [vp]
+    L.oq_free_rope.restype = None
+    L.oq_apply_rope.argtypes = [vp, vp, i32, i32, i32, i32, vp, i32, vp]
+    L.oq_kv_write.argtypes = [vp, vp, vp, vp, i64, vp, i64, i32, i32, vp, vp]
+    L.oq_kv_read.argtypes = [vp, vp, vp, vp, i32, vp, i64, vp, i64, i32, vp]
+    L.oq_kv_attend.argtypes = [vp, vp, vp, vp, i64, vp, i64, i32, i32, i32, vp, vp, i32, i32, vp,
+                               i32, vp, f64, vp]
+    for name in ("oq_build_rope", "oq_rope_values", "oq_apply_rope", "oq_kv_write", "oq_kv_read",
+                 "oq_kv_attend", "oq_build_rpbh", "oq_build_block_rht", "oq_rpbh_tables", "oq_lloyd_max", "oq_lloyd_max_marginal",
                  "oq_codebook_values",
                  "oq_codebook_grid", "oq_quantize_weight", "oq_quantize_act",
                  "oq_quantize_act_gelu", "oq_linear", "oq_quantized_linear",
@@ -271,13 +284,249 @@ def oq_linear_noalloc(ca: Codebook, cw: Codebook, x_codes: torch.Tensor, s: torc
     return y
 
 
+# ---- rotary positions and the quantised key/value cache ------------------------------------
+
+OQ_ROPE_HALF, OQ_ROPE_INTERLEAVED = 0, 1
+OQ_ROPE_PLAIN, OQ_ROPE_LINEAR, OQ_ROPE_NTK, OQ_ROPE_YARN = 0, 1, 2, 3
+ROPE_LAYOUTS = {"half": OQ_ROPE_HALF, "interleaved": OQ_ROPE_INTERLEAVED}
+ROPE_SCALINGS = {"plain": OQ_ROPE_PLAIN, "linear": OQ_ROPE_LINEAR, "ntk": OQ_ROPE_NTK,
+                 "yarn": OQ_ROPE_YARN}
+_ROW_DTYPES = {torch.float32: OQ_F32, torch.bfloat16: OQ_BF16, torch.float16: OQ_F16}
+
+
+def _bad(msg: str):
+    raise OQError(OQ_EINVAL, msg)
+
+
+def _rows(t: torch.Tensor, what: str, heads=None, d=None, dtype=None):
+    """A [tokens, heads, d] tensor whose heads of a token are contiguous; returns its token
+    stride in elements."""
+    if t.dim() != 3 or t.dtype not in _ROW_DTYPES:
+        _bad(f"{what} must be [tokens, heads, d] of fp32, bf16 or fp16")
+    if (heads is not None and t.shape[1] != heads) or (d is not None and t.shape[2] != d):
+        _bad(f"{what} has shape {tuple(t.shape)}: expected [tokens, {heads}, {d}]")
+    if dtype is not None and t.dtype != dtype:
+        _bad(f"{what} has dtype {t.dtype}: expected {dtype}")
+    n, h, e = t.shape
+    if (e > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != e):
+        _bad(f"{what}: the heads of a token must be contiguous")
+    return t.stride(0) if n > 1 else h * e
+
+
+def _ints(t: torch.Tensor, what: str, dtype, shape):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        _bad(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+             f"{tuple(t.shape)}")
+    return t.data_ptr()
+
+
+class _On:
+    """The device all of a call's tensors are on, made current for the call if it is not."""
+
+    def __init__(self, *tensors):
+        dev = tensors[0].device
+        for t in tensors:
+            if t is not None and t.device != dev:
+                _bad(f"tensors on {dev} and {t.device}: all must be on one device")
+        if dev.type != "cuda":
+            _bad(f"tensors on {dev}: a CUDA device is needed")
+        self._dev = dev.index
+        self._guard = None
+
+    def __enter__(self):
+        if self._dev != torch.cuda.current_device():
+            self._guard = torch.cuda.device(self._dev)
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+class Rope:
+    """Handle of rotary positions (oq_build_rope)."""
+
+    def __init__(self, rot_dim: int, layout: str = "half", theta: float = 10000.0,
+                 scaling: str = "plain", factor: float = 1.0, original_len: int = 1):
+        if layout not in ROPE_LAYOUTS or scaling not in ROPE_SCALINGS:
+            _bad(f"layout {layout!r} ({', '.join(ROPE_LAYOUTS)}), scaling {scaling!r} "
+                 f"({', '.join(ROPE_SCALINGS)})")
+        self._h = C.c_void_p()
+        _check(lib().oq_build_rope(rot_dim, ROPE_LAYOUTS[layout], theta, ROPE_SCALINGS[scaling],
+                                   factor, original_len, C.byref(self._h)))
+        self.rot_dim, self.layout, self.scaling = rot_dim, layout, scaling
+
+    @property
+    def handle(self):
+        return self._h
+
+    def values(self):
+        """(freq fp64 [rot_dim/2] in radians a position, amplitude)."""
+        freq = np.empty(self.rot_dim // 2, dtype=np.float64)
+        amp = C.c_double(0)
+        _check(lib().oq_rope_values(self._h, freq.ctypes.data, C.byref(amp)))
+        return freq, amp.value
+
+    def __del__(self):
+        if getattr(self, "_h", None) and self._h.value and _lib is not None:
+            _lib.oq_free_rope(self._h)
+            self._h = C.c_void_p()
+
+
+def oq_build_rope(rot_dim: int, layout: str = "half", theta: float = 10000.0,
+                  scaling: str = "plain", factor: float = 1.0, original_len: int = 1) -> Rope:
+    return Rope(rot_dim, layout, theta, scaling, factor, original_len)
+
+
+class _RopeRows(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("y", C.c_void_p), ("heads", C.c_int),
+                ("x_stride", C.c_longlong), ("y_stride", C.c_longlong)]
+
+
+def oq_apply_rope(rope: Rope, x: torch.Tensor, positions: torch.Tensor, k=None, out=None,
+                  k_out=None, inverse: bool = False, stream=None):
+    """Rotary positions of x [T, heads, d] and, in the same launch, of k [T, k_heads, d] (fp32,
+    bf16 or fp16; token stride free); positions int64 [T].  inverse=True applies the transpose
+    (gradients).  Returns out, or (out, k_out); out=x works in place."""
+    T, heads, d = x.shape if x.dim() == 3 else (0, 0, 0)
+    pairs = [(x, out, "x")] + ([(k, k_out, "k")] if k is not None else [])
+    rows = (_RopeRows * len(pairs))()
+    outs = []
+    for i, (a, b, what) in enumerate(pairs):
+        xs = _rows(a, what, d=d, dtype=x.dtype)
+        if a.shape[0] != T:
+            _bad(f"{what} has {a.shape[0]} tokens, x {T}")
+        if b is None:
+            b = torch.empty(a.shape, dtype=a.dtype, device=a.device)
+        ys = _rows(b, f"the output of {what}", a.shape[1], d, x.dtype)
+        if b.shape[0] != T:
+            _bad(f"the output of {what} has {b.shape[0]} tokens, x {T}")
+        rows[i] = _RopeRows(a.data_ptr(), b.data_ptr(), a.shape[1], xs, ys)
+        outs.append(b)
+    pos = _ints(positions, "positions", torch.int64, (T,))
+    with _On(x, k, positions, *outs):
+        _check(lib().oq_apply_rope(rope.handle, C.addressof(rows), len(pairs),
+                                   _ROW_DTYPES[x.dtype], T, d, pos, 1 if inverse else 0,
+                                   _stream(stream)))
+    return outs[0] if k is None else tuple(outs)
+
+
+class _KVCacheStruct(C.Structure):
+    _fields_ = [("k_codes", C.c_void_p), ("v_codes", C.c_void_p), ("k_norms", C.c_void_p),
+                ("v_norms", C.c_void_p), ("num_pages", C.c_longlong), ("page_size", C.c_int),
+                ("kv_heads", C.c_int), ("d", C.c_int), ("bits", C.c_int)]
+
+
+class KVCache:
+    """A paged cache of keys and values as codes (oq_kv_cache): *_codes uint8 [pages, kv_heads,
+    page_size, d*bits/8] and *_norms fp32 [pages, kv_heads, page_size], the caller's tensors."""
+
+    def __init__(self, k_codes, v_codes, k_norms, v_norms, bits: int):
+        if k_codes.dim() != 4 or bits not in (2, 3, 4, 6, 8):
+            _bad("codes must be [pages, kv_heads, page_size, bytes], bits 2, 3, 4, 6 or 8")
+        pages, heads, page, nb = k_codes.shape
+        if nb * 8 % bits != 0:
+            _bad(f"rows of {nb} bytes hold no whole number of {bits}-bit codes")
+        for t, what in ((k_codes, "k_codes"), (v_codes, "v_codes")):
+            _ints(t, what, torch.uint8, (pages, heads, page, nb))
+        for t, what in ((k_norms, "k_norms"), (v_norms, "v_norms")):
+            _ints(t, what, torch.float32, (pages, heads, page))
+        self.k_codes, self.v_codes, self.k_norms, self.v_norms = k_codes, v_codes, k_norms, v_norms
+        self.num_pages, self.kv_heads, self.page_size = pages, heads, page
+        self.d, self.bits = nb * 8 // bits, bits
+        self._s = _KVCacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_norms.data_ptr(),
+                                 v_norms.data_ptr(), pages, page, heads, self.d, bits)
+        _On(k_codes, v_codes, k_norms, v_norms)          # one CUDA device
+
+    @classmethod
+    def empty(cls, num_pages: int, kv_heads: int, page_size: int, d: int, bits: int, device="cuda"):
+        """A cache in new (zeroed) device memory."""
+        shape = (num_pages, kv_heads, page_size)
+        codes = [torch.zeros(*shape, d * bits // 8, dtype=torch.uint8, device=device)
+                 for _ in range(2)]
+        norms = [torch.zeros(shape, dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(*codes, *norms, bits=bits)
+
+    @property
+    def handle(self):
+        return C.addressof(self._s)
+
+
+def oq_kv_write(r: RPBH, c: Codebook, cache: KVCache, k: torch.Tensor, v: torch.Tensor,
+                slots: torch.Tensor, stream=None):
+    """Store k, v [T, kv_heads, d] (fp32, bf16 or fp16; token stride free) as codes in the slots
+    (int64 [T]; -1: skip; no other slot twice)."""
+    ks = _rows(k, "k", cache.kv_heads, cache.d)
+    vs = _rows(v, "v", cache.kv_heads, cache.d, k.dtype)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        _bad(f"k has {T} tokens, v {v.shape[0]}")
+    at = _ints(slots, "slots", torch.int64, (T,))
+    with _On(cache.k_codes, k, v, slots):
+        _check(lib().oq_kv_write(r.handle, c.handle, cache.handle, k.data_ptr(), ks, v.data_ptr(),
+                                 vs, _ROW_DTYPES[k.dtype], T, at, _stream(stream)))
+
+
+def oq_kv_read(r: RPBH, c: Codebook, cache: KVCache, slots: torch.Tensor, k=None, v=None,
+               out_dtype=torch.bfloat16, stream=None):
+    """The rows that slots (int64 [T]; -1: zeros) stand for: returns (k, v) [T, kv_heads, d]."""
+    T = slots.shape[0] if slots.dim() == 1 else -1
+    at = _ints(slots, "slots", torch.int64, (T,))
+    shape = (T, cache.kv_heads, cache.d)
+    if k is None:
+        k = torch.empty(shape, dtype=out_dtype, device=slots.device)
+    if v is None:
+        v = torch.empty(shape, dtype=k.dtype, device=slots.device)
+    ks = _rows(k, "k", cache.kv_heads, cache.d)
+    vs = _rows(v, "v", cache.kv_heads, cache.d, k.dtype)
+    if k.shape[0] != T or v.shape[0] != T:
+        _bad(f"k and v must have {T} tokens")
+    with _On(cache.k_codes, k, v, slots):
+        _check(lib().oq_kv_read(r.handle, c.handle, cache.handle, at, T, k.data_ptr(), ks,
+                                v.data_ptr(), vs, _ROW_DTYPES[k.dtype], _stream(stream)))
+    return k, v
+
+
+def oq_kv_attend(r: RPBH, c: Codebook, cache: KVCache, q: torch.Tensor, q_start: torch.Tensor,
+                 prefix: torch.Tensor, page_table: torch.Tensor, max_nodes: int = 1,
+                 tree_mask=None, scale=None, out=None, stream=None):
+    """Attention of drafted tokens over the cache: q [rows, q_heads, d] (bf16 or fp16), rows
+    q_start[b] .. q_start[b+1] - 1 of sequence b behind its prefix[b] cached tokens (q_start int32
+    [B+1], prefix int32 [B], page_table int32 [B, width]); tree_mask int64 [rows]: bit j of a
+    row's word shows it node j (None: the nodes up to its own).  scale: 1/sqrt(d) unless given.
+    Rows of out outside every sequence are left as they were.  Returns out."""
+    qs = _rows(q, "q", d=cache.d)
+    rows, heads = q.shape[0], q.shape[1]
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    os_ = _rows(out, "out", heads, cache.d, q.dtype)
+    if out.shape[0] != rows:
+        _bad(f"out has {out.shape[0]} rows, q {rows}")
+    B = prefix.shape[0] if prefix.dim() == 1 else -1
+    width = page_table.shape[1] if page_table.dim() == 2 else 0
+    start_p = _ints(q_start, "q_start", torch.int32, (B + 1,))
+    prefix_p = _ints(prefix, "prefix", torch.int32, (B,))
+    table_p = _ints(page_table, "page_table", torch.int32, (B, width))
+    mask_p = None if tree_mask is None else _ints(tree_mask, "tree_mask", torch.int64, (rows,))
+    if scale is None:
+        scale = cache.d ** -0.5
+    with _On(cache.k_codes, q, out, q_start, prefix, page_table, tree_mask):
+        _check(lib().oq_kv_attend(r.handle, c.handle, cache.handle, q.data_ptr(), qs,
+                                  out.data_ptr(), os_, _ROW_DTYPES[q.dtype], rows, heads, start_p,
+                                  prefix_p, B, max_nodes, table_p, width, mask_p, scale,
+                                  _stream(stream)))
+    return out
+
+
 def oq_check(stream=None):
     _check(lib().oq_check(_stream(stream)))
 
 
-KERNEL_NAMES = {1: "quantize", 2: "decode", 3: "gemm", 4: "fused", 5: "aux"}
+KERNEL_NAMES = {1: "quantize", 2: "decode", 3: "gemm", 4: "fused", 5: "aux", 6: "rope",
+                7: "kv_write", 8: "kv_read", 9: "kv_attend"}
 OQ_KERNEL_QUANTIZE, OQ_KERNEL_DECODE, OQ_KERNEL_GEMM, OQ_KERNEL_FUSED = 1, 2, 3, 4
 OQ_KERNEL_AUX = 5
+OQ_KERNEL_ROPE, OQ_KERNEL_KV_WRITE, OQ_KERNEL_KV_READ, OQ_KERNEL_KV_ATTEND = 6, 7, 8, 9
 
 
 def oq_debug_arm_wait_timeout(kernel: int, limit_cycles: int):

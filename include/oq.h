@@ -58,6 +58,7 @@ extern "C" {
 
 #define OQ_F32 0              /* element types for `dtype` / `out_dtype`                  */
 #define OQ_BF16 1
+#define OQ_F16 2              /* rotary positions and the cache's calls only               */
 
 typedef struct oq_rpbh oq_rpbh;
 typedef struct oq_codebook oq_codebook;
@@ -262,17 +263,124 @@ int oq_linear_noalloc(const oq_codebook *ca, const oq_codebook *cw, const uint8_
  * [1e3, 1e9]. */
 int oq_debug_arm_wait_timeout(int kernel, long long limit_cycles);
 
+/* ---- Rotary positions and the quantised key/value cache ----------------------------------
+ * The pages quantise the linear layers; these calls carry the same quantizer (rotation, norm,
+ * nearest-centroid codes, packed as above) to the attention beside them: keys get their
+ * positions, keys and values are stored as codes, and attention reads the codes.  Since R is
+ * orthogonal, q . k_hat = (R q) . (s/sqrt(d) centroid[codes]) and R^T is applied once to a
+ * finished row: the rotation cancels inside attention as it does inside the linear layer.
+ *
+ * Rows are [tokens, heads, d] with the heads of a token contiguous; a token stride (in elements,
+ * a multiple of 16 bytes) lets them be slices of a fused projection.  dtype is OQ_BF16, OQ_F16
+ * or, where a call says so, OQ_F32.  Each call is one kernel on `stream`, keeps no workspace and
+ * allocates nothing (after its handles' first use on the device), so calls on several streams
+ * and captured graphs may run at the same time. */
+typedef struct oq_rope oq_rope;
+
+#define OQ_KV_MAX_HEADS 1024  /* heads of a token                                          */
+#define OQ_KV_MAX_NODES 64    /* drafted tokens of a sequence in one oq_kv_attend call     */
+
+#define OQ_ROPE_HALF 0          /* pairs (i, i + rot_dim/2)                                */
+#define OQ_ROPE_INTERLEAVED 1   /* pairs (2i, 2i + 1)                                      */
+#define OQ_ROPE_PLAIN 0         /* freq_i = theta^(-2i/rot_dim)                            */
+#define OQ_ROPE_LINEAR 1        /* freq_i / factor                                         */
+#define OQ_ROPE_NTK 2           /* theta * factor^(rot_dim/(rot_dim - 2)) in theta's place */
+#define OQ_ROPE_YARN 3          /* freq_i for pairs that turn 32 times and more in original_len
+                                 * positions, freq_i / factor for those that turn once or less, a
+                                 * ramp between the two pairs (rounded outwards) in between;
+                                 * amplitude 1 + ln(factor) / 10                           */
+
+/* Build the rotary positions of the first rot_dim elements of a head (16 <= rot_dim <= 512, a
+ * multiple of 16).  factor >= 1 is read by the scaled forms, original_len >= 1 by OQ_ROPE_YARN.
+ * Host-only.  Errors: OQ_EINVAL. */
+int oq_build_rope(int rot_dim, int layout, double theta, int scaling, double factor,
+                  int original_len, oq_rope **out);
+/* Copy freq[rot_dim/2] (radians a position) and the amplitude; either may be NULL.  Host-only. */
+int oq_rope_values(const oq_rope *r, double *freq, double *amplitude);
+void oq_free_rope(oq_rope *r);
+
+/* One tensor of oq_apply_rope: x and y [T, heads, d], token strides in elements; y = x (with the
+ * same stride) works in place, any other overlap is not allowed. */
+typedef struct {
+    const void *x;
+    void *y;
+    int heads;
+    long long x_stride, y_stride;
+} oq_rope_rows;
+
+/* Pair (a, b) of every head of token t becomes m (a cos - b sin, a sin + b cos), m the amplitude
+ * and the angle positions[t] * freq_i, reduced in fp64; elements from rot_dim on are copied.
+ * One or two tensors (queries, keys) of the same tokens.  inverse != 0 applies the transpose
+ * (-sin for sin): the gradient of x from the gradient of y.  positions: device, int64 [T], any
+ * sign.  dtype OQ_F32, OQ_BF16 or OQ_F16; the products are fp32, rounded once.  d: a multiple of
+ * 16, rot_dim <= d <= 1024.  T = 0 is a no-op.  Errors: OQ_EINVAL, OQ_EUNSUPPORTED, OQ_ECUDA. */
+int oq_apply_rope(const oq_rope *r, const oq_rope_rows *rows, int num_rows, int dtype, int T, int d,
+                  const int64_t *positions, int inverse, void *stream);
+
+/* A paged cache of keys and values: the caller's device arrays, 16-byte aligned.  Row (page, head,
+ * offset) of *_codes [num_pages, kv_heads, page_size, d*bits/8] has a head's packed codes, the
+ * same row of *_norms [num_pages, kv_heads, page_size] its norm.  A token lives in one slot =
+ * page * page_size + offset for all heads.  d is 128 or 256; page_size a power of two in
+ * [16, 1024]; bits as in a codebook. */
+typedef struct {
+    uint8_t *k_codes, *v_codes;
+    float *k_norms, *v_norms;
+    long long num_pages;
+    int page_size, kv_heads, d, bits;
+} oq_kv_cache;
+
+/* Store T tokens' keys and values: z = R x, norm = ||z||, codes = nearest centroids of z / (norm +
+ * 1e-8), for every head's row, as oq_quantize_act does for a row of dimension d.  k, v: device,
+ * [T, kv_heads, d] of dtype (OQ_F32, OQ_BF16, OQ_F16).  slots: device, int64 [T]; -1 skips the
+ * token (padding); the others must differ from one another (a slot named twice ends up with
+ * either token's rows or a mixture of them; no other slot is touched).  A slot outside the cache
+ * is skipped and reported by oq_check.  A row with a NaN or infinity, or whose squares pass fp32,
+ * gets that norm.  T = 0 is a no-op.
+ * Errors: OQ_EINVAL, OQ_EUNSUPPORTED, OQ_ECUDA. */
+int oq_kv_write(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache, const void *k,
+                long long k_stride, const void *v, long long v_stride, int dtype, int T,
+                const int64_t *slots, void *stream);
+
+/* The rows that T slots stand for: x_hat = norm / sqrt(d) R^T centroid[codes], k and v [T,
+ * kv_heads, d] of dtype.  slots may repeat; -1 gives rows of zeros, and so does a slot outside the
+ * cache (reported by oq_check).  T = 0 is a no-op.  Errors: as oq_kv_write. */
+int oq_kv_read(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache,
+               const int64_t *slots, int T, void *k, long long k_stride, void *v,
+               long long v_stride, int dtype, void *stream);
+
+/* Attention of each sequence's drafted tokens over the cache.  Sequence b has rows q_start[b] ..
+ * q_start[b+1] - 1 of q and out (its nodes, at most max_nodes <= OQ_KV_MAX_NODES; none is
+ * allowed), prefix[b] cached tokens before them, and the nodes' own keys and values cached behind
+ * those: token t of the sequence lies in page page_table[b][t / page_size].  Node i sees the whole
+ * prefix and the nodes j with bit j of tree_mask[row] set (its ancestors and itself, in any
+ * order); with tree_mask = NULL the nodes up to its own, so one node a sequence is a plain
+ * decoding step.  out = sum_t p_t v_hat_t, p the softmax of scale * q . k_hat_t over the tokens it
+ * sees; a row that sees nothing gives zeros.  Query head i reads key head i / (q_heads/kv_heads).
+ * q, out: device, [q_rows, q_heads, d] of dtype (OQ_BF16 or OQ_F16).  q_start: int32 [B+1];
+ * prefix: int32 [B]; page_table: int32 [B, table_width] (entries past a sequence's last page are
+ * not read); tree_mask: int64 [q_rows] or NULL; all device.  Rows of out outside every sequence
+ * are left as they were.  What is not visible is never multiplied: masked tokens may hold
+ * anything.  A sequence whose rows or lengths do not fit (q_start decreasing, past q_rows or over
+ * max_nodes; prefix negative or past the table) is skipped, a token whose page is outside the
+ * cache is not seen, and oq_check reports both.
+ * Errors: as oq_kv_write. */
+int oq_kv_attend(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache, const void *q,
+                 long long q_stride, void *out, long long out_stride, int dtype, int q_rows,
+                 int q_heads, const int32_t *q_start, const int32_t *prefix, int B, int max_nodes,
+                 const int32_t *page_table, int table_width, const int64_t *tree_mask,
+                 double scale, void *stream);
+
 /* Synchronise `stream`, then read and clear the library's device error word.
- * Returns OQ_OK, OQ_EDEVICE (a kernel gave up a bounded wait or saw an internal
- * inconsistency; oq_last_error() says which), or OQ_ECUDA. */
+ * Returns OQ_OK, OQ_EDEVICE (a kernel gave up a bounded wait, or skipped device-side indices
+ * that do not fit; oq_last_error() says which), or OQ_ECUDA. */
 int oq_check(void *stream);
 
 void oq_free_rpbh(oq_rpbh *r);
 void oq_free_codebook(oq_codebook *cb);
 
 /* Per-kernel timing, for profilers and benchmarks (the pages have no counterpart; it only
- * observes the path).  While enabled on the calling thread, every kernel that oq_quantize_*
- * and oq_linear launch is bracketed by two CUDA events recorded on the caller's stream.
+ * observes the path).  While enabled on the calling thread, every kernel that oq_quantize_*,
+ * oq_linear, oq_apply_rope and oq_kv_* launch is bracketed by two CUDA events recorded on the caller's stream.
  * oq_timing_collect() waits for those events, writes up to `capacity` records in launch
  * order (kernel id, milliseconds) and forgets all pending records; *count receives the number
  * written.  Records belong to the device that was current at launch. */
@@ -281,6 +389,10 @@ void oq_free_codebook(oq_codebook *cb);
 #define OQ_KERNEL_GEMM 3       /* tcgen05 codebook GEMM of oq_linear */
 #define OQ_KERNEL_FUSED 4      /* quantize stage and GEMM in one kernel (OQ_FUSED_STEP=1) */
 #define OQ_KERNEL_AUX 5        /* auxiliary launch: the fused step's counter reset */
+#define OQ_KERNEL_ROPE 6       /* oq_apply_rope */
+#define OQ_KERNEL_KV_WRITE 7   /* oq_kv_write */
+#define OQ_KERNEL_KV_READ 8    /* oq_kv_read */
+#define OQ_KERNEL_KV_ATTEND 9  /* oq_kv_attend */
 typedef struct {
     int kernel;
     float ms;
