@@ -6,6 +6,26 @@
 
 namespace oq {
 
+// A kernel's set-up, made once on each device (function attributes belong to a device).
+struct PerDevice {
+    std::mutex mu;
+    bool done[kMaxDevices] = {};
+    template <class F> cudaError_t once(F &&f) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess)
+            return e;
+        if (dev < 0 || dev >= kMaxDevices)
+            return cudaErrorInvalidDevice;
+        std::lock_guard<std::mutex> lk(mu);
+        if (done[dev])
+            return cudaSuccess;
+        e = f();
+        done[dev] = e == cudaSuccess;
+        return e;
+    }
+};
+
 // Rotary positions of up to two tensors (queries and keys) of the same tokens.
 struct RopeParams {
     const void *x[2];
@@ -72,11 +92,18 @@ struct KvAttendParams {
     const long long *mask;        // [q_rows] or null
     int B, table_width, max_nodes;
     const uint16_t *ent;
-    const float *cent;
+    const uint32_t *lut;          // fp16 decode table (oq_cache.cpp, build_kv_lut)
     int h;
-    float qk_scale;               // scale * log2(e) / (sqrt(d) sqrt(h))
-    float o_scale;                // 1 / (sqrt(d) sqrt(h))
+    float qk_scale;               // scale * log2(e) / (sqrt(d h) alpha)
+    float o_scale;                // 1 / (sqrt(d h) alpha)
+    unsigned *err;                // device error word (set by launch_kv_attend)
 };
+// The kernels of one bit width; `splits` CTAs (a cluster) share a row tile's tokens.
+cudaError_t launch_kv_attend_b2(const KvAttendParams &p, int dtype, int splits, cudaStream_t st);
+cudaError_t launch_kv_attend_b3(const KvAttendParams &p, int dtype, int splits, cudaStream_t st);
+cudaError_t launch_kv_attend_b4(const KvAttendParams &p, int dtype, int splits, cudaStream_t st);
+cudaError_t launch_kv_attend_b6(const KvAttendParams &p, int dtype, int splits, cudaStream_t st);
+cudaError_t launch_kv_attend_b8(const KvAttendParams &p, int dtype, int splits, cudaStream_t st);
 cudaError_t launch_kv_attend(const KvAttendParams &p, int dtype, cudaStream_t st, int num_sms,
                              std::string *why);
 

@@ -92,6 +92,63 @@ int upload_ent(oq_rpbh *r, int dev) {
 
 }  // namespace
 
+namespace oq {
+namespace host {
+
+// The fp16 decode table of the cache's kernels: 32-bit words of two centroids.
+//   bits 2: entry e (a byte, four codes) = two words; bits 3, 4: entry e (two codes) = one word,
+//   the lower code in the low half; bits 6, 8: entry e (one code) in both halves.
+// The centroids are multiplied by kv_alpha in [1, 2) before they are rounded to fp16, and the
+// kernels divide by it in fp32: of 4096 factors the one whose rounded centroids are nearest (cells
+// weighted by the mass that the quantizer gives them).  At 4 bits that takes the rounding from
+// 2.8e-4 of a centroid (rms) to about 0.5e-4, at 2 and 3 bits to below 1e-5.
+void build_kv_lut(oq_codebook *cb) {
+    const int L = 1 << cb->bits;
+    auto value = [](uint16_t h) {
+        const int e = (h >> 10) & 31;
+        const double m = std::ldexp(1024.0 + (h & 1023), e - 25);
+        return (h & 0x8000) ? -m : m;
+    };
+    std::vector<double> mass(L);
+    for (int i = 0; i < L; ++i) {                 // N(0, 1) density times the cell's width
+        const double lo = i ? cb->t[i - 1] : cb->c[0] - (cb->t[0] - cb->c[0]);
+        const double hi = i + 1 < L ? cb->t[i] : 2.0 * cb->c[L - 1] - cb->t[L - 2];
+        mass[i] = std::exp(-0.5 * cb->c[i] * cb->c[i]) * (hi - lo);
+    }
+    double best = -1.0;
+    for (int k = 0; k < 4096; ++k) {
+        const double a = 1.0 + k / 4096.0;
+        double err = 0.0;
+        for (int i = L / 2; i < L; ++i) {
+            const double d = value(to_half_bits(a * cb->c[i])) / a - cb->c[i];
+            err += mass[i] * d * d;
+        }
+        if (best < 0.0 || err < best) {
+            best = err;
+            cb->kv_alpha = a;
+        }
+    }
+    uint16_t lut[256];
+    for (int i = 0; i < L; ++i)
+        lut[i] = to_half_bits(cb->kv_alpha * cb->c[i]);
+    cb->kv_lut.clear();
+    const int b = cb->bits;
+    const int entries = b == 6 || b == 3 ? 64 : 256;
+    for (int e = 0; e < entries; ++e) {
+        if (b == 2)
+            for (int k = 0; k < 2; ++k)
+                cb->kv_lut.push_back(lut[(e >> (4 * k)) & 3] |
+                                     (uint32_t)lut[(e >> (4 * k + 2)) & 3] << 16);
+        else if (b <= 4)
+            cb->kv_lut.push_back(lut[e & (L - 1)] | (uint32_t)lut[e >> b] << 16);
+        else
+            cb->kv_lut.push_back(lut[e] | (uint32_t)lut[e] << 16);
+    }
+}
+
+}  // namespace host
+}  // namespace oq
+
 extern "C" {
 
 int oq_build_rope(int rot_dim, int layout, double theta, int scaling, double factor,
@@ -375,7 +432,7 @@ int oq_kv_attend(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cach
     oq_rpbh *rw = const_cast<oq_rpbh *>(r);
     oq_codebook *cw = const_cast<oq_codebook *>(c);
     if ((rc = upload_ent(rw, dev)) != OQ_OK ||
-        (rc = upload(cw->mu, &cw->dev_cent32[dev], cw->cent32, "upload centroids")) != OQ_OK)
+        (rc = upload(cw->mu, &cw->dev_kv_lut[dev], cw->kv_lut, "upload decode table")) != OQ_OK)
         return rc;
     p.q = q;
     p.out = out;
@@ -392,9 +449,9 @@ int oq_kv_attend(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cach
     p.table_width = table_width;
     p.max_nodes = max_nodes;
     p.ent = reinterpret_cast<const uint16_t *>(rw->dev_ent16[dev]);
-    p.cent = reinterpret_cast<const float *>(cw->dev_cent32[dev]);
+    p.lut = cw->dev_kv_lut[dev];
     p.h = r->h;
-    const double unit = 1.0 / std::sqrt((double)r->d * r->h);
+    const double unit = 1.0 / (std::sqrt((double)r->d * r->h) * c->kv_alpha);
     p.qk_scale = (float)(scale * 1.4426950408889634 * unit);
     p.o_scale = (float)unit;
     cudaStream_t st = (cudaStream_t)stream;

@@ -288,7 +288,12 @@ bool solve_lloyd_max(const Marginal &f, int L, std::vector<double> &c) {
     return rmax < 1e-12;
 }
 
-// IEEE binary16, round to nearest even (normal range and zero; centroids are in [1e-3, 5]).
+}  // namespace
+
+namespace oq {
+namespace host {
+
+// IEEE binary16, round to nearest even (normal range and zero; centroids are in [1e-3, 10]).
 uint16_t to_half_bits(double x) {
     uint16_t sgn = std::signbit(x) ? 0x8000 : 0;
     x = std::fabs(x);
@@ -314,7 +319,8 @@ uint16_t to_half_bits(double x) {
     return (uint16_t)(sgn | (E << 10) | f);
 }
 
-}  // namespace
+}  // namespace host
+}  // namespace oq
 
 namespace {
 
@@ -1026,6 +1032,7 @@ int oq_lloyd_max_marginal(int d, int bits, int marginal, oq_codebook **out) {
         cb->lut[i] = to_half_bits(cb->c[i]);
         cb->cent32[i] = (float)cb->c[i];
     }
+    build_kv_lut(cb);
     if (!build_grid(cb)) {
         delete cb;
         return fail(OQ_EINVAL, "%s: could not build the quantizer grid", who);
@@ -1512,6 +1519,10 @@ void oq_free_codebook(oq_codebook *cb) {
         if (cb->dev_cent32[dev]) {
             cudaSetDevice(dev);
             cudaFree(cb->dev_cent32[dev]);
+        }
+        if (cb->dev_kv_lut[dev]) {
+            cudaSetDevice(dev);
+            cudaFree(cb->dev_kv_lut[dev]);
         }
     }
     if (cur >= 0)
