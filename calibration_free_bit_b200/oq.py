@@ -106,6 +106,8 @@ def _check(rc: int):
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if torch.cuda.is_initialized():      # the current stream's handle, without its wrapper
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         if torch.cuda.is_available():
             return torch.cuda.current_stream().cuda_stream
         return None
@@ -308,39 +310,42 @@ def _rows(t: torch.Tensor, what: str, heads=None, d=None, dtype=None):
     if dtype is not None and t.dtype != dtype:
         _bad(f"{what} has dtype {t.dtype}: expected {dtype}")
     n, h, e = t.shape
-    if (e > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != e):
+    sn, sh, se = t.stride()
+    if (e > 1 and se != 1) or (h > 1 and sh != e):
         _bad(f"{what}: the heads of a token must be contiguous")
-    return t.stride(0) if n > 1 else h * e
+    return sn if n > 1 else h * e
 
 
 def _ints(t: torch.Tensor, what: str, dtype, shape):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         _bad(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
              f"{tuple(t.shape)}")
     return t.data_ptr()
 
 
-class _On:
-    """The device all of a call's tensors are on, made current for the call if it is not."""
+def _device(*tensors) -> int:
+    """The index of the CUDA device that all of a call's tensors are on."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            _bad(f"tensors on {tensors[0].device} and {t.device}: all must be on one device")
+    if dev < 0:
+        _bad("tensors on the CPU: a CUDA device is needed")
+    return dev
 
-    def __init__(self, *tensors):
-        dev = tensors[0].device
-        for t in tensors:
-            if t is not None and t.device != dev:
-                _bad(f"tensors on {dev} and {t.device}: all must be on one device")
-        if dev.type != "cuda":
-            _bad(f"tensors on {dev}: a CUDA device is needed")
-        self._dev = dev.index
-        self._guard = None
 
-    def __enter__(self):
-        if self._dev != torch.cuda.current_device():
-            self._guard = torch.cuda.device(self._dev)
-            self._guard.__enter__()
+def _run(dev: int, fn, args, stream):
+    """fn(*args, stream) with the tensors' device current."""
+    if dev == torch._C._cuda_getDevice():
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)))
 
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+
+def _like(t: torch.Tensor) -> torch.Tensor:
+    return (torch.empty_like(t) if t.is_contiguous() else
+            torch.empty(t.shape, dtype=t.dtype, device=t.device))
 
 
 class Rope:
@@ -397,17 +402,16 @@ def oq_apply_rope(rope: Rope, x: torch.Tensor, positions: torch.Tensor, k=None, 
         if a.shape[0] != T:
             _bad(f"{what} has {a.shape[0]} tokens, x {T}")
         if b is None:
-            b = torch.empty(a.shape, dtype=a.dtype, device=a.device)
+            b = _like(a)
         ys = _rows(b, f"the output of {what}", a.shape[1], d, x.dtype)
         if b.shape[0] != T:
             _bad(f"the output of {what} has {b.shape[0]} tokens, x {T}")
         rows[i] = _RopeRows(a.data_ptr(), b.data_ptr(), a.shape[1], xs, ys)
         outs.append(b)
     pos = _ints(positions, "positions", torch.int64, (T,))
-    with _On(x, k, positions, *outs):
-        _check(lib().oq_apply_rope(rope.handle, C.addressof(rows), len(pairs),
-                                   _ROW_DTYPES[x.dtype], T, d, pos, 1 if inverse else 0,
-                                   _stream(stream)))
+    _run(_device(x, k, positions, *outs), lib().oq_apply_rope,
+         (rope.handle, C.addressof(rows), len(pairs), _ROW_DTYPES[x.dtype], T, d, pos,
+          1 if inverse else 0), stream)
     return outs[0] if k is None else tuple(outs)
 
 
@@ -436,7 +440,8 @@ class KVCache:
         self.d, self.bits = nb * 8 // bits, bits
         self._s = _KVCacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_norms.data_ptr(),
                                  v_norms.data_ptr(), pages, page, heads, self.d, bits)
-        _On(k_codes, v_codes, k_norms, v_norms)          # one CUDA device
+        self._at = C.addressof(self._s)
+        self._dev = _device(k_codes, v_codes, k_norms, v_norms)
 
     @classmethod
     def empty(cls, num_pages: int, kv_heads: int, page_size: int, d: int, bits: int, device="cuda"):
@@ -449,7 +454,7 @@ class KVCache:
 
     @property
     def handle(self):
-        return C.addressof(self._s)
+        return self._at
 
 
 def oq_kv_write(r: RPBH, c: Codebook, cache: KVCache, k: torch.Tensor, v: torch.Tensor,
@@ -462,9 +467,9 @@ def oq_kv_write(r: RPBH, c: Codebook, cache: KVCache, k: torch.Tensor, v: torch.
     if v.shape[0] != T:
         _bad(f"k has {T} tokens, v {v.shape[0]}")
     at = _ints(slots, "slots", torch.int64, (T,))
-    with _On(cache.k_codes, k, v, slots):
-        _check(lib().oq_kv_write(r.handle, c.handle, cache.handle, k.data_ptr(), ks, v.data_ptr(),
-                                 vs, _ROW_DTYPES[k.dtype], T, at, _stream(stream)))
+    _run(_device(cache.k_codes, k, v, slots), lib().oq_kv_write,
+         (r.handle, c.handle, cache.handle, k.data_ptr(), ks, v.data_ptr(), vs,
+          _ROW_DTYPES[k.dtype], T, at), stream)
 
 
 def oq_kv_read(r: RPBH, c: Codebook, cache: KVCache, slots: torch.Tensor, k=None, v=None,
@@ -481,9 +486,9 @@ def oq_kv_read(r: RPBH, c: Codebook, cache: KVCache, slots: torch.Tensor, k=None
     vs = _rows(v, "v", cache.kv_heads, cache.d, k.dtype)
     if k.shape[0] != T or v.shape[0] != T:
         _bad(f"k and v must have {T} tokens")
-    with _On(cache.k_codes, k, v, slots):
-        _check(lib().oq_kv_read(r.handle, c.handle, cache.handle, at, T, k.data_ptr(), ks,
-                                v.data_ptr(), vs, _ROW_DTYPES[k.dtype], _stream(stream)))
+    _run(_device(cache.k_codes, k, v, slots), lib().oq_kv_read,
+         (r.handle, c.handle, cache.handle, at, T, k.data_ptr(), ks, v.data_ptr(), vs,
+          _ROW_DTYPES[k.dtype]), stream)
     return k, v
 
 
@@ -498,7 +503,7 @@ def oq_kv_attend(r: RPBH, c: Codebook, cache: KVCache, q: torch.Tensor, q_start:
     qs = _rows(q, "q", d=cache.d)
     rows, heads = q.shape[0], q.shape[1]
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _like(q)
     os_ = _rows(out, "out", heads, cache.d, q.dtype)
     if out.shape[0] != rows:
         _bad(f"out has {out.shape[0]} rows, q {rows}")
@@ -510,11 +515,11 @@ def oq_kv_attend(r: RPBH, c: Codebook, cache: KVCache, q: torch.Tensor, q_start:
     mask_p = None if tree_mask is None else _ints(tree_mask, "tree_mask", torch.int64, (rows,))
     if scale is None:
         scale = cache.d ** -0.5
-    with _On(cache.k_codes, q, out, q_start, prefix, page_table, tree_mask):
-        _check(lib().oq_kv_attend(r.handle, c.handle, cache.handle, q.data_ptr(), qs,
-                                  out.data_ptr(), os_, _ROW_DTYPES[q.dtype], rows, heads, start_p,
-                                  prefix_p, B, max_nodes, table_p, width, mask_p, scale,
-                                  _stream(stream)))
+    _run(_device(cache.k_codes, q, out, q_start, prefix, page_table, tree_mask),
+         lib().oq_kv_attend,
+         (r.handle, c.handle, cache.handle, q.data_ptr(), qs, out.data_ptr(), os_,
+          _ROW_DTYPES[q.dtype], rows, heads, start_p, prefix_p, B, max_nodes, table_p, width,
+          mask_p, scale), stream)
     return out
 
 
