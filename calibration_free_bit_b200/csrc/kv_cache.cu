@@ -8,6 +8,7 @@
 #include "k1_ops.cuh"
 #include "kv_internal.h"
 #include "kv_ops.cuh"
+#include "kv_rows.cuh"
 
 namespace oq {
 namespace {
@@ -16,11 +17,6 @@ using namespace kvops;
 using k1ops::fma_sat;
 
 __device__ unsigned int g_kv_err;
-
-enum : unsigned {
-    KV_ERR_SLOT = 1u << 0,      // a slot outside the cache
-    KV_ERR_WAIT = 1u << 1,      // a bounded wait gave up
-};
 
 constexpr int kWarps = 4;
 
@@ -37,15 +33,6 @@ __device__ __forceinline__ Row row_of(long long r, int heads) {
     o.w = (int)(r & 1);
     o.tok = r >> 1;
     return o;
-}
-
-// Row `slot` of one head in the cache: its index in norms (times row_bytes: in codes).
-__device__ __forceinline__ long long cache_row(const KvView &c, long long slot, int head) {
-    const long long page = slot >> c.page_log2;
-    return ((page * c.kv_heads + head) << c.page_log2) + (slot & ((1 << c.page_log2) - 1));
-}
-__device__ __forceinline__ bool slot_ok(const KvView &c, long long slot) {
-    return slot >= 0 && slot < (c.pages << c.page_log2);
 }
 
 template <class E, int D>
@@ -67,7 +54,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv_write_rows(const KvWriteParams
         const long long slot = p.slots[o.tok];
         if (!slot_ok(p.c, slot)) {
             if (slot != -1 && lane == 0)
-                atomicOr(&g_kv_err, KV_ERR_SLOT);
+                atomicOr(p.err, KV_ERR_SLOT);
             continue;
         }
         const E *x = static_cast<const E *>(p.x[o.w]) + o.tok * p.x_stride[o.w] + o.head * D;
@@ -136,7 +123,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv_read_rows(const KvReadParams p
         E *y = static_cast<E *>(p.y[o.w]) + o.tok * p.y_stride[o.w] + o.head * D;
         if (!slot_ok(p.c, slot)) {
             if (slot != -1 && lane == 0)
-                atomicOr(&g_kv_err, KV_ERR_SLOT);
+                atomicOr(p.err, KV_ERR_SLOT);
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 y[i * 32 + lane] = from_f32<E>(0.f);
@@ -184,21 +171,54 @@ cudaError_t read_rows(const KvReadParams &p, cudaStream_t st, int num_sms) {
 
 }  // namespace
 
-cudaError_t launch_kv_write(const KvWriteParams &p, int dtype, cudaStream_t st, int num_sms,
+namespace {
+
+cudaError_t error_word(unsigned **out) {
+    static PerDevice known;
+    static void *word[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = known.once([&] { return cudaGetSymbolAddress(&word[dev], g_kv_err); });
+    if (e == cudaSuccess)
+        *out = static_cast<unsigned *>(word[dev]);
+    return e;
+}
+
+// Rows (keys and values) from which the tensor cores' form is taken.
+constexpr long long kTensorRows = 512;
+
+}  // namespace
+
+cudaError_t launch_kv_write(const KvWriteParams &params, int dtype, cudaStream_t st, int num_sms,
                             std::string *why) {
     *why = "oq_kv_write: launch";
+    KvWriteParams p = params;
+    const cudaError_t e = error_word(&p.err);
+    if (e != cudaSuccess)
+        return e;
     if (dtype == OQ_F32)
         return write_rows<float>(p, st, num_sms);
+    if (2ll * p.T * p.c.kv_heads >= kTensorRows)
+        return launch_kv_write_tc(p, p.r_img, p.tbl_words, dtype == OQ_BF16, st, num_sms);
     if (dtype == OQ_BF16)
         return write_rows<__nv_bfloat16>(p, st, num_sms);
     return write_rows<__half>(p, st, num_sms);
 }
 
-cudaError_t launch_kv_read(const KvReadParams &p, int dtype, cudaStream_t st, int num_sms,
+cudaError_t launch_kv_read(const KvReadParams &params, int dtype, cudaStream_t st, int num_sms,
                            std::string *why) {
     *why = "oq_kv_read: launch";
+    KvReadParams p = params;
+    const cudaError_t e = error_word(&p.err);
+    if (e != cudaSuccess)
+        return e;
     if (dtype == OQ_F32)
         return read_rows<float>(p, st, num_sms);
+    if (2ll * p.T * p.c.kv_heads >= kTensorRows) {
+        p.scale *= p.alpha_inv;
+        return launch_kv_read_tc(p, p.r_img, dtype == OQ_BF16, st, num_sms);
+    }
     if (dtype == OQ_BF16)
         return read_rows<__nv_bfloat16>(p, st, num_sms);
     return read_rows<__half>(p, st, num_sms);

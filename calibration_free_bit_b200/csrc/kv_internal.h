@@ -59,7 +59,10 @@ struct KvWriteParams {
     int T, h;
     const uint16_t *ent;          // [d] perm | sign bit << 15
     const uint32_t *tbl;          // quantizer grid words (each `tbl_copies` times)
-    int tbl_copies;
+    int tbl_copies, tbl_words;
+    const void *r_img;            // R' as the tensor cores' operand in x's type (16-bit x)
+    int wide;                     // code rows keep 32-byte stores aligned
+    unsigned *err;                // device error word (set by launch_kv_write)
     float eps, K;                 // as K1Params
     int G, F;
 };
@@ -73,9 +76,18 @@ struct KvReadParams {
     const long long *slots;
     int T, h;
     const uint16_t *ent;
-    const float *cent;            // fp32 unit centroids
+    const float *cent;            // fp32 unit centroids (rows kernel)
     float scale;                  // 1 / sqrt(d h): norms times this, on the unnormalised transform
+    const void *r_img;            // R'^T as the tensor cores' fp16 operand (16-bit y)
+    const uint32_t *lut;          // fp16 decode table (tensor cores)
+    float alpha_inv;              // what its centroids are multiplied by, inverted
+    unsigned *err;                // device error word (set by launch_kv_read)
 };
+// The tensor-core forms (kv_tc.cu); p.scale of the read includes alpha_inv.
+cudaError_t launch_kv_write_tc(const KvWriteParams &p, const void *r_img, int tbl_words, bool bf16,
+                               cudaStream_t st, int num_sms);
+cudaError_t launch_kv_read_tc(const KvReadParams &p, const void *r_img, bool bf16, cudaStream_t st,
+                              int num_sms);
 cudaError_t launch_kv_read(const KvReadParams &p, int dtype, cudaStream_t st, int num_sms,
                            std::string *why);
 

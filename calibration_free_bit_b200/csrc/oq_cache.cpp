@@ -86,6 +86,36 @@ int check_slots(const char *who, const int64_t *slots) {
     return OQ_OK;
 }
 
+enum { RMAT_BF16 = 0, RMAT_F16 = 1, RMAT_F16_T = 2 };
+
+// sqrt(h) R (entries +-1 and 0) on the current device, as the K-major, 128-byte-swizzled operand
+// that kv_tc.cu copies into shared memory: row n has elements k = 0 .. d-1 in 64-wide atoms of d
+// rows of 128 bytes, 16-byte chunk c of a row at chunk c ^ (n % 8).  R[i][perm[j]] = sign[j]
+// (-1)^popcount(i & j) for i, j in one block.
+int rotation_matrix(oq_rpbh *r, int which, int dev, const void **out) {
+    {
+        std::lock_guard<std::mutex> lk(r->mu);
+        if (r->rmat[which].empty()) {
+            const int d = r->d, h = r->h;
+            const uint16_t one = which == RMAT_BF16 ? 0x3F80 : 0x3C00;
+            std::vector<uint16_t> m((size_t)d * d, 0);
+            for (int i = 0; i < d; ++i)
+                for (int j = i / h * h; j < i / h * h + h; ++j) {
+                    const bool neg = (__builtin_popcount(i & j & (h - 1)) & 1) ^ (r->sign[j] < 0);
+                    const int n = which == RMAT_F16_T ? r->perm[j] : i;
+                    const int k = which == RMAT_F16_T ? i : r->perm[j];
+                    const size_t at = (size_t)(k >> 6) * d * 64 + (size_t)n * 64 +
+                                      ((((k >> 3) & 7) ^ (n & 7)) << 3) + (k & 7);
+                    m[at] = (uint16_t)(one | (neg ? 0x8000 : 0));
+                }
+            r->rmat[which] = std::move(m);
+        }
+    }
+    const int rc = upload(r->mu, &r->dev_rmat[which][dev], r->rmat[which], "upload rotation matrix");
+    *out = r->dev_rmat[which][dev];
+    return rc;
+}
+
 int upload_ent(oq_rpbh *r, int dev) {
     return upload(r->mu, &r->dev_ent16[dev], r->ent16, "upload rotation entries");
 }
@@ -318,6 +348,9 @@ int oq_kv_write(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache
     if ((rc = upload_ent(rw, dev)) != OQ_OK ||
         (rc = upload(cw->mu, &cw->dev_tbl[dev], cw->tbl_img, "upload quantizer table")) != OQ_OK)
         return rc;
+    if (dtype != OQ_F32 &&
+        (rc = rotation_matrix(rw, dtype == OQ_BF16 ? RMAT_BF16 : RMAT_F16, dev, &p.r_img)) != OQ_OK)
+        return rc;
     p.x[0] = k;
     p.x[1] = v;
     p.x_stride[0] = k_stride;
@@ -328,6 +361,10 @@ int oq_kv_write(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache
     p.ent = reinterpret_cast<const uint16_t *>(rw->dev_ent16[dev]);
     p.tbl = cw->dev_tbl[dev];
     p.tbl_copies = c->bits <= 4 ? 32 : 1;
+    p.tbl_words = (int)cw->tbl_img.size();
+    p.wide = p.c.row_bytes % 32 == 0 &&
+             ((reinterpret_cast<uintptr_t>(cache->k_codes) |
+               reinterpret_cast<uintptr_t>(cache->v_codes)) & 31u) == 0;
     p.eps = 1e-8f;
     p.K = (float)(std::sqrt((double)r->d / r->h) / (c->G * c->delta));
     p.G = c->G;
@@ -368,6 +405,12 @@ int oq_kv_read(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache,
     if ((rc = upload_ent(rw, dev)) != OQ_OK ||
         (rc = upload(cw->mu, &cw->dev_cent32[dev], cw->cent32, "upload centroids")) != OQ_OK)
         return rc;
+    if (dtype != OQ_F32 &&
+        ((rc = rotation_matrix(rw, RMAT_F16_T, dev, &p.r_img)) != OQ_OK ||
+         (rc = upload(cw->mu, &cw->dev_kv_lut[dev], cw->kv_lut, "upload decode table")) != OQ_OK))
+        return rc;
+    p.lut = cw->dev_kv_lut[dev];
+    p.alpha_inv = (float)(1.0 / c->kv_alpha);
     p.y[0] = k;
     p.y[1] = v;
     p.y_stride[0] = k_stride;

@@ -22,6 +22,10 @@ struct oq_rpbh {
     std::mutex mu;
     uint32_t *dev_ent[2][oq::kMaxDevices] = {};
     uint32_t *dev_ent16[oq::kMaxDevices] = {};
+    // d <= 256: the rotation times sqrt(h) as a dense operand of the tensor cores (oq_cache.cpp,
+    // rotation_matrix): [0] bf16, [1] fp16, [2] fp16 transposed
+    std::vector<uint16_t> rmat[3];
+    uint32_t *dev_rmat[3][oq::kMaxDevices] = {};
 };
 
 struct oq_codebook {

@@ -1496,6 +1496,11 @@ void oq_free_rpbh(oq_rpbh *r) {
             cudaSetDevice(dev);
             cudaFree(r->dev_ent16[dev]);
         }
+        for (int f = 0; f < 3; ++f)
+            if (r->dev_rmat[f][dev]) {
+                cudaSetDevice(dev);
+                cudaFree(r->dev_rmat[f][dev]);
+            }
     }
     if (cur >= 0)
         cudaSetDevice(cur);

@@ -160,7 +160,11 @@ def check_codes(got, rows, R, bits, norms):
     (33, 3, 128, 128, 4, 16, F32),
     (12, 2, 256, 32, 8, 16, F32),
     (1000, 8, 128, 128, 4, 64, BF16),
-])
+] + [(T, H, d, h, bits, 16, dtype)                    # enough rows for the tensor cores' form
+     for bits in (2, 3, 4, 6, 8)
+     for T, H, d, h, dtype in ((257, 1, 128, 128, BF16), (131, 3, 128, 16, F16),
+                               (2600, 9, 128, 64, BF16), (256, 1, 256, 256, F16),
+                               (701, 5, 256, 32, BF16))])
 def test_write_and_read_match_fp64(oq, T, H, d, h, bits, page, dtype):
     pages = -(-T // page) + 2
     r, c = oq.oq_build_rpbh(d, h, 0), oq.oq_lloyd_max(d, bits)
@@ -214,10 +218,12 @@ def test_codes_are_those_of_the_activation_quantizer(oq):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-def test_padding_bad_slots_and_special_rows(oq, dtype):
-    T, H, d, page = 21, 2, 128, 16
+@pytest.mark.parametrize("T,d", [(21, 128), (300, 128), (270, 256)])
+def test_padding_bad_slots_and_special_rows(oq, dtype, T, d):
+    H, page = 2, 16
+    pages = -(-T // page)
     r, c = oq.oq_build_rpbh(d, 128, 0), oq.oq_lloyd_max(d, 4)
-    cache = oq.KVCache.empty(2, H, page, d, 4)
+    cache = oq.KVCache.empty(pages, H, page, d, 4)
     x = make_rows(T, H, d, dtype, 9)
     x[3] = 0.0                                        # an empty row: middle codes, norm 0
     slots = torch.arange(T)
@@ -231,10 +237,13 @@ def test_padding_bad_slots_and_special_rows(oq, dtype):
     assert torch.all(k[5] == 0) and torch.all(k[11] == 0) and torch.all(k[3] == 0)
     assert torch.equal(k, v)
     # the same slot read several times, and slots outside the cache
-    again, _ = oq.oq_kv_read(r, c, cache, torch.tensor([7, 7, 0, 7]).cuda(), out_dtype=dtype)
+    # (in a call of the same form: few rows take another one, whose roundings differ)
+    twice = slots.clone()
+    twice[:4] = torch.tensor([7, 7, 0, 7])
+    again, _ = oq.oq_kv_read(r, c, cache, twice.cuda(), out_dtype=dtype)
     assert torch.equal(again[0], k[7]) and torch.equal(again[3], k[7])
     before = [t.clone() for t in (cache.k_codes, cache.v_codes, cache.k_norms, cache.v_norms)]
-    for bad in (2 * page, -2, 1 << 40, -(1 << 62)):
+    for bad in (pages * page, -2, 1 << 40, -(1 << 62)):
         s = torch.full((T,), -1)
         s[4] = bad
         oq.oq_kv_write(r, c, cache, x.cuda(), x.cuda(), s.cuda())
@@ -259,13 +268,14 @@ def test_padding_bad_slots_and_special_rows(oq, dtype):
     assert torch.equal(flat2[other], flat[other])
 
 
-def test_strided_rows_and_the_fused_projection(oq):
-    T, H, d = 45, 3, 128
+@pytest.mark.parametrize("T,d", [(45, 128), (333, 128), (100, 256)])
+def test_strided_rows_and_the_fused_projection(oq, T, d):
+    H = 3
     r, c = oq.oq_build_rpbh(d, 64, 0), oq.oq_lloyd_max(d, 4)
     qkv = make_rows(T, 4 * H, d, BF16, 4).cuda()
     k, v = qkv[:, H:2 * H], qkv[:, 3 * H:]
-    a, b = (oq.KVCache.empty(4, H, 16, d, 4) for _ in range(2))
-    slots = torch.randperm(64, generator=gen(0))[:T].cuda()
+    a, b = (oq.KVCache.empty(T // 16 + 2, H, 16, d, 4) for _ in range(2))
+    slots = torch.randperm(T + 16, generator=gen(0))[:T].cuda()
     oq.oq_kv_write(r, c, a, k, v, slots)
     oq.oq_kv_write(r, c, b, k.contiguous(), v.contiguous(), slots)
     for x, y in ((a.k_codes, b.k_codes), (a.v_codes, b.v_codes), (a.k_norms, b.k_norms),
@@ -277,6 +287,52 @@ def test_strided_rows_and_the_fused_projection(oq):
     oq.oq_check()
     assert torch.equal(wide[:, :H], k2) and torch.equal(wide[:, H:2 * H], v2)
     assert torch.all(wide[:, 2 * H:] == 5.0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_small_large_and_subnormal_rows(oq, dtype):
+    """Rows of any size have the codes of their direction: the smallest normal and subnormal
+    numbers, and rows whose squares pass fp16's range."""
+    T, H, d, bits = 300, 1, 128, 4
+    r, c = oq.oq_build_rpbh(d, 64, 0), oq.oq_lloyd_max(d, bits)
+    cache = oq.KVCache.empty(20, H, 16, d, bits)
+    x = make_rows(T, H, d, F32, 5)
+    tiny = 2.0 ** -15 if dtype == F16 else 2.0 ** -30
+    big = 100.0 if dtype == F16 else 2.0 ** 50
+    x[::3] *= tiny
+    x[1::3] *= big
+    x = x.to(dtype)
+    slots = torch.arange(T)
+    oq.oq_kv_write(r, c, cache, x.cuda(), x.cuda(), slots.cuda())
+    oq.oq_check()
+    R = CO.rotation(d, 64)
+    codes = CO.unpack(cache.k_codes.cpu().numpy().reshape(-1, d // 2)[:T], bits)
+    norms = cache.k_norms.cpu().double().numpy().reshape(-1)[:T]
+    check_codes(codes, f64(x).reshape(T, d), R, bits, norms)
+
+
+def test_caches_at_16_byte_addresses(oq):
+    """Code arrays that are 16- but not 32-byte aligned (a slice of a larger allocation)."""
+    T, H, d, bits = 400, 1, 128, 4
+    r, c = oq.oq_build_rpbh(d, 64, 0), oq.oq_lloyd_max(d, bits)
+    n = 25 * H * 16 * d * bits // 8
+    buf = [torch.zeros(n + 16, dtype=torch.uint8, device="cuda")[16:].view(25, H, 16, -1)
+           for _ in range(2)]
+    a = oq.KVCache.empty(25, H, 16, d, bits)
+    b = oq.KVCache(*buf, torch.zeros_like(a.k_norms), torch.zeros_like(a.k_norms), bits=bits)
+    x = make_rows(T, H, d, BF16, 6).cuda()
+    slots = torch.arange(T).cuda()
+    for cache in (a, b):
+        oq.oq_kv_write(r, c, cache, x, x, slots)
+    oq.oq_check()
+    assert torch.equal(a.k_codes, b.k_codes) and torch.equal(a.v_codes, b.v_codes)
+    for u, v in zip(oq.oq_kv_read(r, c, a, slots), oq.oq_kv_read(r, c, b, slots)):
+        assert torch.equal(u, v)
+    q = torch.randn(1, 2, d, generator=gen(1)).bfloat16().cuda()
+    at = (torch.tensor([0, 1], dtype=torch.int32).cuda(),
+          torch.tensor([399], dtype=torch.int32).cuda(),
+          torch.arange(25, dtype=torch.int32).view(1, -1).cuda())
+    assert torch.equal(oq.oq_kv_attend(r, c, a, q, *at), oq.oq_kv_attend(r, c, b, q, *at))
 
 
 def test_block_rht_and_exact_marginal_handles(oq):
