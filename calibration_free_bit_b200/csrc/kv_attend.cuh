@@ -22,8 +22,8 @@
 //     tensor memory and has nothing to gain at these row counts.
 // Scores, softmax statistics and sums are fp32.  fp16 enters in three places: the rotated query
 // (over a power of two of its own), the centroids (times alpha, see build_kv_lut) and the weights
-// p s_v, which are taken relative to a power of two above the row's largest s_v and times 2^14: what
-// a token adds is resolved down to 2^-39 of the largest.  With SPLIT (fp16 outputs) query and
+// p s_v, which are taken relative to a power of two above the row's largest s_v and times 2^6 to
+// 2^14: what a token adds is resolved down to 2^-31 of the largest.  With SPLIT (fp16 outputs) query and
 // weights enter as a sum of two fp16 numbers, so that only the centroids' rounding is left.
 #pragma once
 
@@ -103,7 +103,10 @@ __device__ __forceinline__ uint32_t half2_rest(float a, float b, uint32_t hi) {
 }
 
 constexpr int kWarps = 4;
-constexpr float kWeightScale = 16384.0f;             // 2^14: the weights' fp16 range
+// A row's reference m is raised only when a score passes it by kSlack (in powers of two), so most
+// steps need no reduction over lanes; weights reach 2^kSlack kWeightScale = 2^14 in fp16.
+constexpr float kSlack = 8.0f, kWeightScale = 64.0f;
+constexpr float kNone = -1e30f;                      // reference of a row that has seen nothing
 
 template <int D, int BITS> struct Shape {
     static constexpr int row_bytes = D * BITS / 8;
@@ -178,8 +181,8 @@ template <int D, int BITS, int NT, bool SPLIT> struct Smem {
     static constexpr bool q_shared = D == 256 && NT == 2;
     static constexpr int part = (D / 16) * NT * 4 * 32 * 4 + NT * 8 * 32 * 4;  // a warp's state
     static constexpr int fin_stride = D + 4;                                 // floats
-    static constexpr int big_a = Lut<BITS>::bytes > (kWarps / 2) * part
-                                     ? Lut<BITS>::bytes : (kWarps / 2) * part;
+    static constexpr int big_a = Lut<BITS, true>::bytes > (kWarps / 2) * part
+                                     ? Lut<BITS, true>::bytes : (kWarps / 2) * part;
     static constexpr int fin = rows * fin_stride * 4;
     static constexpr int big = (big_a > fin ? big_a : fin);                  // table, then partials
     static constexpr int q_at = big;
@@ -211,7 +214,7 @@ attend_tiles(const KvAttendParams p, const int row_tiles) {
     const int rank = blockIdx.x, splits = gridDim.x;       // the cluster is the whole x dimension
     const int kvh = blockIdx.y / row_tiles, tile = blockIdx.y - kvh * row_tiles;
     const int b = blockIdx.z;
-    fill_lut<BITS>(lut, p.lut);
+    fill_lut<BITS, true>(lut, p.lut);
     uint32_t ent[N];
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -224,6 +227,24 @@ attend_tiles(const KvAttendParams p, const int row_tiles) {
     if (row_base >= rows_all)
         return;
     const int nrows = min(M::rows, rows_all - row_base);
+
+    // ---- this warp's tokens: tiles of 16, every kWarps-th of the rank's share; the first are on
+    // their way while the queries are rotated ----
+    const int total = s.prefix + s.nodes;
+    const int tiles = (total + 15) >> 4, share = (tiles + splits - 1) / splits;
+    const int last = min(tiles, (rank + 1) * share);
+    const int *table = p.table + (long long)b * p.table_width;
+    const int in_page = (1 << p.c.page_log2) - 1;
+    const uint32_t col = lut_column<BITS>(lane);
+    int t = rank * share + warp;
+    Tile<D, BITS> ping, pong;
+    int page = 0;
+    bool bad_page = false;
+    if (t < last) {
+        ping.load(p, table[(t << 4) >> p.c.page_log2], (t << 4) & in_page, kvh, g, c);
+        if (t + kWarps < last)
+            page = table[((t + kWarps) << 4) >> p.c.page_log2];
+    }
 
     // ---- rotated queries, fp16 over a power of two a row ----
     for (int r = warp; r < M::rows; r += kWarps) {
@@ -299,16 +320,9 @@ attend_tiles(const KvAttendParams p, const int row_tiles) {
         qs[n][1] = qscale[8 * n + 2 * c + 1];
     }
 
-    // ---- this warp's tokens: tiles of 16, every kWarps-th of the rank's share ----
-    const int total = s.prefix + s.nodes;
-    const int tiles = (total + 15) >> 4, share = (tiles + splits - 1) / splits;
-    const int last = min(tiles, (rank + 1) * share);
-    const int *table = p.table + (long long)b * p.table_width;
-    const int in_page = (1 << p.c.page_log2) - 1;
-    const uint32_t col = BITS == 2 ? (lane & 15) * 8 : lane * 4;
-
     float acc[NT][KS][4];
-    float m[NT][2], l[NT][2], vs[NT][2];          // running maximum, sum, power of two over s_v
+    float m[NT][2], l[NT][2];                     // reference and sum
+    float vs[NT][2], vinv[NT][2];                 // power of two over s_v, kWeightScale over it
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -318,25 +332,11 @@ attend_tiles(const KvAttendParams p, const int row_tiles) {
                 acc[n][j][i] = 0.f;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            m[n][i] = -CUDART_INF_F, l[n][i] = 0.f, vs[n][i] = 0.f;
+            m[n][i] = kNone, l[n][i] = 0.f, vs[n][i] = 0.f, vinv[n][i] = 0.f;
     }
 
-    int t = rank * share + warp;
-    Tile<D, BITS> cur, nxt;
-    int page_n = 0;
-    bool bad_page = false;
-    if (t < last) {
-        cur.load(p, table[(t << 4) >> p.c.page_log2], (t << 4) & in_page, kvh, g, c);
-        if (t + kWarps < last)
-            page_n = table[((t + kWarps) << 4) >> p.c.page_log2];
-    }
-    for (; t < last; t += kWarps) {
-        const int tn = t + kWarps;
-        if (tn < last) {
-            nxt.load(p, page_n, (tn << 4) & in_page, kvh, g, c);
-            if (tn + kWarps < last)
-                page_n = table[((tn + kWarps) << 4) >> p.c.page_log2];
-        }
+    // One step: 16 tokens from token 16 t on.
+    auto step = [&](const Tile<D, BITS> &cur, int t) {
         // S^T = K Q^T
         float st[NT][4];
 #pragma unroll
@@ -347,11 +347,12 @@ attend_tiles(const KvAttendParams p, const int row_tiles) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             uint32_t a[4];
-            quad<BITS>(lut, cur.k[0], ks, col, a[0], a[2]);
-            quad<BITS>(lut, cur.k[1], ks, col, a[1], a[3]);
+            quad<BITS, true>(lut, cur.k[0], ks, col, a[0], a[2]);
+            quad<BITS, true>(lut, cur.k[1], ks, col, a[1], a[3]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                uint2 q = M::q_shared ? qsm[(n * KS + ks) * 32] : qf[M::q_shared ? 0 : n][M::q_shared ? 0 : ks];
+                uint2 q = M::q_shared ? qsm[(n * KS + ks) * 32]
+                                      : qf[M::q_shared ? 0 : n][M::q_shared ? 0 : ks];
                 mma16816(st[n], a, q.x, q.y);
                 if constexpr (SPLIT) {
                     q = M::q_shared ? qsm[M::q_half / 4 + (n * KS + ks) * 32]
@@ -361,16 +362,17 @@ attend_tiles(const KvAttendParams p, const int row_tiles) {
             }
         }
         // scores of tokens g, g + 8 and rows 2c, 2c + 1, in powers of two
-        float vmax[NT][2], smax[NT][2];
+        bool grow = false;
         const int tok = t << 4;
-        const bool edge = !cur.ok || tok + 16 > s.prefix;
-        bad_page |= !cur.ok;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 st[n][i] *= cur.kn[i >> 1] * qs[n][i & 1];
-            if (edge) {
+        if (!cur.ok || tok + 16 > s.prefix) {             // the page is missing, or the tile has nodes
+            bad_page |= !cur.ok;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int node = tok + g + 8 * (i >> 1) - s.prefix;
@@ -378,51 +380,46 @@ attend_tiles(const KvAttendParams p, const int row_tiles) {
                                      ((masks[8 * n + 2 * c + (i & 1)] >> node) & 1ull)));
                     if (!see)
                         st[n][i] = -CUDART_INF_F;
+                    else
+                        grow |= cur.vn[i >> 1] > vs[n][i & 1];
                 }
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    vmax[n][i] = fmaxf(st[n][i] > -CUDART_INF_F ? cur.vn[0] : 0.f,
-                                       st[n][2 + i] > -CUDART_INF_F ? cur.vn[1] : 0.f);
-            } else {
-                vmax[n][0] = vmax[n][1] = fmaxf(cur.vn[0], cur.vn[1]);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                smax[n][i] = fmaxf(st[n][i], st[n][2 + i]);
-        }
-#pragma unroll
-        for (int k = 4; k < 32; k <<= 1)
+        } else {
+            const float v = fmaxf(cur.vn[0], cur.vn[1]);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    smax[n][i] = fmaxf(smax[n][i], __shfl_xor_sync(0xffffffffu, smax[n][i], k));
-                    vmax[n][i] = fmaxf(vmax[n][i], __shfl_xor_sync(0xffffffffu, vmax[n][i], k));
-                }
-        bool grow = false;
+                grow |= v > vs[n][0] || v > vs[n][1];
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                grow |= smax[n][i] > m[n][i] || vmax[n][i] > vs[n][i];
+                grow |= fmaxf(st[n][i], st[n][2 + i]) > m[n][i] + kSlack;
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float f[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float mn = fmaxf(m[n][i], smax[n][i]);
-                    f[i] = m[n][i] > -CUDART_INF_F ? ex2(m[n][i] - mn) : 0.f;
-                    m[n][i] = mn;
+                    float up = fmaxf(st[n][i], st[n][2 + i]);
+                    float v = fmaxf(st[n][i] > -CUDART_INF_F ? cur.vn[0] : 0.f,
+                                    st[n][2 + i] > -CUDART_INF_F ? cur.vn[1] : 0.f);
+#pragma unroll
+                    for (int k = 4; k < 32; k <<= 1) {
+                        up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, k));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, k));
+                    }
+                    up = fmaxf(up, m[n][i]);
+                    f[i] = ex2(m[n][i] - up);
+                    m[n][i] = up;
                     l[n][i] *= f[i];
-                    if (vmax[n][i] > vs[n][i]) {
+                    if (v > vs[n][i]) {
                         // the power of two above, with room for a quarter more, in [2^-100, 2^127]
-                        const uint32_t up =
-                            (__float_as_uint(vmax[n][i] * 1.25f) & 0x7f800000u) + 0x00800000u;
-                        const float nv =
-                            __uint_as_float(min(max(up, 27u << 23), 254u << 23));
+                        const uint32_t p2 =
+                            (__float_as_uint(v * 1.25f) & 0x7f800000u) + 0x00800000u;
+                        const float nv = __uint_as_float(min(max(p2, 27u << 23), 254u << 23));
                         f[i] *= vs[n][i] / nv;
                         vs[n][i] = nv;
+                        vinv[n][i] = kWeightScale / nv;
                     }
                 }
 #pragma unroll
@@ -438,15 +435,16 @@ attend_tiles(const KvAttendParams p, const int row_tiles) {
         for (int n = 0; n < NT; ++n) {
             float w[4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float ref = m[n][i] > -CUDART_INF_F ? m[n][i] : 0.f;
-                const float inv = vs[n][i] > 0.f ? kWeightScale / vs[n][i] : 0.f;
+            for (int i = 0; i < 4; ++i) {
+                const float e = ex2(st[n][i] - m[n][i & 1]);
+                l[n][i & 1] += e;
+                w[i] = e * (cur.vn[i >> 1] * vinv[n][i & 1]);
+            }
+            if (!cur.ok || tok + 16 > s.prefix) {         // what is not seen may have any norm
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float e = ex2(st[n][2 * k + i] - ref);
-                    l[n][i] += e;
-                    w[2 * k + i] = st[n][2 * k + i] > -CUDART_INF_F ? e * (cur.vn[k] * inv) : 0.f;
-                }
+                for (int i = 0; i < 4; ++i)
+                    if (st[n][i] == -CUDART_INF_F)
+                        w[i] = 0.f;
             }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -461,31 +459,41 @@ attend_tiles(const KvAttendParams p, const int row_tiles) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             cur.values(i, g, vw[i]);
+        mixed<BITS>(vw[0], vw[1]);
+        mixed<BITS>(vw[2], vw[3]);
 #pragma unroll
         for (int j = 0; j < KS; j += 2) {
-            uint32_t lo[4], hi[4];
+            uint32_t x[4], y[4];
+            quad_of_two<BITS, true>(lut, vw[0], vw[1], j / 2, col, x);
+            quad_of_two<BITS, true>(lut, vw[2], vw[3], j / 2, col, y);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                quad<BITS>(lut, vw[i], j / 2, col, lo[i], hi[i]);
-            uint32_t a[4], a2[4];
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t a[4] = {x[2 * h], x[2 * h + 1], y[2 * h], y[2 * h + 1]};
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                a[2 * i] = prmt(lo[2 * i], lo[2 * i + 1], 0x5410);
-                a[2 * i + 1] = prmt(lo[2 * i], lo[2 * i + 1], 0x7632);
-                a2[2 * i] = prmt(hi[2 * i], hi[2 * i + 1], 0x5410);
-                a2[2 * i + 1] = prmt(hi[2 * i], hi[2 * i + 1], 0x7632);
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                mma16816(acc[n][j], a, pb[n][0], pb[n][1]);
-                mma16816(acc[n][j + 1], a2, pb[n][0], pb[n][1]);
-                if constexpr (SPLIT) {
-                    mma16816(acc[n][j], a, pl[n][0], pl[n][1]);
-                    mma16816(acc[n][j + 1], a2, pl[n][0], pl[n][1]);
+                for (int n = 0; n < NT; ++n) {
+                    mma16816(acc[n][j + h], a, pb[n][0], pb[n][1]);
+                    if constexpr (SPLIT)
+                        mma16816(acc[n][j + h], a, pl[n][0], pl[n][1]);
                 }
             }
         }
-        cur = nxt;
+    };
+    // the tile after t, and the page of the one after that
+    auto fetch = [&](Tile<D, BITS> &to, int t) {
+        const int tn = t + kWarps;
+        if (tn < last) {
+            to.load(p, page, (tn << 4) & in_page, kvh, g, c);
+            if (tn + kWarps < last)
+                page = table[((tn + kWarps) << 4) >> p.c.page_log2];
+        }
+    };
+    for (; t < last; t += 2 * kWarps) {
+        fetch(pong, t);
+        step(ping, t);
+        if (t + kWarps >= last)
+            break;
+        fetch(ping, t + kWarps);
+        step(pong, t + kWarps);
     }
     if (bad_page && lane == 0)
         atomicOr(p.err, AT_ERR_PAGE);
@@ -534,8 +542,8 @@ attend_tiles(const KvAttendParams p, const int row_tiles) {
                     const float om = mine[(NT * KS * 4 + n * 4 + i) * 32];
                     const float ol = mine[(NT * KS * 4 + n * 4 + 2 + i) * 32];
                     const float mn = fmaxf(m[n][i], om);
-                    f[i] = m[n][i] > -CUDART_INF_F ? ex2(m[n][i] - mn) : 0.f;
-                    h[i] = om > -CUDART_INF_F ? ex2(om - mn) : 0.f;
+                    f[i] = ex2(m[n][i] - mn);
+                    h[i] = ex2(om - mn);
                     m[n][i] = mn;
                     l[n][i] = l[n][i] * f[i] + ol * h[i];
                 }
@@ -574,7 +582,7 @@ attend_tiles(const KvAttendParams p, const int row_tiles) {
     else
         __syncthreads();
     for (int r = rank + splits * warp; r < nrows; r += splits * kWarps) {
-        float mx = -CUDART_INF_F;
+        float mx = kNone;
         for (int k = 0; k < splits; ++k)
             mx = fmaxf(mx, *cl.map_shared_rank(row_m + r, k));
         float o[N], sum = 0.f;
@@ -582,8 +590,7 @@ attend_tiles(const KvAttendParams p, const int row_tiles) {
         for (int i = 0; i < N; ++i)
             o[i] = 0.f;
         for (int k = 0; k < splits; ++k) {
-            const float mk = *cl.map_shared_rank(row_m + r, k);
-            const float f = mk > -CUDART_INF_F ? ex2(mk - mx) : 0.f;
+            const float f = ex2(*cl.map_shared_rank(row_m + r, k) - mx);
             sum += f * *cl.map_shared_rank(row_l + r, k);
             const float4 *src = reinterpret_cast<const float4 *>(
                 cl.map_shared_rank(fin + r * M::fin_stride + lane * N, k));
@@ -594,7 +601,7 @@ attend_tiles(const KvAttendParams p, const int row_tiles) {
             }
         }
         warp_wht<D>(o, p.h, lane);
-        const float inv = mx > -CUDART_INF_F ? p.o_scale / sum : 0.f;
+        const float inv = sum == 0.f ? 0.f : p.o_scale / sum;      // nothing seen: zeros
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < N; ++i)

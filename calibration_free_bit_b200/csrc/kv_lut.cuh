@@ -14,33 +14,52 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
 }
 
 // ---- codes -> pairs of fp16 centroids ----
-// Table in shared memory, one copy a lane: bits 2: entry e = 16 columns of 8 bytes; else 32
-// columns of 4 bytes.
-template <int BITS> struct Lut {
-    static constexpr int entries = BITS == 3 || BITS == 6 ? 64 : 256;
-    static constexpr int bytes = entries * 128;
+// Table in shared memory, one copy a lane, so that any entries at once are free of bank conflicts.
+// Entries lie PITCH bytes apart: 128, or 256 for entries of a whole byte (bits 2, 4, 8; the second
+// half is not used): one byte permute of the code word and the lane's column then forms the
+// address, where 128 takes a shift and a mask.  A lane's column has 8 bytes at bits 2 (16 columns,
+// two lanes each), else 4.
+template <int BITS, bool WIDE> struct Lut {
+    static constexpr bool whole = BITS != 3 && BITS != 6;
+    static constexpr int entries = whole ? 256 : 64;
+    static constexpr int pitch = whole && WIDE ? 256 : 128;
+    static constexpr int bytes = entries * pitch;
 };
 
-template <int BITS>
+template <int BITS, bool WIDE>
 __device__ __forceinline__ void fill_lut(unsigned char *lut, const uint32_t *src) {
-    if constexpr (BITS == 2) {
-        for (int i = threadIdx.x; i < 256 * 16; i += blockDim.x)
-            reinterpret_cast<uint2 *>(lut)[i] = reinterpret_cast<const uint2 *>(src)[i >> 4];
-    } else {
-        for (int i = threadIdx.x; i < Lut<BITS>::entries * 8; i += blockDim.x) {
-            const uint32_t v = src[i >> 3];
-            reinterpret_cast<uint4 *>(lut)[i] = make_uint4(v, v, v, v);
+    using L = Lut<BITS, WIDE>;
+    for (int i = threadIdx.x; i < L::entries * 8; i += blockDim.x) {
+        uint4 v;
+        if constexpr (BITS == 2) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(src) + (i >> 3));
+            v = make_uint4(u.x, u.y, u.x, u.y);
+        } else {
+            const uint32_t u = __ldg(src + (i >> 3));
+            v = make_uint4(u, u, u, u);
         }
+        *reinterpret_cast<uint4 *>(lut + (i >> 3) * L::pitch + (i & 7) * 16) = v;
     }
 }
 
-// Entry of the group of bits [at, at + n) of w (n <= 8, at a compile-time constant), `col` this
-// lane's column offset in bytes.
-__device__ __forceinline__ uint32_t look(const unsigned char *lut, uint32_t w, int at, int n,
-                                         uint32_t col) {
-    const uint32_t mask = ((1u << n) - 1u) << 7;
+template <int BITS> __device__ __forceinline__ uint32_t lut_column(int lane) {
+    return BITS == 2 ? (lane & 15) * 8 : lane * 4;
+}
+
+// Entry of byte k of w (k a compile-time constant).
+template <class V, bool WIDE>
+__device__ __forceinline__ V look8(const unsigned char *lut, uint32_t w, int k, uint32_t col) {
+    if constexpr (WIDE)
+        return *reinterpret_cast<const V *>(lut + prmt(w, col, 0x5504u | ((uint32_t)k << 4)));
+    const uint32_t sh = k ? w >> (8 * k - 7) : w << 7;
+    return *reinterpret_cast<const V *>(lut + ((sh & 0x7f80u) | col));
+}
+
+// Entry of the 6 bits of w from bit `at` on.
+__device__ __forceinline__ uint32_t look6(const unsigned char *lut, uint32_t w, int at,
+                                          uint32_t col) {
     const uint32_t sh = at >= 7 ? w >> (at - 7) : w << (7 - at);
-    return *reinterpret_cast<const uint32_t *>(lut + ((sh & mask) | col));
+    return *reinterpret_cast<const uint32_t *>(lut + ((sh & (63u << 7)) | col));
 }
 
 // Bits [at, at + n) of the words w as the low bits of one word (at, n compile-time).
@@ -53,32 +72,75 @@ __device__ __forceinline__ uint32_t word_at(const uint32_t (&w)[W], int at, int 
 }
 
 // Codes 4 i .. 4 i + 3 of the packed words w as two fp16 pairs.
-template <int BITS, int W>
+template <int BITS, bool WIDE, int W>
 __device__ __forceinline__ void quad(const unsigned char *lut, const uint32_t (&w)[W], int i,
                                      uint32_t col, uint32_t &lo, uint32_t &hi) {
     if constexpr (BITS == 2) {
-        const uint32_t v = w[i >> 2];
-        const int at = 8 * (i & 3);
-        const uint32_t sh = at >= 7 ? v >> (at - 7) : v << (7 - at);
-        const uint2 e = *reinterpret_cast<const uint2 *>(lut + ((sh & 0x7f80u) | col));
+        const uint2 e = look8<uint2, WIDE>(lut, w[i >> 2], i & 3, col);
         lo = e.x;
         hi = e.y;
     } else if constexpr (BITS == 4) {
-        const uint32_t v = w[i >> 1];
-        lo = look(lut, v, 16 * (i & 1), 8, col);
-        hi = look(lut, v, 16 * (i & 1) + 8, 8, col);
+        lo = look8<uint32_t, WIDE>(lut, w[i >> 1], 2 * (i & 1), col);
+        hi = look8<uint32_t, WIDE>(lut, w[i >> 1], 2 * (i & 1) + 1, col);
     } else if constexpr (BITS == 3) {
         const uint32_t v = word_at(w, 12 * i, 12);
-        lo = look(lut, v, 0, 6, col);
-        hi = look(lut, v, 6, 6, col);
+        lo = look6(lut, v, 0, col);
+        hi = look6(lut, v, 6, col);
     } else if constexpr (BITS == 6) {
         const uint32_t v = word_at(w, 24 * i, 24);
-        lo = prmt(look(lut, v, 0, 6, col), look(lut, v, 6, 6, col), 0x5410);
-        hi = prmt(look(lut, v, 12, 6, col), look(lut, v, 18, 6, col), 0x5410);
+        lo = prmt(look6(lut, v, 0, col), look6(lut, v, 6, col), 0x5410);
+        hi = prmt(look6(lut, v, 12, col), look6(lut, v, 18, col), 0x5410);
     } else {
         const uint32_t v = w[i];
-        lo = prmt(look(lut, v, 0, 8, col), look(lut, v, 8, 8, col), 0x5410);
-        hi = prmt(look(lut, v, 16, 8, col), look(lut, v, 24, 8, col), 0x5410);
+        lo = prmt(look8<uint32_t, WIDE>(lut, v, 0, col), look8<uint32_t, WIDE>(lut, v, 1, col), 0x5410);
+        hi = prmt(look8<uint32_t, WIDE>(lut, v, 2, col), look8<uint32_t, WIDE>(lut, v, 3, col), 0x5410);
+    }
+}
+
+// The same codes of two rows x and y (the packed words of each), transposed: o[k] = (code 4 i + k
+// of x, that of y).  4-bit codes are merged to bytes of one code of each row first (`mixed`).
+template <int BITS, bool WIDE, int W>
+__device__ __forceinline__ void quad_of_two(const unsigned char *lut, const uint32_t (&x)[W],
+                                            const uint32_t (&y)[W], int i, uint32_t col,
+                                            uint32_t (&o)[4]) {
+    if constexpr (BITS == 4) {
+        // x = even codes of both rows, y = odd ones
+        const int k = 2 * (i & 1);
+        o[0] = look8<uint32_t, WIDE>(lut, x[i >> 1], k, col);
+        o[1] = look8<uint32_t, WIDE>(lut, y[i >> 1], k, col);
+        o[2] = look8<uint32_t, WIDE>(lut, x[i >> 1], k + 1, col);
+        o[3] = look8<uint32_t, WIDE>(lut, y[i >> 1], k + 1, col);
+    } else if constexpr (BITS == 6) {
+        const uint32_t u = word_at(x, 24 * i, 24), v = word_at(y, 24 * i, 24);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            o[k] = prmt(look6(lut, u, 6 * k, col), look6(lut, v, 6 * k, col), 0x5410);
+    } else if constexpr (BITS == 8) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            o[k] = prmt(look8<uint32_t, WIDE>(lut, x[i], k, col), look8<uint32_t, WIDE>(lut, y[i], k, col),
+                        0x5410);
+    } else {
+        uint32_t a, b, c, d;
+        quad<BITS, WIDE>(lut, x, i, col, a, b);
+        quad<BITS, WIDE>(lut, y, i, col, c, d);
+        o[0] = prmt(a, c, 0x5410);
+        o[1] = prmt(a, c, 0x7632);
+        o[2] = prmt(b, d, 0x5410);
+        o[3] = prmt(b, d, 0x7632);
+    }
+}
+
+// Two rows' words as quad_of_two takes them.
+template <int BITS, int W>
+__device__ __forceinline__ void mixed(uint32_t (&x)[W], uint32_t (&y)[W]) {
+    if constexpr (BITS == 4) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const uint32_t a = x[i], b = y[i];
+            x[i] = (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u);
+            y[i] = ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+        }
     }
 }
 
