@@ -5,8 +5,8 @@ rotate + norm + quantize on the CUDA cores), csrc/k1_tc.cu (the same with the bl
 on the tensor cores, bf16 rows), csrc/k2_decode.cu (code -> fp16 prepass), csrc/k2_linear.cu
 (tcgen05 GEMM; it decodes 4-bit activation codes itself), csrc/k3_fused.cu (the one-call step
 as one persistent kernel); csrc/oq_cache.cpp, csrc/rope.cu, csrc/kv_cache.cu,
-csrc/kv_tc.cu and csrc/kv_attend*.cu (rotary positions, the quantised key/value cache and the attention over it;
-the latter an object for each bit width, from csrc/kv_attend.cuh).
+csrc/kv_tc.cu, csrc/kv_attend*.cu and csrc/kv_wide*.cu (rotary positions, the quantised
+key/value cache and the attention over it; the latter an object for each bit width).
 Objects are compiled
 in parallel into calibration_free_bit_b200/_build/ and linked into
 calibration_free_bit_b200/liboq.so; the CUDA runtime is linked statically, the driver API is
@@ -26,7 +26,8 @@ INCLUDE = os.path.join(ROOT, "include")
 SOURCES = ["oq_host.cpp", "k1_rotquant.cu", "k1_tc.cu", "k2_decode.cu", "k2_linear.cu",
            "k3_fused.cu", "oq_cache.cpp", "rope.cu", "kv_cache.cu", "kv_tc.cu", "kv_attend.cu",
            "kv_attend_b2.cu", "kv_attend_b3.cu", "kv_attend_b4.cu", "kv_attend_b6.cu",
-           "kv_attend_b8.cu"]
+           "kv_attend_b8.cu", "kv_wide_b2.cu", "kv_wide_b3.cu", "kv_wide_b4.cu", "kv_wide_b6.cu",
+           "kv_wide_b8.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O3",
                 "-I" + INCLUDE, "-I" + CSRC]

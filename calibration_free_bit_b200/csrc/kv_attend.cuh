@@ -28,8 +28,8 @@
 #pragma once
 
 #include <cooperative_groups.h>
-#include <math_constants.h>
 
+#include "kv_attend_ops.cuh"
 #include "kv_internal.h"
 #include "kv_lut.cuh"
 #include "kv_ops.cuh"
@@ -38,43 +38,6 @@ namespace oq {
 namespace attend {
 
 using namespace kvops;
-
-enum : unsigned {
-    AT_ERR_ROWS = 1u << 0,      // q_start: decreasing, past the rows given, or over max_nodes
-    AT_ERR_LEN = 1u << 1,       // prefix negative, or past the page table
-    AT_ERR_PAGE = 1u << 2,      // a page index outside the cache
-    AT_ERR_WAIT = 1u << 3,      // a bounded wait gave up
-};
-
-// One sequence's rows and lengths; false (with the error recorded) if they are not usable.
-struct Seq {
-    int row0, nodes, prefix;
-};
-__device__ __forceinline__ bool load_seq(const KvAttendParams &p, int b, Seq *s, bool tell) {
-    const int r0 = p.q_start[b], r1 = p.q_start[b + 1];
-    const int prefix = p.prefix[b];
-    unsigned err = 0;
-    if (r0 < 0 || r1 < r0 || (long long)r1 > p.q_rows || r1 - r0 > p.max_nodes)
-        err = AT_ERR_ROWS;
-    else if (prefix < 0 ||
-             (long long)prefix + (r1 - r0) > ((long long)p.table_width << p.c.page_log2))
-        err = AT_ERR_LEN;
-    if (err) {
-        if (tell)
-            atomicOr(p.err, err);
-        return false;
-    }
-    s->row0 = r0;
-    s->nodes = r1 - r0;
-    s->prefix = prefix;
-    return true;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // c += a b: a 16 x 16 (row), b 16 x 8 (column), fp16 in, fp32 out.
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -91,23 +54,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     return r;
 }
 
-__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// What fp16 leaves of a and b.
-__device__ __forceinline__ uint32_t half2_rest(float a, float b, uint32_t hi) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-    return half2_bits(a - f.x, b - f.y);
-}
-
 constexpr int kWarps = 4;
-// A row's reference m is raised only when a score passes it by kSlack (in powers of two), so most
-// steps need no reduction over lanes; weights reach 2^kSlack kWeightScale = 2^14 in fp16.
-constexpr float kSlack = 8.0f, kWeightScale = 64.0f;
-constexpr float kNone = -1e30f;                      // reference of a row that has seen nothing
-
 template <int D, int BITS> struct Shape {
     static constexpr int row_bytes = D * BITS / 8;
     static constexpr int k_bytes = row_bytes / 4;     // a lane's share of a key row

@@ -108,16 +108,41 @@ struct KvAttendParams {
     int h;
     float qk_scale;               // scale * log2(e) / (sqrt(d h) alpha)
     float o_scale;                // 1 / (sqrt(d h) alpha)
+    const void *r_img;            // R' as the tensor cores' operand in q's type (kv_wide.cuh)
     unsigned *err;                // device error word (set by launch_kv_attend)
 };
+// Workspace and work list of the forms that share out all tokens evenly (kv_attend_ops.cuh).
+struct KvAttendSpace {
+    float *part;                  // [slots][rows][d] sums of a piece's rows
+    float *stat;                  // [slots][2][rows] references and weights' sums
+    long long *first;             // [B + 1] units before each sequence
+    int rows;                     // rows of a slot: the tile's, or all a sequence can have
+    int segments;                 // segments of a sequence with the most rows
+    int most, least;              // workers, and units that one has at least
+    static size_t stat_at(long long slots, int rows, int d) { return (size_t)slots * rows * d * 4; }
+    static size_t first_at(long long slots, int rows, int d) {
+        return stat_at(slots, rows, d) + ((size_t)slots * rows * 8 + 15) / 16 * 16;
+    }
+};
+// Many rows a key head, heads of 128 (kv_wide.cuh).
+cudaError_t launch_kv_wide(const KvAttendParams &p, const KvAttendSpace &ws, int dtype,
+                           cudaStream_t st);
+cudaError_t launch_kv_wide_b2(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, cudaStream_t st);
+cudaError_t launch_kv_wide_b3(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, cudaStream_t st);
+cudaError_t launch_kv_wide_b4(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, cudaStream_t st);
+cudaError_t launch_kv_wide_b6(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, cudaStream_t st);
+cudaError_t launch_kv_wide_b8(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, cudaStream_t st);
+// Device memory that launch_kv_attend needs for a call, 0 for none; it is given to it as `space`.
+size_t kv_attend_space(const KvAttendParams &p, int num_sms);
+
 // The kernels of one bit width; `splits` CTAs (a cluster) share a row tile's tokens.
 cudaError_t launch_kv_attend_b2(const KvAttendParams &p, int dtype, int splits, cudaStream_t st);
 cudaError_t launch_kv_attend_b3(const KvAttendParams &p, int dtype, int splits, cudaStream_t st);
 cudaError_t launch_kv_attend_b4(const KvAttendParams &p, int dtype, int splits, cudaStream_t st);
 cudaError_t launch_kv_attend_b6(const KvAttendParams &p, int dtype, int splits, cudaStream_t st);
 cudaError_t launch_kv_attend_b8(const KvAttendParams &p, int dtype, int splits, cudaStream_t st);
-cudaError_t launch_kv_attend(const KvAttendParams &p, int dtype, cudaStream_t st, int num_sms,
-                             std::string *why);
+cudaError_t launch_kv_attend(const KvAttendParams &p, void *space, int dtype, cudaStream_t st,
+                             int num_sms, std::string *why);
 
 cudaError_t read_and_clear_kv_error(unsigned *out, cudaStream_t st);
 cudaError_t read_and_clear_attend_error(unsigned *out, cudaStream_t st);

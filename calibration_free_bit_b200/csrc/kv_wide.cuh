@@ -1,0 +1,565 @@
+// kv_wide.cuh -- the cache's attention for many rows a key head (trees of drafted tokens), heads of
+// 128: tcgen05 with tiles of 128 rows by 128 tokens.  Method and checks: kv_attend.cuh; work list:
+// kv_attend_ops.cuh; the pieces of a segment are joined by a second kernel (kv_attend.cu).
+//
+// One CTA per SM walks a contiguous range of units.  For a piece it rotates the 128 queries (one
+// tcgen05.mma with the rotation's dense operand) and keeps them as the A operand in shared memory;
+// then, per unit, decoder warps turn the codes of 128 tokens into the fp16 operands K (elements
+// contiguous, K-major) and V (the same layout, read as N-major), one row a thread; S = Q K^T goes to
+// tensor memory; a softmax thread owns a row, takes S from there and puts the weights back as the A
+// operand of O += P V.  Two softmax groups take the units in turn, each with its own S, O and row
+// statistics, so that one's exponentials run beside the other's products; they meet at the end.
+// What bounds a unit: shared memory (16384 table lookups and 64 KB of operands stored), the
+// exponentials (16384), and the issue slots of both, about a thousand cycles each.
+//   - Key norms enter the operand (times 2^-e, e by 32 tokens, so that fp16 holds any norm): scores
+//     of a group of 32 tokens then share one factor, and the search for a new maximum is a maximum
+//     over raw products.  Value norms enter with the weights, a row at a time, so that what a row
+//     does not see (a NaN, an infinity) never reaches it.
+#pragma once
+
+#include <type_traits>
+
+#include "kv_attend_ops.cuh"
+#include "kv_internal.h"
+#include "kv_lut.cuh"
+#include "kv_ops.cuh"
+#include "sm100_common.cuh"
+
+namespace oq {
+namespace attend {
+
+using namespace sm100;
+using kvops::prmt;
+
+namespace wide {
+
+constexpr int kRows = 128, kTokens = 128, D = 128;
+constexpr int kSoftWarps = 8, kDecWarps = 8;
+constexpr int kThreads = 32 * (kSoftWarps + kDecWarps + 1);
+constexpr int kTile = 128 * D * 2;                    // an operand: 32 KB
+
+struct Smem {
+    static constexpr int q_at = 0;
+    static constexpr int k_at = kTile;                // two stages
+    static constexpr int v_at = 3 * kTile;            // two stages
+    static constexpr int lut_at = 5 * kTile;
+    static constexpr int vn_at = lut_at + 32768;      // [2][128] value norms
+    static constexpr int kexp_at = vn_at + 1024;      // [2][4] powers of two of the key norms
+    static constexpr int vmax_at = kexp_at + 32;      // [2][4] largest value norms
+    static constexpr int bad_at = vmax_at + 32;       // [2][4] tokens of missing pages
+    static constexpr int qs_at = bad_at + 32;         // [128] score factor of a row
+    static constexpr int mask_at = qs_at + 512;       // [128]
+    static constexpr int stat_at = mask_at + 1024;    // [2][3][128]: m, l, s_v scale
+    static constexpr int work_at = stat_at + 3072;
+    static constexpr int bars_at = work_at + 64;
+    static constexpr int bytes = bars_at + 128 + 1024;
+};
+enum { B_FULL = 0, B_S = 2, B_P = 4, B_PV = 6, B_Q = 8, B_END = 9 };
+
+__device__ __forceinline__ uint32_t operand_at(int r, int ch) {
+    return (uint32_t)(ch >> 3) * 16384u + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+}
+
+// V as the B operand of P V: N (elements) contiguous.  Atoms of 64 elements by 8 tokens; the next
+// 8 tokens lie 1024 bytes on, the next 64 elements 16 KB.
+__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(16384 >> 4) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+template <bool BF16> __device__ __forceinline__ uint32_t idesc_q() {
+    return idesc_f16(128, 128) | (BF16 ? (1u << 7) | (1u << 10) : 0u);
+}
+
+struct Work {
+    long long u0, u1, before;
+    int b;
+};
+
+}  // namespace wide
+
+template <class E, int BITS>
+__global__ void __launch_bounds__(wide::kThreads, 1)
+attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) {
+    using namespace wide;
+    using S = wide::Smem;
+    extern __shared__ unsigned char raw[];
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    unsigned char *sm = raw + (base - smem_u32(raw));
+    const uint32_t bars = base + S::bars_at;
+    auto bar = [&](int i) { return bars + 8u * i; };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + S::bars_at + 96);
+    volatile int *gone = reinterpret_cast<volatile int *>(sm + S::bars_at + 100);
+    Work *work = reinterpret_cast<Work *>(sm + S::work_at);
+    float *vn_s = reinterpret_cast<float *>(sm + S::vn_at);
+    float *kexp_s = reinterpret_cast<float *>(sm + S::kexp_at);
+    float *vmax_s = reinterpret_cast<float *>(sm + S::vmax_at);
+    uint32_t *bad_s = reinterpret_cast<uint32_t *>(sm + S::bad_at);
+    float *qs_s = reinterpret_cast<float *>(sm + S::qs_at);
+    unsigned long long *mask_s = reinterpret_cast<unsigned long long *>(sm + S::mask_at);
+    float *stat_s = reinterpret_cast<float *>(sm + S::stat_at);
+    unsigned char *lut = sm + S::lut_at;
+
+    pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    fill_lut<BITS, false>(lut, p.lut);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(B_FULL + i), kDecWarps);
+            mbar_init(bar(B_S + i), 1);
+            mbar_init(bar(B_P + i), 4);
+            mbar_init(bar(B_PV + i), 1);
+        }
+        mbar_init(bar(B_Q), 1);
+        mbar_init(bar(B_END), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        *gone = 0;
+    }
+    pdl_wait();
+    if (warp == kSoftWarps + kDecWarps) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(tmem_slot)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        const long long U =
+            count_units<kTokens, kRows>(p, blockIdx.x == 0 ? ws.first : nullptr);
+        const long long W = workers_for(U, gridDim.x, ws.least);
+        Work w = {0, 0, 0, 0};
+        if (blockIdx.x < W) {
+            w.u0 = blockIdx.x * U / W;
+            w.u1 = (blockIdx.x + 1) * U / W;
+            w.b = find_sequence<kTokens, kRows>(p, w.u0, &w.before);
+        }
+        if (lane == 0)
+            *work = w;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    auto wait = [&](int i, uint32_t parity) {
+        if (*gone)
+            return;
+        if (!mbar_wait(bar(i), parity & 1u)) {
+            *gone = 1;
+            atomicOr(p.err, AT_ERR_WAIT);
+        }
+    };
+
+    long long u = work->u0, before = work->before;
+    const long long u1 = work->u1;
+    int b = work->b;
+    uint32_t used[2] = {0, 0}, pieces = 0;           // units so far of either group, pieces
+    while (u < u1) {
+        Seq s;
+        Units un = units_of<kTokens, kRows>(p, b, &s, false);
+        if (u >= before + (long long)un.tiles * un.segments) {
+            before += (long long)un.tiles * un.segments;
+            ++b;
+            continue;
+        }
+        const int seg = (int)((u - before) / un.tiles);
+        const int tile0 = (int)((u - before) - (long long)seg * un.tiles);
+        const int n = (int)min((long long)(un.tiles - tile0), u1 - u);
+        const int row_tiles = un.segments / p.c.kv_heads;
+        const int kvh = seg / row_tiles, row_base = (seg - kvh * row_tiles) * kRows;
+        const int nrows = min(kRows, s.nodes * p.group - row_base);
+        const int total = s.prefix + s.nodes;
+
+        // ---- queries: raw rows to V's first stage, the rotation to K's ----
+        if (warp < kSoftWarps) {
+            for (int i = threadIdx.x; i < kTile / 16; i += 32 * kSoftWarps)
+                reinterpret_cast<uint4 *>(sm + S::k_at)[i] = __ldg(r_img + i);
+            if (threadIdx.x < kRows) {
+                const int node = (row_base + threadIdx.x) / p.group;
+                mask_s[threadIdx.x] =
+                    threadIdx.x >= nrows ? 0ull
+                    : p.mask ? (unsigned long long)p.mask[s.row0 + node] &
+                                   (s.nodes >= 64 ? ~0ull : (1ull << s.nodes) - 1ull)
+                             : (2ull << node) - 1ull;
+            }
+        } else if (warp < kSoftWarps + kDecWarps) {
+            const int t = threadIdx.x - 32 * kSoftWarps, ch = t & 15;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = i * 16 + (t >> 4);
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (r < nrows) {
+                    const int node = (row_base + r) / p.group, e = row_base + r - node * p.group;
+                    v = *reinterpret_cast<const uint4 *>(
+                        static_cast<const E *>(p.q) + (s.row0 + node) * p.q_stride +
+                        (kvh * p.group + e) * D + ch * 8);
+                }
+                *reinterpret_cast<uint4 *>(sm + S::v_at + operand_at(r, ch)) = v;
+            }
+        }
+        fence_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        if (threadIdx.x == 32 * (kSoftWarps + kDecWarps)) {
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                mma_ss(tmem, sw128_desc(base + S::v_at + (k >> 2) * 16384) + 2 * (k & 3),
+                       sw128_desc(base + S::k_at + (k >> 2) * 16384) + 2 * (k & 3),
+                       idesc_q<std::is_same<E, __nv_bfloat16>::value>(), k != 0);
+            mma_commit(bar(B_Q));
+        }
+        if (warp < 4) {
+            wait(B_Q, pieces);
+            tc_fence_after();
+            const uint32_t mine = tmem + ((uint32_t)(32 * warp) << 16);
+            float big = 0.f;
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                uint32_t z[32];
+                tmem_ld32(mine + 32 * k, z);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    big = fmaxf(big, fabsf(__uint_as_float(z[i])));
+            }
+            // 2^e <= big < 2^(e+1); values over 2^e stay below 2 (2^e and its inverse are normal)
+            uint32_t ex = (__float_as_uint(big) >> 23) & 255u;
+            ex = ex < 1u ? 1u : (ex > 253u ? 253u : ex);
+            const float up = __uint_as_float(ex << 23), down = __uint_as_float((254u - ex) << 23);
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                uint32_t z[32];
+                tmem_ld32(mine + 32 * k, z);
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    auto f = [&](int j) { return __uint_as_float(z[i + j]) * down; };
+                    *reinterpret_cast<uint4 *>(sm + S::q_at +
+                                               operand_at(threadIdx.x, 4 * k + i / 8)) =
+                        make_uint4(half2_bits(f(0), f(1)), half2_bits(f(2), f(3)),
+                                   half2_bits(f(4), f(5)), half2_bits(f(6), f(7)));
+                }
+            }
+            qs_s[threadIdx.x] = up * p.qk_scale;
+            fence_async_smem();
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+
+        if (warp < kSoftWarps) {
+            // ---------------- softmax: group `me` has units me, me + 2, ... ----------------
+            const int me = warp >> 2, r = threadIdx.x & 127;
+            const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+            const uint32_t tS = tmem + lanes + 128 * me, tO = tmem + lanes + 256 + 128 * me;
+            const float qs = qs_s[r];
+            const unsigned long long mask = mask_s[r];
+            float m = kNone, l = 0.f, vs = 0.f, vinv = 0.f;
+            for (int i = me; i < n; i += 2) {
+                const uint32_t c = used[me] + (i >> 1);
+                const int tok = (tile0 + i) * kTokens;
+                wait(B_FULL + me, c);                 // the norms, exponents and lost tokens
+                wait(B_S + me, c);
+                tc_fence_after();
+                const float4 ke = *reinterpret_cast<const float4 *>(kexp_s + 4 * me);
+                const float4 vm = *reinterpret_cast<const float4 *>(vmax_s + 4 * me);
+                const uint4 bad = *reinterpret_cast<const uint4 *>(bad_s + 4 * me);
+                const float f[4] = {qs * ke.x, qs * ke.y, qs * ke.z, qs * ke.w};
+                const uint32_t out[4] = {bad.x, bad.y, bad.z, bad.w};
+                const bool edge = tok + kTokens > s.prefix || (bad.x | bad.y | bad.z | bad.w);
+                // tokens of group k that this row sees
+                auto seen = [&](int k) -> uint32_t {
+                    const int first = tok + 32 * k - s.prefix;        // node of its first token
+                    uint32_t v;
+                    if (first <= -32)
+                        v = ~0u;
+                    else if (first < 0)
+                        v = (uint32_t)(mask << -first) | ((1u << -first) - 1u);
+                    else
+                        v = first < 64 ? (uint32_t)(mask >> first) : 0u;
+                    return v & ~out[k];
+                };
+                const float *vn = vn_s + 128 * me;
+                float top = -CUDART_INF_F, vtop;
+                if (!edge) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t z[32];
+                        tmem_ld32(tS + 32 * k, z);
+                        float a = fmaxf(__uint_as_float(z[0]), __uint_as_float(z[1]));
+#pragma unroll
+                        for (int j = 2; j < 32; j += 2)
+                            a = fmaxf(a, fmaxf(__uint_as_float(z[j]), __uint_as_float(z[j + 1])));
+                        top = fmaxf(top, a * f[k]);
+                    }
+                    vtop = fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w));
+                } else {
+                    vtop = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t v = seen(k);
+                        uint32_t z[32];
+                        tmem_ld32(tS + 32 * k, z);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if ((v >> j) & 1u) {
+                                top = fmaxf(top, __uint_as_float(z[j]) * f[k]);
+                                vtop = fmaxf(vtop, vn[32 * k + j]);
+                            }
+                    }
+                }
+                if (__any_sync(0xffffffffu, top > m + kSlack || vtop > vs)) {
+                    const float up = fmaxf(m, top);
+                    float fac = ex2(m - up);
+                    m = up;
+                    l *= fac;
+                    if (vtop > vs) {
+                        // the power of two above, with room for a quarter more, in [2^-100, 2^127]
+                        const uint32_t p2 =
+                            (__float_as_uint(vtop * 1.25f) & 0x7f800000u) + 0x00800000u;
+                        const float nv = __uint_as_float(min(max(p2, 27u << 23), 254u << 23));
+                        fac *= vs / nv;
+                        vs = nv;
+                        vinv = kWeightScale / nv;
+                    }
+                    if (i >= 2) {                     // the sums so far, once they are complete
+                        wait(B_PV + me, c - 1);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t z[32];
+                            tmem_ld32(tO + 32 * k, z);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                z[j] = __float_as_uint(__uint_as_float(z[j]) * fac);
+                            tmem_st32(tO + 32 * k, z);
+                        }
+                    }
+                }
+                float ls[2] = {0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t z[32], w[16];
+                    tmem_ld32(tS + 32 * k, z);
+                    const uint32_t v = edge ? seen(k) : 0u;
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 nv = *reinterpret_cast<const float4 *>(vn + 32 * k + j);
+                        const float nn[4] = {nv.x, nv.y, nv.z, nv.w};
+                        float pw[4];
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            float x = fmaf(__uint_as_float(z[j + h]), f[k], -m);
+                            if (edge && !((v >> (j + h)) & 1u))
+                                x = -CUDART_INF_F;
+                            const float e = ex2(x);
+                            ls[h & 1] += e;
+                            pw[h] = e * (nn[h] * vinv);
+                            if (edge && !((v >> (j + h)) & 1u))
+                                pw[h] = 0.f;
+                        }
+                        w[j / 2] = half2_bits(pw[0], pw[1]);
+                        w[j / 2 + 1] = half2_bits(pw[2], pw[3]);
+                    }
+                    tmem_st16(tS + 16 * k, w);
+                }
+                l += ls[0] + ls[1];
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar(B_P + me));
+            }
+            // ---- the groups meet, and the piece goes to its slot ----
+            const int mine = (n + 1 - me) / 2;       // units of this group
+            if (mine > 0) {
+                wait(B_PV + me, used[me] + mine - 1);
+                tc_fence_after();
+            }
+            stat_s[me * 384 + r] = m;
+            stat_s[me * 384 + 128 + r] = l;
+            stat_s[me * 384 + 256 + r] = vs * (1.0f / kWeightScale);
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            const float om = stat_s[(me ^ 1) * 384 + r], ol = stat_s[(me ^ 1) * 384 + 128 + r];
+            const float mx = fmaxf(m, om);
+            const float fac = ex2(m - mx) * vs * (1.0f / kWeightScale);
+            float *buf = reinterpret_cast<float *>(sm + S::k_at);        // [element][row]
+            if (me == 1 && mine > 0) {
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t z[32];
+                    tmem_ld32(tO + 32 * k, z);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        buf[(32 * k + j) * 128 + r] = __uint_as_float(z[j]) * fac;
+                }
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (me == 0) {
+                const long long slot = (long long)b * ws.segments + seg + blockIdx.x;
+                if (r < nrows) {
+                    ws.stat[(slot * 2) * ws.rows + r] = mx;
+                    ws.stat[(slot * 2 + 1) * ws.rows + r] = l * ex2(m - mx) + ol * ex2(om - mx);
+                }
+                float *dst = ws.part + (slot * ws.rows + r) * D;
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t z[32];
+                    tmem_ld32(tO + 32 * k, z);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        float o = __uint_as_float(z[j]) * fac;
+                        if (n > 1)
+                            o += buf[(32 * k + j) * 128 + r];
+                        z[j] = __float_as_uint(o);
+                    }
+                    if (r < nrows)
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8)
+                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                                         ::"l"(dst + 32 * k + j), "r"(z[j]), "r"(z[j + 1]),
+                                         "r"(z[j + 2]), "r"(z[j + 3]), "r"(z[j + 4]),
+                                         "r"(z[j + 5]), "r"(z[j + 6]), "r"(z[j + 7]) : "memory");
+                }
+            }
+        } else if (warp < kSoftWarps + kDecWarps) {
+            // ---------------- decoders: a token's key row or value row a thread ----------------
+            const int t = threadIdx.x - 32 * kSoftWarps, w = t >> 7, row = t & 127;
+            const int *table = p.table + (long long)b * p.table_width;
+            const uint32_t col = lut_column<BITS>(lane);
+            constexpr int words = 4 * BITS;
+            uint32_t codes[words];
+            float norm = 0.f;
+            bool missing = false, valid = false;
+            auto load = [&](int i) {
+                const int tok = (tile0 + i) * kTokens + row;
+                valid = tok < total;
+                missing = false;
+                norm = 0.f;
+                int page = -1;
+                if (valid) {
+                    page = table[tok >> p.c.page_log2];
+                    missing = page < 0 || page >= p.c.pages;
+                    valid = !missing;
+                }
+                if (valid) {
+                    const long long at =
+                        (((long long)page * p.c.kv_heads + kvh) << p.c.page_log2) +
+                        (tok & ((1 << p.c.page_log2) - 1));
+                    load_words<words, 16>(codes, p.c.codes[w] + at * (D * BITS / 8));
+                    norm = __ldg(p.c.norms[w] + at);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < words; ++k)
+                        codes[k] = 0;
+                }
+            };
+            load(0);
+            for (int i = 0; i < n; ++i) {
+                const int st = i & 1;
+                const uint32_t c = used[st] + (i >> 1);
+                // the largest norm of the warp's 32 tokens (they are one group of scores)
+                float top = valid && norm < CUDART_INF_F ? norm : 0.f;
+#pragma unroll
+                for (int k = 16; k; k >>= 1)
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+                const uint32_t lost = __ballot_sync(0xffffffffu, missing);
+                uint32_t ex = (__float_as_uint(top) >> 23) & 255u;
+                ex = ex < 28u ? 28u : (ex > 253u ? 253u : ex);
+                const __half2 by = __float2half2_rn(norm * __uint_as_float((254u - ex) << 23));
+                if (c > 0)
+                    wait(B_PV + st, c - 1);
+                if (w == 0) {
+                    if (lane == 0) {
+                        kexp_s[4 * st + (warp & 3)] = __uint_as_float(ex << 23);
+                        bad_s[4 * st + (warp & 3)] = lost;
+                        if (lost)
+                            atomicOr(p.err, AT_ERR_PAGE);
+                    }
+                } else {
+                    vn_s[128 * st + row] = norm;
+                    if (lane == 0)
+                        vmax_s[4 * st + (warp & 3)] = top;
+                }
+                unsigned char *to = sm + (w == 0 ? S::k_at : S::v_at) + st * kTile;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    uint4 v;
+                    quad<BITS, false>(lut, codes, 2 * k, col, v.x, v.y);
+                    quad<BITS, false>(lut, codes, 2 * k + 1, col, v.z, v.w);
+                    if (w == 0) {
+                        __half2 *h = reinterpret_cast<__half2 *>(&v);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            h[j] = __hmul2(h[j], by);
+                    }
+                    *reinterpret_cast<uint4 *>(to + operand_at(row, k)) = v;
+                }
+                if (i + 1 < n)
+                    load(i + 1);
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar(B_FULL + st));
+            }
+        } else if (lane == 0) {
+            // ---------------- products ----------------
+            auto pv = [&](int i) {
+                const int st = i & 1;
+                wait(B_P + st, used[st] + (i >> 1));
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_ts(tmem + 256 + 128 * st, tmem + 128 * st + 8 * k,
+                           v_desc(base + S::v_at + st * kTile + k * 2048),
+                           idesc_f16(128, 128) | (1u << 16), i >= 2 || k != 0);
+                mma_commit(bar(B_PV + st));
+            };
+            for (int i = 0; i < n; ++i) {
+                const int st = i & 1;
+                wait(B_FULL + st, used[st] + (i >> 1));
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_ss(tmem + 128 * st,
+                           sw128_desc(base + S::q_at + (k >> 2) * 16384) + 2 * (k & 3),
+                           sw128_desc(base + S::k_at + st * kTile + (k >> 2) * 16384) + 2 * (k & 3),
+                           idesc_f16(128, 128), k != 0);
+                mma_commit(bar(B_S + st));
+                if (i > 0)
+                    pv(i - 1);
+            }
+            pv(n - 1);
+        }
+        __syncwarp();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        used[0] += (n + 1) / 2;
+        used[1] += n / 2;
+        ++pieces;
+        u += n;
+    }
+    // nothing of the products may be under way when the tensor memory goes back
+    if (threadIdx.x == 32 * (kSoftWarps + kDecWarps)) {
+        mma_commit(bar(B_END));
+        wait(B_END, 0);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kSoftWarps + kDecWarps)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+}
+
+template <class E, int BITS>
+cudaError_t launch_wide(const KvAttendParams &p, const KvAttendSpace &ws, cudaStream_t st) {
+    auto *kern = attend_wide<E, BITS>;
+    static PerDevice ready;
+    const cudaError_t e = ready.once([&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    wide::Smem::bytes);
+    });
+    if (e != cudaSuccess)
+        return e;
+    return launch_pdl(kern, dim3(ws.most), dim3(wide::kThreads), (size_t)wide::Smem::bytes, st, p,
+                      static_cast<const uint4 *>(p.r_img), ws);
+}
+
+}  // namespace attend
+}  // namespace oq

@@ -79,6 +79,9 @@ void build_kv_lut(oq_codebook *cb);      // oq_cache.cpp
 // The current device, checked once to be sm_100.
 int current_device(int *dev_out, DeviceInfo **info_out);
 
+// The device's stream-ordered memory pool (created once; nullptr and *rc set on failure).
+cudaMemPool_t device_pool(int dev, DeviceInfo *di, int *rc);
+
 // A handle's table on the current device, copied there at its first use.
 template <class T>
 int upload(std::mutex &mu, uint32_t **slot, const std::vector<T> &host, const char *what) {

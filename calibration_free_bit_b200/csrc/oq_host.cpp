@@ -592,6 +592,11 @@ int quantize_rows(const oq_rpbh *r, const oq_codebook *cb, const void *x, int dt
     return OQ_OK;
 }
 
+}  // namespace
+
+namespace oq {
+namespace host {
+
 cudaMemPool_t device_pool(int dev, DeviceInfo *di, int *rc) {
     std::lock_guard<std::mutex> lk(g_dev_mu);
     if (di->pool)
@@ -611,6 +616,11 @@ cudaMemPool_t device_pool(int dev, DeviceInfo *di, int *rc) {
     di->pool = pool;
     return pool;
 }
+
+}  // namespace host
+}  // namespace oq
+
+namespace {
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
