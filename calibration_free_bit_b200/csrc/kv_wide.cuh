@@ -71,6 +71,12 @@ template <bool BF16> __device__ __forceinline__ uint32_t idesc_q() {
     return idesc_f16(128, 128) | (BF16 ? (1u << 7) | (1u << 10) : 0u);
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 struct Work {
     long long u0, u1, before;
     int b;
@@ -256,11 +262,9 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                 wait(B_FULL + me, c);                 // the norms, exponents and lost tokens
                 wait(B_S + me, c);
                 tc_fence_after();
-                const float4 ke = *reinterpret_cast<const float4 *>(kexp_s + 4 * me);
+                const float *ke = kexp_s + 4 * me, *vn = vn_s + 128 * me;
                 const float4 vm = *reinterpret_cast<const float4 *>(vmax_s + 4 * me);
                 const uint4 bad = *reinterpret_cast<const uint4 *>(bad_s + 4 * me);
-                const float f[4] = {qs * ke.x, qs * ke.y, qs * ke.z, qs * ke.w};
-                const uint32_t out[4] = {bad.x, bad.y, bad.z, bad.w};
                 const bool edge = tok + kTokens > s.prefix || (bad.x | bad.y | bad.z | bad.w);
                 // tokens of group k that this row sees
                 auto seen = [&](int k) -> uint32_t {
@@ -272,33 +276,38 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                         v = (uint32_t)(mask << -first) | ((1u << -first) - 1u);
                     else
                         v = first < 64 ? (uint32_t)(mask >> first) : 0u;
-                    return v & ~out[k];
+                    return v & ~bad_s[4 * me + k];
                 };
-                const float *vn = vn_s + 128 * me;
+                // the row's largest score and the largest value norm that it sees
                 float top = -CUDART_INF_F, vtop;
                 if (!edge) {
-#pragma unroll
+#pragma unroll 1
                     for (int k = 0; k < 4; ++k) {
                         uint32_t z[32];
                         tmem_ld32(tS + 32 * k, z);
-                        float a = fmaxf(__uint_as_float(z[0]), __uint_as_float(z[1]));
+                        float a[2];
 #pragma unroll
-                        for (int j = 2; j < 32; j += 2)
-                            a = fmaxf(a, fmaxf(__uint_as_float(z[j]), __uint_as_float(z[j + 1])));
-                        top = fmaxf(top, a * f[k]);
+                        for (int h = 0; h < 2; ++h) {
+                            a[h] = fmaxf(__uint_as_float(z[h]), __uint_as_float(z[2 + h]));
+#pragma unroll
+                            for (int j = 4 + h; j < 32; j += 4)
+                                a[h] = max3(a[h], __uint_as_float(z[j]), __uint_as_float(z[j + 2]));
+                        }
+                        top = fmaxf(top, fmaxf(a[0], a[1]) * (qs * ke[k]));
                     }
                     vtop = fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w));
                 } else {
                     vtop = 0.f;
-#pragma unroll
+#pragma unroll 1
                     for (int k = 0; k < 4; ++k) {
                         const uint32_t v = seen(k);
+                        const float f = qs * ke[k];
                         uint32_t z[32];
                         tmem_ld32(tS + 32 * k, z);
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if ((v >> j) & 1u) {
-                                top = fmaxf(top, __uint_as_float(z[j]) * f[k]);
+                                top = fmaxf(top, __uint_as_float(z[j]) * f);
                                 vtop = fmaxf(vtop, vn[32 * k + j]);
                             }
                     }
@@ -331,34 +340,58 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                         }
                     }
                 }
-                float ls[2] = {0.f, 0.f};
+                if (!edge) {
+                    float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    const float2 mm = make_float2(-m, -m), vi = make_float2(vinv, vinv);
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t z[32], w[16];
+                        tmem_ld32(tS + 32 * k, z);
+                        const float f = qs * ke[k];
+                        const float2 ff = make_float2(f, f);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t z[32], w[16];
-                    tmem_ld32(tS + 32 * k, z);
-                    const uint32_t v = edge ? seen(k) : 0u;
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 nv = *reinterpret_cast<const float4 *>(vn + 32 * k + j);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 nv = *reinterpret_cast<const float4 *>(vn + 32 * k + j);
-                        const float nn[4] = {nv.x, nv.y, nv.z, nv.w};
-                        float pw[4];
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            float x = fmaf(__uint_as_float(z[j + h]), f[k], -m);
-                            if (edge && !((v >> (j + h)) & 1u))
-                                x = -CUDART_INF_F;
-                            const float e = ex2(x);
-                            ls[h & 1] += e;
-                            pw[h] = e * (nn[h] * vinv);
-                            if (edge && !((v >> (j + h)) & 1u))
-                                pw[h] = 0.f;
+                            for (int h = 0; h < 2; ++h) {
+                                const float2 x = __ffma2_rn(
+                                    make_float2(__uint_as_float(z[j + 2 * h]),
+                                                __uint_as_float(z[j + 2 * h + 1])), ff, mm);
+                                const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                                ls[h] = __fadd2_rn(ls[h], e);
+                                const float2 n2 = h ? make_float2(nv.z, nv.w)
+                                                    : make_float2(nv.x, nv.y);
+                                const float2 pw = __fmul2_rn(e, __fmul2_rn(n2, vi));
+                                w[j / 2 + h] = half2_bits(pw.x, pw.y);
+                            }
                         }
-                        w[j / 2] = half2_bits(pw[0], pw[1]);
-                        w[j / 2 + 1] = half2_bits(pw[2], pw[3]);
+                        tmem_st16(tS + 16 * k, w);
                     }
-                    tmem_st16(tS + 16 * k, w);
+                    l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+                } else {
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t z[32], w[16];
+                        tmem_ld32(tS + 32 * k, z);
+                        const uint32_t v = seen(k);
+                        const float f = qs * ke[k];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            float pw[2];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                pw[h] = 0.f;
+                                if ((v >> (j + h)) & 1u) {
+                                    const float e = ex2(fmaf(__uint_as_float(z[j + h]), f, -m));
+                                    l += e;
+                                    pw[h] = e * (vn[32 * k + j + h] * vinv);
+                                }
+                            }
+                            w[j / 2] = half2_bits(pw[0], pw[1]);
+                        }
+                        tmem_st16(tS + 16 * k, w);
+                    }
                 }
-                l += ls[0] + ls[1];
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
