@@ -35,7 +35,7 @@ namespace wide {
 
 constexpr int kRows = 128, kTokens = 128, D = 128;
 constexpr int kSoftWarps = 8, kDecWarps = 8;
-constexpr int kThreads = 32 * (kSoftWarps + kDecWarps + 1);
+constexpr int kThreads = 32 * (kSoftWarps + kDecWarps + 2);       // and the two that issue products
 constexpr int kTile = 128 * D * 2;                    // an operand: 32 KB
 
 struct Smem {
@@ -54,7 +54,7 @@ struct Smem {
     static constexpr int bars_at = work_at + 64;
     static constexpr int bytes = bars_at + 128 + 1024;
 };
-enum { B_FULL = 0, B_S = 2, B_P = 4, B_PV = 6, B_Q = 8, B_END = 9 };
+enum { B_K = 0, B_V = 2, B_S = 4, B_P = 6, B_PV = 8, B_Q = 10, B_END = 11 };   // two each to B_Q
 
 __device__ __forceinline__ uint32_t operand_at(int r, int ch) {
     return (uint32_t)(ch >> 3) * 16384u + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
@@ -94,8 +94,8 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
     unsigned char *sm = raw + (base - smem_u32(raw));
     const uint32_t bars = base + S::bars_at;
     auto bar = [&](int i) { return bars + 8u * i; };
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + S::bars_at + 96);
-    volatile int *gone = reinterpret_cast<volatile int *>(sm + S::bars_at + 100);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + S::bars_at + 112);
+    volatile int *gone = reinterpret_cast<volatile int *>(sm + S::bars_at + 116);
     Work *work = reinterpret_cast<Work *>(sm + S::work_at);
     float *vn_s = reinterpret_cast<float *>(sm + S::vn_at);
     float *kexp_s = reinterpret_cast<float *>(sm + S::kexp_at);
@@ -111,7 +111,8 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
     fill_lut<BITS, false>(lut, p.lut);
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(B_FULL + i), kDecWarps);
+            mbar_init(bar(B_K + i), kDecWarps / 2);
+            mbar_init(bar(B_V + i), kDecWarps / 2);
             mbar_init(bar(B_S + i), 1);
             mbar_init(bar(B_P + i), 4);
             mbar_init(bar(B_PV + i), 1);
@@ -259,10 +260,11 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
             for (int i = me; i < n; i += 2) {
                 const uint32_t c = used[me] + (i >> 1);
                 const int tok = (tile0 + i) * kTokens;
-                wait(B_FULL + me, c);                 // the norms, exponents and lost tokens
+                wait(B_K + me, c);                    // exponents and lost tokens
                 wait(B_S + me, c);
                 tc_fence_after();
                 const float *ke = kexp_s + 4 * me, *vn = vn_s + 128 * me;
+                wait(B_V + me, c);                    // value norms
                 const float4 vm = *reinterpret_cast<const float4 *>(vmax_s + 4 * me);
                 const uint4 bad = *reinterpret_cast<const uint4 *>(bad_s + 4 * me);
                 const bool edge = tok + kTokens > s.prefix || (bad.x | bad.y | bad.z | bad.w);
@@ -456,36 +458,56 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
             const int *table = p.table + (long long)b * p.table_width;
             const uint32_t col = lut_column<BITS>(lane);
             constexpr int words = 4 * BITS;
-            uint32_t codes[words];
-            float norm = 0.f;
-            bool missing = false, valid = false;
-            auto load = [&](int i) {
+            // One unit ahead in registers where they hold two rows, and two ahead on the way to
+            // the L2; a page's index is known three ahead, so that no load waits for another.
+            constexpr bool ahead = BITS <= 4;
+            struct Row {
+                uint32_t codes[words];
+                float norm;
+                bool missing, valid;
+            };
+            auto page_of = [&](int i) -> int {
                 const int tok = (tile0 + i) * kTokens + row;
-                valid = tok < total;
-                missing = false;
-                norm = 0.f;
-                int page = -1;
-                if (valid) {
-                    page = table[tok >> p.c.page_log2];
-                    missing = page < 0 || page >= p.c.pages;
-                    valid = !missing;
+                return i < n && tok < total ? __ldg(table + (tok >> p.c.page_log2)) : -1;
+            };
+            auto row_of = [&](int i, int page) -> long long {
+                return (((long long)page * p.c.kv_heads + kvh) << p.c.page_log2) +
+                       (((tile0 + i) * kTokens + row) & ((1 << p.c.page_log2) - 1));
+            };
+            auto fetch = [&](int i, int page) {
+                if (page >= 0 && page < p.c.pages) {
+                    const uint8_t *at = p.c.codes[w] + row_of(i, page) * (D * BITS / 8);
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
                 }
-                if (valid) {
-                    const long long at =
-                        (((long long)page * p.c.kv_heads + kvh) << p.c.page_log2) +
-                        (tok & ((1 << p.c.page_log2) - 1));
-                    load_words<words, 16>(codes, p.c.codes[w] + at * (D * BITS / 8));
-                    norm = __ldg(p.c.norms[w] + at);
+            };
+            auto load = [&](Row &to, int i, int page) {
+                const bool real = i < n && (tile0 + i) * kTokens + row < total;
+                to.valid = page >= 0 && page < p.c.pages;
+                to.missing = real && !to.valid;
+                to.norm = 0.f;
+                if (to.valid) {
+                    const long long at = row_of(i, page);
+                    load_words<words, 16>(to.codes, p.c.codes[w] + at * (D * BITS / 8));
+                    to.norm = __ldg(p.c.norms[w] + at);
                 } else {
 #pragma unroll
                     for (int k = 0; k < words; ++k)
-                        codes[k] = 0;
+                        to.codes[k] = 0;
                 }
             };
-            load(0);
+            Row cur, nxt;
+            int page1 = page_of(1), page2 = page_of(2);
+            load(cur, 0, page_of(0));
+            fetch(1, page1);
             for (int i = 0; i < n; ++i) {
                 const int st = i & 1;
                 const uint32_t c = used[st] + (i >> 1);
+                if constexpr (ahead)
+                    load(nxt, i + 1, page1);
+                fetch(i + 2, page2);
+                const int page3 = page_of(i + 3);
+                const float norm = cur.norm;
+                const bool valid = cur.valid, missing = cur.missing;
                 // the largest norm of the warp's 32 tokens (they are one group of scores)
                 float top = valid && norm < CUDART_INF_F ? norm : 0.f;
 #pragma unroll
@@ -495,9 +517,32 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                 uint32_t ex = (__float_as_uint(top) >> 23) & 255u;
                 ex = ex < 28u ? 28u : (ex > 253u ? 253u : ex);
                 const __half2 by = __float2half2_rn(norm * __uint_as_float((254u - ex) << 23));
+                // K's stage is free after S, V's and the norms' after P V
                 if (c > 0)
-                    wait(B_PV + st, c - 1);
+                    wait((w == 0 ? B_S : B_PV) + st, c - 1);
+                unsigned char *to = sm + (w == 0 ? S::k_at : S::v_at) + st * kTile;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    uint4 v;
+                    quad<BITS, false>(lut, cur.codes, 2 * k, col, v.x, v.y);
+                    quad<BITS, false>(lut, cur.codes, 2 * k + 1, col, v.z, v.w);
+                    if (w == 0) {
+                        __half2 *h = reinterpret_cast<__half2 *>(&v);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            h[j] = __hmul2(h[j], by);
+                    }
+                    *reinterpret_cast<uint4 *>(to + operand_at(row, k)) = v;
+                }
+                if constexpr (ahead)
+                    cur = nxt;
+                else
+                    load(cur, i + 1, page1);
+                page1 = page2;
+                page2 = page3;
                 if (w == 0) {
+                    if (c > 0)
+                        wait(B_PV + st, c - 1);
                     if (lane == 0) {
                         kexp_s[4 * st + (warp & 3)] = __uint_as_float(ex << 23);
                         bad_s[4 * st + (warp & 3)] = lost;
@@ -509,43 +554,19 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                     if (lane == 0)
                         vmax_s[4 * st + (warp & 3)] = top;
                 }
-                unsigned char *to = sm + (w == 0 ? S::k_at : S::v_at) + st * kTile;
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    uint4 v;
-                    quad<BITS, false>(lut, codes, 2 * k, col, v.x, v.y);
-                    quad<BITS, false>(lut, codes, 2 * k + 1, col, v.z, v.w);
-                    if (w == 0) {
-                        __half2 *h = reinterpret_cast<__half2 *>(&v);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            h[j] = __hmul2(h[j], by);
-                    }
-                    *reinterpret_cast<uint4 *>(to + operand_at(row, k)) = v;
-                }
-                if (i + 1 < n)
-                    load(i + 1);
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(bar(B_FULL + st));
+                    mbar_arrive(bar((w == 0 ? B_K : B_V) + st));
             }
-        } else if (lane == 0) {
-            // ---------------- products ----------------
-            auto pv = [&](int i) {
-                const int st = i & 1;
-                wait(B_P + st, used[st] + (i >> 1));
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_ts(tmem + 256 + 128 * st, tmem + 128 * st + 8 * k,
-                           v_desc(base + S::v_at + st * kTile + k * 2048),
-                           idesc_f16(128, 128) | (1u << 16), i >= 2 || k != 0);
-                mma_commit(bar(B_PV + st));
-            };
+        } else if (lane == 0 && warp == kSoftWarps + kDecWarps) {
+            // ---------------- S = Q K^T ----------------
             for (int i = 0; i < n; ++i) {
                 const int st = i & 1;
-                wait(B_FULL + st, used[st] + (i >> 1));
+                const uint32_t c = used[st] + (i >> 1);
+                wait(B_K + st, c);
+                if (c > 0)
+                    wait(B_PV + st, c - 1);           // the weights lie where S goes
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
@@ -554,10 +575,22 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                            sw128_desc(base + S::k_at + st * kTile + (k >> 2) * 16384) + 2 * (k & 3),
                            idesc_f16(128, 128), k != 0);
                 mma_commit(bar(B_S + st));
-                if (i > 0)
-                    pv(i - 1);
             }
-            pv(n - 1);
+        } else if (lane == 0) {
+            // ---------------- O += P V ----------------
+            for (int i = 0; i < n; ++i) {
+                const int st = i & 1;
+                const uint32_t c = used[st] + (i >> 1);
+                wait(B_V + st, c);
+                wait(B_P + st, c);
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_ts(tmem + 256 + 128 * st, tmem + 128 * st + 8 * k,
+                           v_desc(base + S::v_at + st * kTile + k * 2048),
+                           idesc_f16(128, 128) | (1u << 16), i >= 2 || k != 0);
+                mma_commit(bar(B_PV + st));
+            }
         }
         __syncwarp();
         tc_fence_before();
