@@ -361,12 +361,19 @@ kv_read_tc(const KvReadParams p, const uint4 *r_img, const int tiles) {
     for (; tile < tiles; tile += stride) {
         bulk_wait_read<0>();                              // the last tile's rows have left
         group_sync(1 + grp, G::group_threads);
+        // four chunks of 8 elements at a time, so that their lookups are under way together (the
+        // compiler does not move a load over a store to the operand)
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {                    // 8 elements a step
-            uint4 v;
-            quad<BITS, false>(lut, codes, 2 * k, col, v.x, v.y);
-            quad<BITS, false>(lut, codes, 2 * k + 1, col, v.z, v.w);
-            *reinterpret_cast<uint4 *>(a_sm + operand_at(row, part * 16 + k, 128)) = v;
+        for (int k = 0; k < 16; k += 4) {
+            uint4 v[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                quad<BITS, false>(lut, codes, 2 * (k + h), col, v[h].x, v[h].y);
+                quad<BITS, false>(lut, codes, 2 * (k + h) + 1, col, v[h].z, v[h].w);
+            }
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                *reinterpret_cast<uint4 *>(a_sm + operand_at(row, part * 16 + k + h, 128)) = v[h];
         }
         fence_async_smem();
         tc_fence_before();

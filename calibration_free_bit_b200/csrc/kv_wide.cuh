@@ -34,8 +34,15 @@ using kvops::prmt;
 namespace wide {
 
 constexpr int kRows = 128, kTokens = 128, D = 128;
-constexpr int kSoftWarps = 8, kDecWarps = 8;
-constexpr int kThreads = 32 * (kSoftWarps + kDecWarps + 2);       // and the two that issue products
+// Warps: two softmax groups, eight decoders each for keys and values, and a group of four of which
+// two issue products (the others leave).
+constexpr int kSoftWarps = 8, kDecWarps = 16;
+constexpr int kThreads = 32 * (kSoftWarps + kDecWarps + 4);
+constexpr int kWorking = 32 * (kSoftWarps + kDecWarps + 2);       // that meet at barrier 0
+// Registers a thread: 72 at the launch, 896 threads; 112 + 56 + 24 leave 64 x 128 x 8 of them free
+constexpr int kSoftRegs = 112, kDecRegs = 56, kIssueRegs = 24;
+static_assert(32 * (kSoftWarps * kSoftRegs + kDecWarps * kDecRegs + 4 * kIssueRegs) <=
+                  kThreads * 72, "registers: no more than the launch's");
 constexpr int kTile = 128 * D * 2;                    // an operand: 32 KB
 
 struct Smem {
@@ -54,7 +61,7 @@ struct Smem {
     static constexpr int bars_at = work_at + 64;
     static constexpr int bytes = bars_at + 128 + 1024;
 };
-enum { B_K = 0, B_V = 2, B_S = 4, B_P = 6, B_PV = 8, B_Q = 10, B_END = 11 };   // two each to B_Q
+enum { B_K = 0, B_V = 2, B_S = 4, B_P = 6, B_PV = 8, B_Q = 10 };   // two each to B_Q
 
 __device__ __forceinline__ uint32_t operand_at(int r, int ch) {
     return (uint32_t)(ch >> 3) * 16384u + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
@@ -118,7 +125,6 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
             mbar_init(bar(B_PV + i), 1);
         }
         mbar_init(bar(B_Q), 1);
-        mbar_init(bar(B_END), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         *gone = 0;
     }
@@ -153,104 +159,103 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
         }
     };
 
-    long long u = work->u0, before = work->before;
-    const long long u1 = work->u1;
-    int b = work->b;
-    uint32_t used[2] = {0, 0}, pieces = 0;           // units so far of either group, pieces
-    while (u < u1) {
+    // The pieces of this worker's range, one after another, as every warp sees them.
+    struct Piece {
         Seq s;
-        Units un = units_of<kTokens, kRows>(p, b, &s, false);
-        if (u >= before + (long long)un.tiles * un.segments) {
-            before += (long long)un.tiles * un.segments;
-            ++b;
-            continue;
+        int b, seg, tile0, n, kvh, row_base, nrows, total;
+    };
+    struct Walk {
+        long long u, u1, before;
+        int b;
+    };
+    auto next = [&](Walk &w, Piece &q) -> bool {
+        while (w.u < w.u1) {
+            const Units un = units_of<kTokens, kRows>(p, w.b, &q.s, false);
+            const long long all = (long long)un.tiles * un.segments;
+            if (w.u >= w.before + all) {
+                w.before += all;
+                ++w.b;
+                continue;
+            }
+            q.b = w.b;
+            q.seg = (int)((w.u - w.before) / un.tiles);
+            q.tile0 = (int)((w.u - w.before) - (long long)q.seg * un.tiles);
+            q.n = (int)min((long long)(un.tiles - q.tile0), w.u1 - w.u);
+            const int row_tiles = un.segments / p.c.kv_heads;
+            q.kvh = q.seg / row_tiles;
+            q.row_base = (q.seg - q.kvh * row_tiles) * kRows;
+            q.nrows = min(kRows, q.s.nodes * p.group - q.row_base);
+            q.total = q.s.prefix + q.s.nodes;
+            w.u += q.n;
+            return true;
         }
-        const int seg = (int)((u - before) / un.tiles);
-        const int tile0 = (int)((u - before) - (long long)seg * un.tiles);
-        const int n = (int)min((long long)(un.tiles - tile0), u1 - u);
-        const int row_tiles = un.segments / p.c.kv_heads;
-        const int kvh = seg / row_tiles, row_base = (seg - kvh * row_tiles) * kRows;
-        const int nrows = min(kRows, s.nodes * p.group - row_base);
-        const int total = s.prefix + s.nodes;
+        return false;
+    };
+    auto meet = [&] {
+        __syncwarp();
+        tc_fence_before();
+        asm volatile("bar.sync 0, %0;" ::"n"(kWorking) : "memory");
+        tc_fence_after();
+    };
+    Walk walk = {work->u0, work->u1, work->before, work->b};
+    Piece q;
+    uint32_t used[2] = {0, 0};                       // units so far of either group
 
-        // ---- queries: raw rows to V's first stage, the rotation to K's ----
-        if (warp < kSoftWarps) {
+    if (warp < kSoftWarps) {
+        // ---------------- softmax: group `me` has units me, me + 2, ... ----------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        uint32_t pieces = 0;
+        while (next(walk, q)) {
+            const Seq &s = q.s;
+            const int n = q.n, tile0 = q.tile0, nrows = q.nrows;
+            // the rotation to K's first stage (the raw queries go to V's)
             for (int i = threadIdx.x; i < kTile / 16; i += 32 * kSoftWarps)
                 reinterpret_cast<uint4 *>(sm + S::k_at)[i] = __ldg(r_img + i);
             if (threadIdx.x < kRows) {
-                const int node = (row_base + threadIdx.x) / p.group;
+                const int node = (q.row_base + threadIdx.x) / p.group;
                 mask_s[threadIdx.x] =
                     threadIdx.x >= nrows ? 0ull
                     : p.mask ? (unsigned long long)p.mask[s.row0 + node] &
                                    (s.nodes >= 64 ? ~0ull : (1ull << s.nodes) - 1ull)
                              : (2ull << node) - 1ull;
             }
-        } else if (warp < kSoftWarps + kDecWarps) {
-            const int t = threadIdx.x - 32 * kSoftWarps, ch = t & 15;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = i * 16 + (t >> 4);
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (r < nrows) {
-                    const int node = (row_base + r) / p.group, e = row_base + r - node * p.group;
-                    v = *reinterpret_cast<const uint4 *>(
-                        static_cast<const E *>(p.q) + (s.row0 + node) * p.q_stride +
-                        (kvh * p.group + e) * D + ch * 8);
-                }
-                *reinterpret_cast<uint4 *>(sm + S::v_at + operand_at(r, ch)) = v;
-            }
-        }
-        fence_async_smem();
-        tc_fence_before();
-        __syncthreads();
-        if (threadIdx.x == 32 * (kSoftWarps + kDecWarps)) {
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                mma_ss(tmem, sw128_desc(base + S::v_at + (k >> 2) * 16384) + 2 * (k & 3),
-                       sw128_desc(base + S::k_at + (k >> 2) * 16384) + 2 * (k & 3),
-                       idesc_q<std::is_same<E, __nv_bfloat16>::value>(), k != 0);
-            mma_commit(bar(B_Q));
-        }
-        if (warp < 4) {
-            wait(B_Q, pieces);
-            tc_fence_after();
-            const uint32_t mine = tmem + ((uint32_t)(32 * warp) << 16);
-            float big = 0.f;
-#pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-                uint32_t z[32];
-                tmem_ld32(mine + 32 * k, z);
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    big = fmaxf(big, fabsf(__uint_as_float(z[i])));
-            }
-            // 2^e <= big < 2^(e+1); values over 2^e stay below 2 (2^e and its inverse are normal)
-            uint32_t ex = (__float_as_uint(big) >> 23) & 255u;
-            ex = ex < 1u ? 1u : (ex > 253u ? 253u : ex);
-            const float up = __uint_as_float(ex << 23), down = __uint_as_float((254u - ex) << 23);
-#pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-                uint32_t z[32];
-                tmem_ld32(mine + 32 * k, z);
-#pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                    auto f = [&](int j) { return __uint_as_float(z[i + j]) * down; };
-                    *reinterpret_cast<uint4 *>(sm + S::q_at +
-                                               operand_at(threadIdx.x, 4 * k + i / 8)) =
-                        make_uint4(half2_bits(f(0), f(1)), half2_bits(f(2), f(3)),
-                                   half2_bits(f(4), f(5)), half2_bits(f(6), f(7)));
-                }
-            }
-            qs_s[threadIdx.x] = up * p.qk_scale;
             fence_async_smem();
-        }
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-
-        if (warp < kSoftWarps) {
-            // ---------------- softmax: group `me` has units me, me + 2, ... ----------------
+            meet();
+            if (warp < 4) {
+                // rotated queries, fp16 over a power of two a row
+                wait(B_Q, pieces);
+                tc_fence_after();
+                const uint32_t mine = tmem + ((uint32_t)(32 * warp) << 16);
+                float big = 0.f;
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t z[32];
+                    tmem_ld32(mine + 32 * k, z);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        big = fmaxf(big, fabsf(__uint_as_float(z[i])));
+                }
+                // 2^e <= big < 2^(e+1); values over 2^e stay below 2 (2^e and its inverse are normal)
+                uint32_t ex = (__float_as_uint(big) >> 23) & 255u;
+                ex = ex < 1u ? 1u : (ex > 253u ? 253u : ex);
+                const float up = __uint_as_float(ex << 23), down = __uint_as_float((254u - ex) << 23);
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t z[32];
+                    tmem_ld32(mine + 32 * k, z);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        auto f = [&](int j) { return __uint_as_float(z[i + j]) * down; };
+                        *reinterpret_cast<uint4 *>(sm + S::q_at +
+                                                   operand_at(threadIdx.x, 4 * k + i / 8)) =
+                            make_uint4(half2_bits(f(0), f(1)), half2_bits(f(2), f(3)),
+                                       half2_bits(f(4), f(5)), half2_bits(f(6), f(7)));
+                    }
+                }
+                qs_s[threadIdx.x] = up * p.qk_scale;
+                fence_async_smem();
+            }
+            meet();
             const int me = warp >> 2, r = threadIdx.x & 127;
             const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
             const uint32_t tS = tmem + lanes + 128 * me, tO = tmem + lanes + 256 + 128 * me;
@@ -426,7 +431,7 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
             }
             asm volatile("bar.sync 1, 256;" ::: "memory");
             if (me == 0) {
-                const long long slot = (long long)b * ws.segments + seg + blockIdx.x;
+                const long long slot = (long long)q.b * ws.segments + q.seg + blockIdx.x;
                 if (r < nrows) {
                     ws.stat[(slot * 2) * ws.rows + r] = mx;
                     ws.stat[(slot * 2 + 1) * ws.rows + r] = l * ex2(m - mx) + ol * ex2(om - mx);
@@ -452,15 +457,39 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                                          "r"(z[j + 5]), "r"(z[j + 6]), "r"(z[j + 7]) : "memory");
                 }
             }
-        } else if (warp < kSoftWarps + kDecWarps) {
-            // ---------------- decoders: a token's key row or value row a thread ----------------
-            const int t = threadIdx.x - 32 * kSoftWarps, w = t >> 7, row = t & 127;
+            meet();
+            used[0] += (n + 1) / 2;
+            used[1] += n / 2;
+            ++pieces;
+        }
+    } else if (warp < kSoftWarps + kDecWarps) {
+        // ---------------- decoders: half a token's key row or value row a thread ----------------
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDecRegs));
+        const int dt = threadIdx.x - 32 * kSoftWarps;
+        while (next(walk, q)) {
+            const int n = q.n, tile0 = q.tile0, total = q.total, kvh = q.kvh, b = q.b;
+            const int ch = dt & 15;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = i * 32 + (dt >> 4);
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (r < q.nrows) {
+                    const int node = (q.row_base + r) / p.group, e = q.row_base + r - node * p.group;
+                    v = *reinterpret_cast<const uint4 *>(
+                        static_cast<const E *>(p.q) + (q.s.row0 + node) * p.q_stride +
+                        (kvh * p.group + e) * D + ch * 8);
+                }
+                *reinterpret_cast<uint4 *>(sm + S::v_at + operand_at(r, ch)) = v;
+            }
+            fence_async_smem();
+            meet();
+            meet();
+            const int w = dt >> 8, part = (dt >> 7) & 1, row = dt & 127;
             const int *table = p.table + (long long)b * p.table_width;
             const uint32_t col = lut_column<BITS>(lane);
-            constexpr int words = 4 * BITS;
-            // One unit ahead in registers where they hold two rows, and two ahead on the way to
-            // the L2; a page's index is known three ahead, so that no load waits for another.
-            constexpr bool ahead = BITS <= 4;
+            constexpr int words = 2 * BITS;               // 64 codes
+            // One unit ahead in registers and two ahead on the way to the L2; a page's index is
+            // known three ahead, so that no load waits for another.
             struct Row {
                 uint32_t codes[words];
                 float norm;
@@ -476,7 +505,7 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
             };
             auto fetch = [&](int i, int page) {
                 if (page >= 0 && page < p.c.pages) {
-                    const uint8_t *at = p.c.codes[w] + row_of(i, page) * (D * BITS / 8);
+                    const uint8_t *at = p.c.codes[w] + row_of(i, page) * (D * BITS / 8) + part * (8 * BITS);
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
                 }
             };
@@ -487,7 +516,8 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                 to.norm = 0.f;
                 if (to.valid) {
                     const long long at = row_of(i, page);
-                    load_words<words, 16>(to.codes, p.c.codes[w] + at * (D * BITS / 8));
+                    load_words<words, 8 * BITS>(
+                        to.codes, p.c.codes[w] + at * (D * BITS / 8) + part * (8 * BITS));
                     to.norm = __ldg(p.c.norms[w] + at);
                 } else {
 #pragma unroll
@@ -502,8 +532,7 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
             for (int i = 0; i < n; ++i) {
                 const int st = i & 1;
                 const uint32_t c = used[st] + (i >> 1);
-                if constexpr (ahead)
-                    load(nxt, i + 1, page1);
+                load(nxt, i + 1, page1);
                 fetch(i + 2, page2);
                 const int page3 = page_of(i + 3);
                 const float norm = cur.norm;
@@ -521,35 +550,42 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                 if (c > 0)
                     wait((w == 0 ? B_S : B_PV) + st, c - 1);
                 unsigned char *to = sm + (w == 0 ? S::k_at : S::v_at) + st * kTile;
+                // four chunks of 8 elements at a time, so that their lookups are under way together
+                // (the compiler does not move a load over a store to the operand)
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    uint4 v;
-                    quad<BITS, false>(lut, cur.codes, 2 * k, col, v.x, v.y);
-                    quad<BITS, false>(lut, cur.codes, 2 * k + 1, col, v.z, v.w);
-                    if (w == 0) {
-                        __half2 *h = reinterpret_cast<__half2 *>(&v);
+                for (int k = 0; k < 8; k += 4) {
+                    uint4 v[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            h[j] = __hmul2(h[j], by);
+                    for (int h = 0; h < 4; ++h) {
+                        quad<BITS, false>(lut, cur.codes, 2 * (k + h), col, v[h].x, v[h].y);
+                        quad<BITS, false>(lut, cur.codes, 2 * (k + h) + 1, col, v[h].z, v[h].w);
                     }
-                    *reinterpret_cast<uint4 *>(to + operand_at(row, k)) = v;
+                    if (w == 0) {
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            __half2 *x = reinterpret_cast<__half2 *>(&v[h]);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                x[j] = __hmul2(x[j], by);
+                        }
+                    }
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+                        *reinterpret_cast<uint4 *>(to + operand_at(row, 8 * part + k + h)) = v[h];
                 }
-                if constexpr (ahead)
-                    cur = nxt;
-                else
-                    load(cur, i + 1, page1);
+                cur = nxt;
                 page1 = page2;
                 page2 = page3;
                 if (w == 0) {
                     if (c > 0)
                         wait(B_PV + st, c - 1);
-                    if (lane == 0) {
+                    if (part == 0 && lane == 0) {
                         kexp_s[4 * st + (warp & 3)] = __uint_as_float(ex << 23);
                         bad_s[4 * st + (warp & 3)] = lost;
                         if (lost)
                             atomicOr(p.err, AT_ERR_PAGE);
                     }
-                } else {
+                } else if (part == 0) {
                     vn_s[128 * st + row] = norm;
                     if (lane == 0)
                         vmax_s[4 * st + (warp & 3)] = top;
@@ -559,56 +595,67 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                 if (lane == 0)
                     mbar_arrive(bar((w == 0 ? B_K : B_V) + st));
             }
-        } else if (lane == 0 && warp == kSoftWarps + kDecWarps) {
-            // ---------------- S = Q K^T ----------------
-            for (int i = 0; i < n; ++i) {
-                const int st = i & 1;
-                const uint32_t c = used[st] + (i >> 1);
-                wait(B_K + st, c);
-                if (c > 0)
-                    wait(B_PV + st, c - 1);           // the weights lie where S goes
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_ss(tmem + 128 * st,
-                           sw128_desc(base + S::q_at + (k >> 2) * 16384) + 2 * (k & 3),
-                           sw128_desc(base + S::k_at + st * kTile + (k >> 2) * 16384) + 2 * (k & 3),
-                           idesc_f16(128, 128), k != 0);
-                mma_commit(bar(B_S + st));
-            }
-        } else if (lane == 0) {
-            // ---------------- O += P V ----------------
-            for (int i = 0; i < n; ++i) {
-                const int st = i & 1;
-                const uint32_t c = used[st] + (i >> 1);
-                wait(B_V + st, c);
-                wait(B_P + st, c);
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_ts(tmem + 256 + 128 * st, tmem + 128 * st + 8 * k,
-                           v_desc(base + S::v_at + st * kTile + k * 2048),
-                           idesc_f16(128, 128) | (1u << 16), i >= 2 || k != 0);
-                mma_commit(bar(B_PV + st));
-            }
+            meet();
+            used[0] += (n + 1) / 2;
+            used[1] += n / 2;
         }
-        __syncwarp();
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        used[0] += (n + 1) / 2;
-        used[1] += n / 2;
-        ++pieces;
-        u += n;
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+        const int which = warp - kSoftWarps - kDecWarps;
+        if (which >= 2)
+            return;
+        while (next(walk, q)) {
+            const int n = q.n;
+            meet();
+            if (which == 0 && lane == 0) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_ss(tmem, sw128_desc(base + S::v_at + (k >> 2) * 16384) + 2 * (k & 3),
+                           sw128_desc(base + S::k_at + (k >> 2) * 16384) + 2 * (k & 3),
+                           idesc_q<std::is_same<E, __nv_bfloat16>::value>(), k != 0);
+                mma_commit(bar(B_Q));
+            }
+            meet();
+            if (which == 0 && lane == 0) {
+                // ---------------- S = Q K^T ----------------
+                for (int i = 0; i < n; ++i) {
+                    const int st = i & 1;
+                    const uint32_t c = used[st] + (i >> 1);
+                    wait(B_K + st, c);
+                    if (c > 0)
+                        wait(B_PV + st, c - 1);           // the weights lie where S goes
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_ss(tmem + 128 * st,
+                               sw128_desc(base + S::q_at + (k >> 2) * 16384) + 2 * (k & 3),
+                               sw128_desc(base + S::k_at + st * kTile + (k >> 2) * 16384) + 2 * (k & 3),
+                               idesc_f16(128, 128), k != 0);
+                    mma_commit(bar(B_S + st));
+                }
+            } else if (lane == 0) {
+                // ---------------- O += P V ----------------
+                for (int i = 0; i < n; ++i) {
+                    const int st = i & 1;
+                    const uint32_t c = used[st] + (i >> 1);
+                    wait(B_V + st, c);
+                    wait(B_P + st, c);
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_ts(tmem + 256 + 128 * st, tmem + 128 * st + 8 * k,
+                               v_desc(base + S::v_at + st * kTile + k * 2048),
+                               idesc_f16(128, 128) | (1u << 16), i >= 2 || k != 0);
+                    mma_commit(bar(B_PV + st));
+                }
+            }
+            meet();
+            used[0] += (n + 1) / 2;
+            used[1] += n / 2;
+        }
     }
-    // nothing of the products may be under way when the tensor memory goes back
-    if (threadIdx.x == 32 * (kSoftWarps + kDecWarps)) {
-        mma_commit(bar(B_END));
-        wait(B_END, 0);
-    }
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
+    // Every product has been waited for by the group that uses it, so the tensor memory is free.
+    meet();
     if (warp == kSoftWarps + kDecWarps)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
