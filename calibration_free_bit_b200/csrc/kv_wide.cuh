@@ -39,10 +39,6 @@ constexpr int kRows = 128, kTokens = 128, D = 128;
 constexpr int kSoftWarps = 8, kDecWarps = 16;
 constexpr int kThreads = 32 * (kSoftWarps + kDecWarps + 4);
 constexpr int kWorking = 32 * (kSoftWarps + kDecWarps + 2);       // that meet at barrier 0
-// Registers a thread: 72 at the launch, 896 threads; 112 + 56 + 24 leave 64 x 128 x 8 of them free
-constexpr int kSoftRegs = 112, kDecRegs = 56, kIssueRegs = 24;
-static_assert(32 * (kSoftWarps * kSoftRegs + kDecWarps * kDecRegs + 4 * kIssueRegs) <=
-                  kThreads * 72, "registers: no more than the launch's");
 constexpr int kTile = 128 * D * 2;                    // an operand: 32 KB
 
 struct Smem {
@@ -203,7 +199,6 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
 
     if (warp < kSoftWarps) {
         // ---------------- softmax: group `me` has units me, me + 2, ... ----------------
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         uint32_t pieces = 0;
         while (next(walk, q)) {
             const Seq &s = q.s;
@@ -464,7 +459,6 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
         }
     } else if (warp < kSoftWarps + kDecWarps) {
         // ---------------- decoders: half a token's key row or value row a thread ----------------
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDecRegs));
         const int dt = threadIdx.x - 32 * kSoftWarps;
         while (next(walk, q)) {
             const int n = q.n, tile0 = q.tile0, total = q.total, kvh = q.kvh, b = q.b;
@@ -600,7 +594,6 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
             used[1] += n / 2;
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
         const int which = warp - kSoftWarps - kDecWarps;
         if (which >= 2)
             return;
