@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv_write_rows(const KvWriteParams
                 atomicOr(p.err, KV_ERR_SLOT);
             continue;
         }
-        const E *x = static_cast<const E *>(p.x[o.w]) + o.tok * p.x_stride[o.w] + o.head * D;
+        const E *x = static_cast<const E *>(pick(p.x, o.w)) + o.tok * pick(p.x_stride, o.w) + o.head * D;
 #pragma unroll
         for (int i = 0; i < N; ++i)
             xs[warp][i * 32 + lane] = to_f32(x[i * 32 + lane]);
@@ -88,8 +88,8 @@ __global__ void __launch_bounds__(32 * kWarps) kv_write_rows(const KvWriteParams
         __syncwarp();
         const long long at = cache_row(p.c, slot, o.head);
         if (lane == 0)
-            p.c.norms[o.w][at] = norm;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(p.c.codes[o.w] + at * p.c.row_bytes);
+            pick(p.c.norms, o.w)[at] = norm;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(pick(p.c.codes, o.w) + at * p.c.row_bytes);
         for (int w = lane; w < p.c.row_bytes / 4; w += 32) {
             uint32_t v = 0;
             // codes that overlap bits [32 w, 32 w + 32)
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv_read_rows(const KvReadParams p
          r += (long long)gridDim.x * kWarps) {
         const Row o = row_of(r, p.c.kv_heads);
         const long long slot = p.slots[o.tok];
-        E *y = static_cast<E *>(p.y[o.w]) + o.tok * p.y_stride[o.w] + o.head * D;
+        E *y = static_cast<E *>(pick(p.y, o.w)) + o.tok * pick(p.y_stride, o.w) + o.head * D;
         if (!slot_ok(p.c, slot)) {
             if (slot != -1 && lane == 0)
                 atomicOr(p.err, KV_ERR_SLOT);
@@ -130,13 +130,13 @@ __global__ void __launch_bounds__(32 * kWarps) kv_read_rows(const KvReadParams p
             continue;
         }
         const long long at = cache_row(p.c, slot, o.head);
-        const uint8_t *row = p.c.codes[o.w] + at * p.c.row_bytes;
+        const uint8_t *row = pick(p.c.codes, o.w) + at * p.c.row_bytes;
         float z[N];
 #pragma unroll
         for (int i = 0; i < N; ++i)
             z[i] = p.cent[code_at(row, lane * N + i, p.c.bits)];
         warp_wht<D>(z, p.h, lane);
-        const float s = p.c.norms[o.w][at] * p.scale;
+        const float s = pick(p.c.norms, o.w)[at] * p.scale;
 #pragma unroll
         for (int i = 0; i < N; ++i)
             xs[warp][ent[i] & 0x7fffu] = s * ((ent[i] & 0x8000u) ? -z[i] : z[i]);

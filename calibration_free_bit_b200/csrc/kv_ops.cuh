@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 namespace oq {
 namespace kvops {
@@ -20,12 +21,46 @@ template <> __device__ __forceinline__ float from_f32<float>(float v) { return v
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-// 16 bytes of elements <-> fp32.
+// One of a pair of kernel parameters (indexed by a variable they would go through local memory).
+template <class T> __device__ __forceinline__ T pick(T const (&of)[2], int w) {
+    return w ? of[1] : of[0];
+}
+
+// 16 bytes of elements <-> fp32 (n of them).
 template <class E> struct Vec {
     static constexpr int n = 16 / sizeof(E);
-    union { uint4 u; E e[n]; };
-    __device__ __forceinline__ void load(const E *p) { u = *reinterpret_cast<const uint4 *>(p); }
-    __device__ __forceinline__ void store(E *p) const { *reinterpret_cast<uint4 *>(p) = u; }
+    static __device__ __forceinline__ void unpack(const uint4 &u, float (&f)[n]) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(E) == 4) {
+                f[i] = __uint_as_float(w[i]);
+            } else if constexpr (std::is_same<E, __nv_bfloat16>::value) {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            } else {
+                const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                f[2 * i] = h.x;
+                f[2 * i + 1] = h.y;
+            }
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&f)[n]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(E) == 4) {
+                w[i] = __float_as_uint(f[i]);
+            } else if constexpr (std::is_same<E, __nv_bfloat16>::value) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            } else {
+                const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
 };
 
 // The unnormalised block Walsh-Hadamard transform (blocks of h) of a row of D held by a warp:

@@ -162,10 +162,10 @@ kv_write_tc(const KvWriteParams p, const uint4 *r_img, const int tbl_words, cons
     auto load = [&](int tile) {
         const int w = tile >= half_tiles;
         const long long r0 = (long long)(tile - w * half_tiles) * 128;
-        const char *x = static_cast<const char *>(p.x[w]);
+        const char *x = static_cast<const char *>(pick(p.x, w));
         constexpr int chunks = D / 8, step = G::group_threads / chunks;
         const int ch = tid % chunks;
-        const bool flat = p.x_stride[w] == (long long)heads * D;
+        const bool flat = pick(p.x_stride, w) == (long long)heads * D;
 #pragma unroll
         for (int i = 0; i < 128 / step; ++i) {
             const int r = i * step + tid / chunks;
@@ -177,7 +177,7 @@ kv_write_tc(const KvWriteParams p, const uint4 *r_img, const int tbl_words, cons
                     from = at * D;
                 } else {
                     const long long tok = at / heads;
-                    from = tok * p.x_stride[w] + (at - tok * heads) * D;
+                    from = tok * pick(p.x_stride, w) + (at - tok * heads) * D;
                 }
             }
             cp16(sA + operand_at(r, ch, 128), x + (from + ch * 8) * 2, real);
@@ -252,7 +252,7 @@ kv_write_tc(const KvWriteParams p, const uint4 *r_img, const int tbl_words, cons
             pack32<BITS>(z, out + k * BITS);
         }
         if (dst >= 0) {
-            uint8_t *to = p.c.codes[w] + dst * (D * BITS / 8) + part * (16 * BITS);
+            uint8_t *to = pick(p.c.codes, w) + dst * (D * BITS / 8) + part * (16 * BITS);
             if (BITS % 2 == 0 && p.wide) {
 #pragma unroll
                 for (int k = 0; k + 7 < 4 * BITS; k += 8)
@@ -267,7 +267,7 @@ kv_write_tc(const KvWriteParams p, const uint4 *r_img, const int tbl_words, cons
                         make_uint4(out[k], out[k + 1], out[k + 2], out[k + 3]);
             }
             if (part == 0)
-                p.c.norms[w][dst] = norm;
+                pick(p.c.norms, w)[dst] = norm;
         }
     }
     tear_down<D>(tmem0);
@@ -332,7 +332,7 @@ kv_read_tc(const KvReadParams p, const uint4 *r_img, const int tiles) {
         if (at < rows) {
             const long long tok = at / heads;
             const int head = (int)(at - tok * heads);
-            to = static_cast<E *>(p.y[w]) + tok * p.y_stride[w] + head * D + part * 128;
+            to = static_cast<E *>(pick(p.y, w)) + tok * pick(p.y_stride, w) + head * D + part * 128;
             const long long slot = p.slots[tok];
             if (slot_ok(p.c, slot))
                 src = cache_row(p.c, slot, head);
@@ -340,8 +340,8 @@ kv_read_tc(const KvReadParams p, const uint4 *r_img, const int tiles) {
                 atomicOr(p.err, KV_ERR_SLOT);
         }
         if (src >= 0) {
-            norm = p.c.norms[w][src];
-            load_words<words, 16>(c, p.c.codes[w] + src * (D * BITS / 8) + part * (16 * BITS));
+            norm = pick(p.c.norms, w)[src];
+            load_words<words, 16>(c, pick(p.c.codes, w) + src * (D * BITS / 8) + part * (16 * BITS));
         } else {
 #pragma unroll
             for (int i = 0; i < words; ++i)

@@ -499,7 +499,7 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
             };
             auto fetch = [&](int i, int page) {
                 if (page >= 0 && page < p.c.pages) {
-                    const uint8_t *at = p.c.codes[w] + row_of(i, page) * (D * BITS / 8) + part * (8 * BITS);
+                    const uint8_t *at = pick(p.c.codes, w) + row_of(i, page) * (D * BITS / 8) + part * (8 * BITS);
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
                 }
             };
@@ -511,8 +511,8 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                 if (to.valid) {
                     const long long at = row_of(i, page);
                     load_words<words, 8 * BITS>(
-                        to.codes, p.c.codes[w] + at * (D * BITS / 8) + part * (8 * BITS));
-                    to.norm = __ldg(p.c.norms[w] + at);
+                        to.codes, pick(p.c.codes, w) + at * (D * BITS / 8) + part * (8 * BITS));
+                    to.norm = __ldg(pick(p.c.norms, w) + at);
                 } else {
 #pragma unroll
                     for (int k = 0; k < words; ++k)
