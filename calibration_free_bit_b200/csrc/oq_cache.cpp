@@ -260,13 +260,13 @@ void oq_free_rope(oq_rope *r) {
     delete r;
 }
 
-int oq_apply_rope(const oq_rope *r, const oq_rope_rows *rows, int num_rows, int dtype, int T, int d,
-                  const int64_t *positions, int inverse, void *stream) {
+int oq_apply_rope(const oq_rope *r, const void *x, long long x_stride, void *y, long long y_stride,
+                  int heads, const void *k, long long k_stride, void *ky, long long ky_stride,
+                  int k_heads, int dtype, int T, int d, const int64_t *positions, int inverse,
+                  void *stream) {
     const char *who = "oq_apply_rope";
-    if (!r || !rows)
-        return fail(OQ_EINVAL, "%s: null handle or rows", who);
-    if (num_rows != 1 && num_rows != 2)
-        return fail(OQ_EINVAL, "%s: num_rows = %d (1 or 2 tensors)", who, num_rows);
+    if (!r)
+        return fail(OQ_EINVAL, "%s: null handle", who);
     if (dtype != OQ_F32 && dtype != OQ_BF16 && dtype != OQ_F16)
         return fail(OQ_EINVAL, "%s: dtype must be OQ_F32, OQ_BF16 or OQ_F16", who);
     if (d < r->rot || d > 1024 || d % 16 != 0)
@@ -274,29 +274,29 @@ int oq_apply_rope(const oq_rope *r, const oq_rope_rows *rows, int num_rows, int 
                     who, d, r->rot);
     if (T < 0)
         return fail(OQ_EINVAL, "%s: negative row count %d", who, T);
-    for (int i = 0; i < num_rows; ++i)
-        if (rows[i].heads < 1 || rows[i].heads > OQ_KV_MAX_HEADS)
-            return fail(OQ_EINVAL, "%s: heads = %d not in [1, %d]", who, rows[i].heads,
+    oq::RopeParams p{};
+    p.x[0] = x, p.y[0] = y, p.x_stride[0] = x_stride, p.y_stride[0] = y_stride, p.heads[0] = heads;
+    if (k)
+        p.x[1] = k, p.y[1] = ky, p.x_stride[1] = k_stride, p.y_stride[1] = ky_stride,
+        p.heads[1] = k_heads;
+    for (int i = 0; i < (k ? 2 : 1); ++i)
+        if (p.heads[i] < 1 || p.heads[i] > OQ_KV_MAX_HEADS)
+            return fail(OQ_EINVAL, "%s: %d heads, not in [1, %d]", who, p.heads[i],
                         OQ_KV_MAX_HEADS);
     if (T == 0)
         return OQ_OK;
     if (!positions || (reinterpret_cast<uintptr_t>(positions) & 7u))
         return fail(OQ_EINVAL, "%s: positions must be a non-null, 8-byte aligned pointer", who);
-    oq::RopeParams p{};
-    for (int i = 0; i < num_rows; ++i) {
-        int rc = check_rows(who, i ? "x[1]" : "x[0]", rows[i].x, rows[i].x_stride, dtype);
+    for (int i = 0; i < (k ? 2 : 1); ++i) {
+        int rc = check_rows(who, i ? "k" : "x", p.x[i], p.x_stride[i], dtype);
         if (rc == OQ_OK)
-            rc = check_out_rows(who, i ? "y[1]" : "y[0]", rows[i].y, rows[i].y_stride, dtype,
-                                (long long)rows[i].heads * d);
+            rc = check_out_rows(who, i ? "ky" : "y", p.y[i], p.y_stride[i], dtype,
+                                (long long)p.heads[i] * d);
         if (rc != OQ_OK)
             return rc;
-        if (rows[i].x == rows[i].y && rows[i].x_stride != rows[i].y_stride)
-            return fail(OQ_EINVAL, "%s: in place, x and y need the same token stride", who);
-        p.x[i] = rows[i].x;
-        p.y[i] = rows[i].y;
-        p.heads[i] = rows[i].heads;
-        p.x_stride[i] = rows[i].x_stride;
-        p.y_stride[i] = rows[i].y_stride;
+        if (p.x[i] == p.y[i] && p.x_stride[i] != p.y_stride[i])
+            return fail(OQ_EINVAL, "%s: in place, both strides of %s must be the same", who,
+                        i ? "k" : "x");
     }
     int dev;
     DeviceInfo *di;

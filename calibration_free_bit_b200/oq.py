@@ -75,7 +75,8 @@ def lib():
     L.oq_rope_values.argtypes = [vp, vp, C.POINTER(f64)]
     L.oq_free_rope.argtypes = [vp]
     L.oq_free_rope.restype = None
-    L.oq_apply_rope.argtypes = [vp, vp, i32, i32, i32, i32, vp, i32, vp]
+    L.oq_apply_rope.argtypes = [vp, vp, i64, vp, i64, i32, vp, i64, vp, i64, i32, i32, i32, i32,
+                                vp, i32, vp]
     L.oq_kv_write.argtypes = [vp, vp, vp, vp, i64, vp, i64, i32, i32, vp, vp]
     L.oq_kv_read.argtypes = [vp, vp, vp, vp, i32, vp, i64, vp, i64, i32, vp]
     L.oq_kv_attend.argtypes = [vp, vp, vp, vp, i64, vp, i64, i32, i32, i32, vp, vp, i32, i32, vp,
@@ -344,8 +345,7 @@ def _run(dev: int, fn, args, stream):
 
 
 def _like(t: torch.Tensor) -> torch.Tensor:
-    return (torch.empty_like(t) if t.is_contiguous() else
-            torch.empty(t.shape, dtype=t.dtype, device=t.device))
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 class Rope:
@@ -383,36 +383,33 @@ def oq_build_rope(rot_dim: int, layout: str = "half", theta: float = 10000.0,
     return Rope(rot_dim, layout, theta, scaling, factor, original_len)
 
 
-class _RopeRows(C.Structure):
-    _fields_ = [("x", C.c_void_p), ("y", C.c_void_p), ("heads", C.c_int),
-                ("x_stride", C.c_longlong), ("y_stride", C.c_longlong)]
-
-
 def oq_apply_rope(rope: Rope, x: torch.Tensor, positions: torch.Tensor, k=None, out=None,
                   k_out=None, inverse: bool = False, stream=None):
     """Rotary positions of x [T, heads, d] and, in the same launch, of k [T, k_heads, d] (fp32,
     bf16 or fp16; token stride free); positions int64 [T].  inverse=True applies the transpose
     (gradients).  Returns out, or (out, k_out); out=x works in place."""
-    T, heads, d = x.shape if x.dim() == 3 else (0, 0, 0)
-    pairs = [(x, out, "x")] + ([(k, k_out, "k")] if k is not None else [])
-    rows = (_RopeRows * len(pairs))()
-    outs = []
-    for i, (a, b, what) in enumerate(pairs):
-        xs = _rows(a, what, d=d, dtype=x.dtype)
-        if a.shape[0] != T:
-            _bad(f"{what} has {a.shape[0]} tokens, x {T}")
-        if b is None:
-            b = _like(a)
-        ys = _rows(b, f"the output of {what}", a.shape[1], d, x.dtype)
-        if b.shape[0] != T:
-            _bad(f"the output of {what} has {b.shape[0]} tokens, x {T}")
-        rows[i] = _RopeRows(a.data_ptr(), b.data_ptr(), a.shape[1], xs, ys)
-        outs.append(b)
+    xs = _rows(x, "x")
+    T, heads, d = x.shape
+    if out is None:
+        out = _like(x)
+    ys = _rows(out, "out", heads, d, x.dtype)
+    if out.shape[0] != T:
+        _bad(f"out has {out.shape[0]} tokens, x {T}")
+    kp, ks, kyp, kys, k_heads = None, 0, None, 0, 0
+    if k is not None:
+        ks = _rows(k, "k", d=d, dtype=x.dtype)
+        if k_out is None:
+            k_out = _like(k)
+        k_heads = k.shape[1]
+        kys = _rows(k_out, "k_out", k_heads, d, x.dtype)
+        if k.shape[0] != T or k_out.shape[0] != T:
+            _bad(f"k has {k.shape[0]} tokens, k_out {k_out.shape[0]}, x {T}")
+        kp, kyp = k.data_ptr(), k_out.data_ptr()
     pos = _ints(positions, "positions", torch.int64, (T,))
-    _run(_device(x, k, positions, *outs), lib().oq_apply_rope,
-         (rope.handle, C.addressof(rows), len(pairs), _ROW_DTYPES[x.dtype], T, d, pos,
-          1 if inverse else 0), stream)
-    return outs[0] if k is None else tuple(outs)
+    _run(_device(x, positions, out, k, k_out), lib().oq_apply_rope,
+         (rope.handle, x.data_ptr(), xs, out.data_ptr(), ys, heads, kp, ks, kyp, kys, k_heads,
+          _ROW_DTYPES[x.dtype], T, d, pos, 1 if inverse else 0), stream)
+    return out if k is None else (out, k_out)
 
 
 class _KVCacheStruct(C.Structure):
@@ -479,9 +476,9 @@ def oq_kv_read(r: RPBH, c: Codebook, cache: KVCache, slots: torch.Tensor, k=None
     at = _ints(slots, "slots", torch.int64, (T,))
     shape = (T, cache.kv_heads, cache.d)
     if k is None:
-        k = torch.empty(shape, dtype=out_dtype, device=slots.device)
+        k = slots.new_empty(shape, dtype=out_dtype)
     if v is None:
-        v = torch.empty(shape, dtype=k.dtype, device=slots.device)
+        v = slots.new_empty(shape, dtype=k.dtype)
     ks = _rows(k, "k", cache.kv_heads, cache.d)
     vs = _rows(v, "v", cache.kv_heads, cache.d, k.dtype)
     if k.shape[0] != T or v.shape[0] != T:

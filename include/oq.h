@@ -299,23 +299,18 @@ int oq_build_rope(int rot_dim, int layout, double theta, int scaling, double fac
 int oq_rope_values(const oq_rope *r, double *freq, double *amplitude);
 void oq_free_rope(oq_rope *r);
 
-/* One tensor of oq_apply_rope: x and y [T, heads, d], token strides in elements; y = x (with the
- * same stride) works in place, any other overlap is not allowed. */
-typedef struct {
-    const void *x;
-    void *y;
-    int heads;
-    long long x_stride, y_stride;
-} oq_rope_rows;
-
 /* Pair (a, b) of every head of token t becomes m (a cos - b sin, a sin + b cos), m the amplitude
  * and the angle positions[t] * freq_i, reduced in fp64; elements from rot_dim on are copied.
- * One or two tensors (queries, keys) of the same tokens.  inverse != 0 applies the transpose
+ * x and y [T, heads, d], and with k != NULL, in the same launch, the keys k and ky [T, k_heads, d] of
+ * the same tokens (k_heads, the strides and ky are not read without k).  y = x (with the same
+ * stride) works in place; any other overlap is not allowed.  inverse != 0 applies the transpose
  * (-sin for sin): the gradient of x from the gradient of y.  positions: device, int64 [T], any
  * sign.  dtype OQ_F32, OQ_BF16 or OQ_F16; the products are fp32, rounded once.  d: a multiple of
  * 16, rot_dim <= d <= 1024.  T = 0 is a no-op.  Errors: OQ_EINVAL, OQ_EUNSUPPORTED, OQ_ECUDA. */
-int oq_apply_rope(const oq_rope *r, const oq_rope_rows *rows, int num_rows, int dtype, int T, int d,
-                  const int64_t *positions, int inverse, void *stream);
+int oq_apply_rope(const oq_rope *r, const void *x, long long x_stride, void *y, long long y_stride,
+                  int heads, const void *k, long long k_stride, void *ky, long long ky_stride,
+                  int k_heads, int dtype, int T, int d, const int64_t *positions, int inverse,
+                  void *stream);
 
 /* A paged cache of keys and values: the caller's device arrays, 16-byte aligned.  Row (page, head,
  * offset) of *_codes [num_pages, kv_heads, page_size, d*bits/8] has a head's packed codes, the

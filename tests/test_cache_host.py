@@ -55,21 +55,20 @@ _ROPE = []
 def _rope_call(**kw):
     if not _ROPE:
         _ROPE.append(oq.oq_build_rope(128))
-    a = dict(r=_ROPE[0].handle, n=1, dtype=oq.OQ_BF16, T=4, d=128, pos=FAKE, x=FAKE,
-             y=FAKE, heads=2, xs=256, ys=256)
+    a = dict(r=_ROPE[0].handle, dtype=oq.OQ_BF16, T=4, d=128, pos=FAKE, x=FAKE, y=FAKE, heads=2,
+             xs=256, ys=256, k=None, ks=128, ky=FAKE, kys=128, k_heads=1)
     a.update(kw)
-    rows = (oq._RopeRows * 2)()
-    for i in range(2):
-        rows[i] = oq._RopeRows(a["x"], a["y"], a["heads"], a["xs"], a["ys"])
-    return oq.lib().oq_apply_rope(a["r"], C.addressof(rows), a["n"], a["dtype"], a["T"], a["d"],
-                                  a["pos"], 0, None)
+    return oq.lib().oq_apply_rope(a["r"], a["x"], a["xs"], a["y"], a["ys"], a["heads"], a["k"],
+                                  a["ks"], a["ky"], a["kys"], a["k_heads"], a["dtype"], a["T"],
+                                  a["d"], a["pos"], 0, None)
 
 
 @pytest.mark.parametrize("kw", [
-    dict(r=None), dict(n=0), dict(n=3), dict(dtype=3), dict(dtype=-1), dict(d=64), dict(d=136),
-    dict(d=2048), dict(T=-1), dict(heads=0), dict(heads=1025), dict(pos=None), dict(pos=FAKE + 4),
-    dict(x=None), dict(y=None), dict(x=FAKE + 2), dict(xs=-256), dict(xs=260), dict(ys=248),
-    dict(xs=512)])       # in place with two strides
+    dict(r=None), dict(dtype=3), dict(dtype=-1), dict(d=64), dict(d=136), dict(d=2048), dict(T=-1),
+    dict(heads=0), dict(heads=1025), dict(pos=None), dict(pos=FAKE + 4), dict(x=None), dict(y=None),
+    dict(x=FAKE + 2), dict(xs=-256), dict(xs=260), dict(ys=248), dict(xs=512),  # in place, 2 strides
+    dict(k=FAKE, ky=None), dict(k=FAKE + 4), dict(k=FAKE, k_heads=0), dict(k=FAKE, kys=120),
+    dict(k=FAKE, ks=256)])
 def test_apply_rope_refusals(kw):
     assert _rope_call(**kw) == oq.OQ_EINVAL, kw
 
