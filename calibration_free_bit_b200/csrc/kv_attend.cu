@@ -84,61 +84,66 @@ cudaError_t join(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, cu
                       ws);
 }
 
-// How a call runs.
+#define OQ_BY_BITS(bits, call)  \
+    switch (bits) {             \
+    case 2:                     \
+        return call(2);         \
+    case 3:                     \
+        return call(3);         \
+    case 4:                     \
+        return call(4);         \
+    case 6:                     \
+        return call(6);         \
+    default:                    \
+        return call(8);         \
+    }
+
+int narrow_workers(const KvAttendParams &p, int dtype, int sms) {
+#define OQ_CALL(B) kv_attend_workers_b##B(p, dtype, sms)
+    OQ_BY_BITS(p.c.bits, OQ_CALL)
+#undef OQ_CALL
+}
+cudaError_t launch_narrow(const KvAttendParams &p, const KvAttendSpace &ws, int dtype,
+                          cudaStream_t st) {
+#define OQ_CALL(B) launch_kv_attend_b##B(p, ws, dtype, st)
+    OQ_BY_BITS(p.c.bits, OQ_CALL)
+#undef OQ_CALL
+}
+cudaError_t launch_wide(const KvAttendParams &p, const KvAttendSpace &ws, int dtype,
+                        cudaStream_t st) {
+#define OQ_CALL(B) launch_kv_wide_b##B(p, ws, dtype, st)
+    OQ_BY_BITS(p.c.bits, OQ_CALL)
+#undef OQ_CALL
+}
+
+// How a call runs: tiles of 128 rows (kv_wide.cuh) for more than 16 rows a key head of 128, else
+// of 8 or 16 (kv_attend.cuh).
 struct Plan {
-    bool wide = false;            // kv_wide.cuh and a join; else kv_attend.cuh
-    int splits = 1;               // kv_attend.cuh: CTAs that share a row tile's tokens
-    long long slots = 0;          // wide: the workspace's
-    KvAttendSpace ws = {};
+    bool wide;
+    int tile;                     // rows of a tile
+    long long slots;              // of the workspace
+    KvAttendSpace ws;
 };
 
-Plan plan_for(const KvAttendParams &p, int num_sms) {
-    Plan a;
+Plan plan_for(const KvAttendParams &p, int dtype, int num_sms) {
+    Plan a = {};
     const int rows = p.max_nodes * p.group;
-    const long long tokens = (long long)p.table_width << p.c.page_log2;
-    if (p.c.d == 128 && rows > 16) {
-        a.ws.rows = rows < 128 ? rows : 128;
-        a.ws.segments = p.c.kv_heads * ((rows + 127) / 128);
-        a.ws.most = num_sms;
-        a.ws.least = 1;
-        a.slots = (long long)p.B * a.ws.segments + a.ws.most;
-        // a workspace of this size at most (its slots go with the sequences, used or not)
-        a.wide = a.slots * a.ws.rows * 128 * 4 <= (1ll << 30);
-        if (a.wide)
-            return a;
-    }
-    // Enough CTAs to give every SM a few, but none with less than two steps for each of its
-    // warps at the longest context the table can hold.
-    const int tile = rows <= 8 ? 8 : 16;
-    const long long ctas = (long long)p.c.kv_heads * ((rows + tile - 1) / tile) * p.B;
-    while (a.splits < 16 && ctas * a.splits < 4ll * num_sms && tokens >= 128ll * a.splits)
-        a.splits *= 2;
+    a.wide = p.c.d == 128 && rows > 16;
+    a.tile = a.wide ? 128 : rows <= 8 ? 8 : 16;
+    a.ws.rows = rows < a.tile ? rows : a.tile;
+    a.ws.segments = p.c.kv_heads * ((rows + a.tile - 1) / a.tile);
+    a.ws.most = a.wide ? num_sms : narrow_workers(p, dtype, num_sms);
+    // a wide worker is an SM, a narrow one a warp, which should not be set up for less than this
+    a.ws.least = a.wide ? 1 : 4;
+    a.slots = (long long)p.B * a.ws.segments + a.ws.most;
     return a;
 }
 
 }  // namespace
 }  // namespace attend
 
-cudaError_t launch_kv_wide(const KvAttendParams &p, const KvAttendSpace &ws, int dtype,
-                           cudaStream_t st) {
-    switch (p.c.bits) {
-    case 2:
-        return launch_kv_wide_b2(p, ws, dtype, st);
-    case 3:
-        return launch_kv_wide_b3(p, ws, dtype, st);
-    case 4:
-        return launch_kv_wide_b4(p, ws, dtype, st);
-    case 6:
-        return launch_kv_wide_b6(p, ws, dtype, st);
-    default:
-        return launch_kv_wide_b8(p, ws, dtype, st);
-    }
-}
-
-size_t kv_attend_space(const KvAttendParams &p, int num_sms) {
-    const attend::Plan a = attend::plan_for(p, num_sms);
-    if (!a.wide)
-        return 0;
+size_t kv_attend_space(const KvAttendParams &p, int dtype, int num_sms) {
+    const attend::Plan a = attend::plan_for(p, dtype, num_sms);
     return KvAttendSpace::first_at(a.slots, a.ws.rows, p.c.d) + (size_t)(p.B + 1) * 8;
 }
 
@@ -155,28 +160,23 @@ cudaError_t launch_kv_attend(const KvAttendParams &params, void *space, int dtyp
     if (e != cudaSuccess)
         return e;
     p.err = static_cast<unsigned *>(word[dev]);
-    attend::Plan a = attend::plan_for(p, num_sms);
+    attend::Plan a = attend::plan_for(p, dtype, num_sms);
+    char *w = static_cast<char *>(space);
+    a.ws.part = reinterpret_cast<float *>(w);
+    a.ws.stat = reinterpret_cast<float *>(w + KvAttendSpace::stat_at(a.slots, a.ws.rows, p.c.d));
+    a.ws.first =
+        reinterpret_cast<long long *>(w + KvAttendSpace::first_at(a.slots, a.ws.rows, p.c.d));
     if (a.wide) {
-        char *w = static_cast<char *>(space);
-        a.ws.part = reinterpret_cast<float *>(w);
-        a.ws.stat = reinterpret_cast<float *>(w + KvAttendSpace::stat_at(a.slots, a.ws.rows, 128));
-        a.ws.first =
-            reinterpret_cast<long long *>(w + KvAttendSpace::first_at(a.slots, a.ws.rows, 128));
-        e = launch_kv_wide(p, a.ws, dtype, st);
+        e = attend::launch_wide(p, a.ws, dtype, st);
         return e != cudaSuccess ? e : attend::join<128, 128, 128>(p, a.ws, dtype, st);
     }
-    switch (p.c.bits) {
-    case 2:
-        return launch_kv_attend_b2(p, dtype, a.splits, st);
-    case 3:
-        return launch_kv_attend_b3(p, dtype, a.splits, st);
-    case 4:
-        return launch_kv_attend_b4(p, dtype, a.splits, st);
-    case 6:
-        return launch_kv_attend_b6(p, dtype, a.splits, st);
-    default:
-        return launch_kv_attend_b8(p, dtype, a.splits, st);
-    }
+    if ((e = attend::launch_narrow(p, a.ws, dtype, st)) != cudaSuccess)
+        return e;
+    if (p.c.d == 128)
+        return a.tile == 8 ? attend::join<128, 16, 8>(p, a.ws, dtype, st)
+                           : attend::join<128, 16, 16>(p, a.ws, dtype, st);
+    return a.tile == 8 ? attend::join<256, 16, 8>(p, a.ws, dtype, st)
+                       : attend::join<256, 16, 16>(p, a.ws, dtype, st);
 }
 
 cudaError_t read_and_clear_attend_error(unsigned *out, cudaStream_t st) {

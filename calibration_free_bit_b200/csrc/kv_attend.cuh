@@ -1,5 +1,5 @@
 // kv_attend.cuh -- attention of drafted tokens over the quantised cache, one instance a bit width
-// (kv_attend_b*.cu); launch_kv_attend (kv_attend.cu) picks it.
+// (kv_attend_b*.cu); launch_kv_attend (kv_attend.cu) picks it.  Work list: kv_attend_ops.cuh.
 //
 // o = sum_t p_t v_hat_t, p = softmax_t(scale * q . k_hat_t), over the visible cached tokens t of
 // the row's sequence: its prefix, and those of its drafted tokens that the row's mask names (bit
@@ -8,12 +8,13 @@
 // once, to the finished row.
 //
 // What bounds it is the cache's bytes (a token of one head: two rows of codes and two norms), and
-// behind them the decode of two codes to a pair of fp16 centroids.  So:
+// right behind them shared memory: two codes a lookup.  So:
 //   - the rows of one key head (its query heads times the nodes) share a pass over its tokens, in
-//     tiles of 8 NT rows, and a tile's tokens are split over a cluster of CTAs (flash decoding),
-//     whose partial results meet in shared memory: one launch, no workspace, a fixed order;
+//     tiles of 8 NT rows; a unit of work is 16 tokens of a tile, a worker is one warp, all warps of
+//     all SMs have the same number of units, and no warp waits for another.  What a warp has of a
+//     segment goes to the workspace; a second kernel joins the pieces in a fixed order;
 //   - codes go from global memory straight to the registers of the lane that decodes them, 16 bytes
-//     and less at a time, a step ahead of their use, and through a table in shared memory with a
+//     and less at a time, a unit ahead of their use, and through a table in shared memory with a
 //     column a lane (no bank conflicts) into the operand of a matrix instruction;
 //   - products are transposed, S^T = K Q^T and O^T = V^T P^T (mma.sync m16n8k16): the 16-wide side
 //     is the cache, so 8 rows fill an instruction and an accumulator takes 32 registers.  The
@@ -23,11 +24,9 @@
 // Scores, softmax statistics and sums are fp32.  fp16 enters in three places: the rotated query
 // (over a power of two of its own), the centroids (times alpha, see build_kv_lut) and the weights
 // p s_v, which are taken relative to a power of two above the row's largest s_v and times 2^6 to
-// 2^14: what a token adds is resolved down to 2^-31 of the largest.  With SPLIT (fp16 outputs) query and
-// weights enter as a sum of two fp16 numbers, so that only the centroids' rounding is left.
+// 2^14: what a token adds is resolved down to 2^-31 of the largest.  With SPLIT (fp16 outputs) query
+// and weights enter as a sum of two fp16 numbers, so that only the centroids' rounding is left.
 #pragma once
-
-#include <cooperative_groups.h>
 
 #include "kv_attend_ops.cuh"
 #include "kv_internal.h"
@@ -54,7 +53,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     return r;
 }
 
-constexpr int kWarps = 4;
 template <int D, int BITS> struct Shape {
     static constexpr int row_bytes = D * BITS / 8;
     static constexpr int k_bytes = row_bytes / 4;     // a lane's share of a key row
@@ -123,78 +121,66 @@ template <int D, int BITS> struct Tile {
 };
 
 template <int D, int BITS, int NT, bool SPLIT> struct Smem {
+    // Warps of the one CTA on an SM: as many as its registers hold.
+    static constexpr int warps = D == 128 && NT == 1 ? (SPLIT || BITS == 8 ? 12 : 16) : 8;
     static constexpr int rows = 8 * NT;
     // queries stay in shared memory where registers do not hold them beside the accumulators
     static constexpr bool q_shared = D == 256 && NT == 2;
-    static constexpr int part = (D / 16) * NT * 4 * 32 * 4 + NT * 8 * 32 * 4;  // a warp's state
-    static constexpr int fin_stride = D + 4;                                 // floats
-    static constexpr int big_a = Lut<BITS, true>::bytes > (kWarps / 2) * part
-                                     ? Lut<BITS, true>::bytes : (kWarps / 2) * part;
-    static constexpr int fin = rows * fin_stride * 4;
-    static constexpr int big = (big_a > fin ? big_a : fin);                  // table, then partials
-    static constexpr int q_at = big;
     static constexpr int q_half = rows * D;                                  // halves
-    static constexpr int q_bytes = q_half * 2 * (SPLIT ? 2 : 1);
-    static constexpr int x_at = q_at + q_bytes;                              // [kWarps][D] floats
-    static constexpr int mask_at = x_at + kWarps * D * 4;
-    static constexpr int stat_at = mask_at + rows * 8;                       // qs, m, l: [rows]
-    static constexpr int bytes = stat_at + rows * 12;
+    // a warp's own: queries, a row being rotated, masks, score factors
+    static constexpr int x_at = q_half * 2 * (SPLIT ? 2 : 1);
+    static constexpr int mask_at = x_at + D * 4;
+    static constexpr int scale_at = mask_at + rows * 8;
+    static constexpr int own = (scale_at + rows * 4 + 15) / 16 * 16;
+    static constexpr int bytes = Lut<BITS, true>::bytes + warps * own;
 };
 
 template <class E, int D, int BITS, int NT, bool SPLIT>
-__global__ void __launch_bounds__(32 * kWarps)
-attend_tiles(const KvAttendParams p, const int row_tiles) {
+__global__ void __launch_bounds__(32 * Smem<D, BITS, NT, SPLIT>::warps, 1)
+attend_tiles(const KvAttendParams p, const KvAttendSpace ws) {
     using S = Shape<D, BITS>;
     using M = Smem<D, BITS, NT, SPLIT>;
     constexpr int N = D / 32, KS = D / 16;
     extern __shared__ __align__(128) unsigned char sm[];
-    namespace cg = cooperative_groups;
     unsigned char *lut = sm;
-    __half *qh = reinterpret_cast<__half *>(sm + M::q_at);
-    float *xs = reinterpret_cast<float *>(sm + M::x_at);
-    unsigned long long *masks = reinterpret_cast<unsigned long long *>(sm + M::mask_at);
-    float *qscale = reinterpret_cast<float *>(sm + M::stat_at);
-    float *row_m = qscale + M::rows, *row_l = row_m + M::rows;
 
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int rank = blockIdx.x, splits = gridDim.x;       // the cluster is the whole x dimension
-    const int kvh = blockIdx.y / row_tiles, tile = blockIdx.y - kvh * row_tiles;
-    const int b = blockIdx.z;
+    unsigned char *own = sm + Lut<BITS, true>::bytes + warp * M::own;
+    __half *qh = reinterpret_cast<__half *>(own);
+    float *xs = reinterpret_cast<float *>(own + M::x_at);
+    unsigned long long *masks = reinterpret_cast<unsigned long long *>(own + M::mask_at);
+    float *qscale = reinterpret_cast<float *>(own + M::scale_at);
     fill_lut<BITS, true>(lut, p.lut);
     uint32_t ent[N];
 #pragma unroll
     for (int i = 0; i < N; ++i)
         ent[i] = p.ent[lane * N + i];
+    __syncthreads();
     pdl_wait();
-    Seq s;
-    if (!load_seq(p, b, &s, blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0))
-        return;                                            // the whole cluster returns
-    const int rows_all = s.nodes * p.group, row_base = tile * M::rows;
-    if (row_base >= rows_all)
-        return;
-    const int nrows = min(M::rows, rows_all - row_base);
-
-    // ---- this warp's tokens: tiles of 16, every kWarps-th of the rank's share; the first are on
-    // their way while the queries are rotated ----
-    const int total = s.prefix + s.nodes;
-    const int tiles = (total + 15) >> 4, share = (tiles + splits - 1) / splits;
-    const int last = min(tiles, (rank + 1) * share);
-    const int *table = p.table + (long long)b * p.table_width;
-    const int in_page = (1 << p.c.page_log2) - 1;
     const uint32_t col = lut_column<BITS>(lane);
-    int t = rank * share + warp;
+    // neighbouring workers on different SMs: few units reach all of them
+    const long long worker = (long long)warp * gridDim.x + blockIdx.x;
+    Walk walk = take_range<16, M::rows>(p, ws, worker, worker == 0);
+    Piece piece;
+    while (next_piece<16, M::rows>(p, walk, piece)) {
+    const Seq &s = piece.s;
+    const int kvh = piece.kvh, row_base = piece.row_base, nrows = piece.nrows;
+    // the first tiles are on their way while the queries are rotated
+    const int last = piece.tile0 + piece.n;
+    const int *table = p.table + (long long)piece.b * p.table_width;
+    const int in_page = (1 << p.c.page_log2) - 1;
+    int t = piece.tile0;
     Tile<D, BITS> ping, pong;
     int page = 0;
     bool bad_page = false;
-    if (t < last) {
-        ping.load(p, table[(t << 4) >> p.c.page_log2], (t << 4) & in_page, kvh, g, c);
-        if (t + kWarps < last)
-            page = table[((t + kWarps) << 4) >> p.c.page_log2];
-    }
+    ping.load(p, table[(t << 4) >> p.c.page_log2], (t << 4) & in_page, kvh, g, c);
+    if (t + 1 < last)
+        page = table[((t + 1) << 4) >> p.c.page_log2];
 
     // ---- rotated queries, fp16 over a power of two a row ----
-    for (int r = warp; r < M::rows; r += kWarps) {
+    __syncwarp();
+    for (int r = 0; r < M::rows; ++r) {
         float z[N];
         if (r < nrows) {
             const int node = (row_base + r) / p.group, e = (row_base + r) - node * p.group;
@@ -202,11 +188,11 @@ attend_tiles(const KvAttendParams p, const int row_tiles) {
             const E *q = static_cast<const E *>(p.q) + row * p.q_stride + (kvh * p.group + e) * D;
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                xs[warp * D + i * 32 + lane] = to_f32(q[i * 32 + lane]);
+                xs[i * 32 + lane] = to_f32(q[i * 32 + lane]);
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float v = xs[warp * D + (ent[i] & 0x7fffu)];
+                const float v = xs[ent[i] & 0x7fffu];
                 z[i] = (ent[i] & 0x8000u) ? -v : v;
             }
             warp_wht<D>(z, p.h, lane);
@@ -245,7 +231,6 @@ attend_tiles(const KvAttendParams p, const int row_tiles) {
             qscale[r] = up * p.qk_scale;
         __syncwarp();
     }
-    __syncthreads();
     // B operands of S^T = K Q^T: row n = g, elements c D/4 + 4 ks + {0, 1}, {2, 3}
     const uint2 *qsm = reinterpret_cast<const uint2 *>(qh) + lane;
     uint2 qf[M::q_shared ? 1 : NT][M::q_shared ? 1 : KS];
@@ -427,25 +412,25 @@ attend_tiles(const KvAttendParams p, const int row_tiles) {
     };
     // the tile after t, and the page of the one after that
     auto fetch = [&](Tile<D, BITS> &to, int t) {
-        const int tn = t + kWarps;
-        if (tn < last) {
-            to.load(p, page, (tn << 4) & in_page, kvh, g, c);
-            if (tn + kWarps < last)
-                page = table[((tn + kWarps) << 4) >> p.c.page_log2];
+        if (t + 1 < last) {
+            to.load(p, page, ((t + 1) << 4) & in_page, kvh, g, c);
+            if (t + 2 < last)
+                page = table[((t + 2) << 4) >> p.c.page_log2];
         }
     };
-    for (; t < last; t += 2 * kWarps) {
+    for (; t < last; t += 2) {
         fetch(pong, t);
         step(ping, t);
-        if (t + kWarps >= last)
+        if (t + 1 >= last)
             break;
-        fetch(ping, t + kWarps);
-        step(pong, t + kWarps);
+        fetch(ping, t + 1);
+        step(pong, t + 1);
     }
     if (bad_page && lane == 0)
         atomicOr(p.err, AT_ERR_PAGE);
 
-    // ---- the block's warps meet ----
+    // ---- the piece goes to its slot ----
+    const long long slot = (long long)piece.b * ws.segments + piece.seg + worker;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -453,164 +438,65 @@ attend_tiles(const KvAttendParams p, const int row_tiles) {
 #pragma unroll
             for (int k = 4; k < 32; k <<= 1)
                 l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], k);
+            const int r = 8 * n + 2 * c + i;
+            if (r >= nrows)
+                continue;
+            if (g == 0) {
+                ws.stat[slot * 2 * ws.rows + r] = m[n][i];
+                ws.stat[(slot * 2 + 1) * ws.rows + r] = l[n][i];
+            }
             const float f = vs[n][i] * (1.0f / kWeightScale);
+            float4 *dst = reinterpret_cast<float4 *>(ws.part + (slot * ws.rows + r) * D + g * (D / 8));
 #pragma unroll
-            for (int j = 0; j < KS; ++j) {
-                acc[n][j][i] *= f;
-                acc[n][j][2 + i] *= f;
-            }
-        }
-#pragma unroll
-    for (int half = kWarps / 2; half >= 1; half >>= 1) {
-        __syncthreads();                                  // the table / the last round is done with
-        float *mine = reinterpret_cast<float *>(sm + (warp & (half - 1)) * M::part) + lane;
-        if (warp >= half && warp < 2 * half) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                for (int j = 0; j < KS; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mine[((n * KS + j) * 4 + i) * 32] = acc[n][j][i];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    mine[(NT * KS * 4 + n * 4 + i) * 32] = m[n][i];
-                    mine[(NT * KS * 4 + n * 4 + 2 + i) * 32] = l[n][i];
-                }
-            }
-        }
-        __syncthreads();
-        if (warp < half) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float f[2], h[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float om = mine[(NT * KS * 4 + n * 4 + i) * 32];
-                    const float ol = mine[(NT * KS * 4 + n * 4 + 2 + i) * 32];
-                    const float mn = fmaxf(m[n][i], om);
-                    f[i] = ex2(m[n][i] - mn);
-                    h[i] = ex2(om - mn);
-                    m[n][i] = mn;
-                    l[n][i] = l[n][i] * f[i] + ol * h[i];
-                }
-#pragma unroll
-                for (int j = 0; j < KS; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[n][j][i] = acc[n][j][i] * f[i & 1] +
-                                       mine[((n * KS + j) * 4 + i) * 32] * h[i & 1];
-            }
+            for (int j = 0; j < KS; j += 2)
+                dst[j / 2] = make_float4(acc[n][j][i] * f, acc[n][j][2 + i] * f,
+                                         acc[n][j + 1][i] * f, acc[n][j + 1][2 + i] * f);
         }
     }
-    __syncthreads();
-    float *fin = reinterpret_cast<float *>(sm);           // [rows][fin_stride]
-    if (warp == 0) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = 8 * n + 2 * c + i;
-#pragma unroll
-                for (int j = 0; j < KS; ++j) {
-                    fin[r * M::fin_stride + g * (D / 8) + 2 * j] = acc[n][j][i];
-                    fin[r * M::fin_stride + g * (D / 8) + 2 * j + 1] = acc[n][j][2 + i];
-                }
-                if (g == 0) {
-                    row_m[r] = m[n][i];
-                    row_l[r] = l[n][i];
-                }
-            }
-    }
-    // ---- the cluster's blocks meet: rank k finishes rows k, k + splits, ... ----
-    cg::cluster_group cl = cg::this_cluster();
-    if (splits > 1)
-        cl.sync();
-    else
-        __syncthreads();
-    for (int r = rank + splits * warp; r < nrows; r += splits * kWarps) {
-        float mx = kNone;
-        for (int k = 0; k < splits; ++k)
-            mx = fmaxf(mx, *cl.map_shared_rank(row_m + r, k));
-        float o[N], sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            o[i] = 0.f;
-        for (int k = 0; k < splits; ++k) {
-            const float f = ex2(*cl.map_shared_rank(row_m + r, k) - mx);
-            sum += f * *cl.map_shared_rank(row_l + r, k);
-            const float4 *src = reinterpret_cast<const float4 *>(
-                cl.map_shared_rank(fin + r * M::fin_stride + lane * N, k));
-#pragma unroll
-            for (int i = 0; i < N; i += 4) {
-                const float4 v = src[i / 4];
-                o[i] += f * v.x, o[i + 1] += f * v.y, o[i + 2] += f * v.z, o[i + 3] += f * v.w;
-            }
-        }
-        warp_wht<D>(o, p.h, lane);
-        const float inv = sum == 0.f ? 0.f : p.o_scale / sum;      // nothing seen: zeros
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            xs[warp * D + (ent[i] & 0x7fffu)] = inv * ((ent[i] & 0x8000u) ? -o[i] : o[i]);
-        __syncwarp();
-        const int node = (row_base + r) / p.group, e = (row_base + r) - node * p.group;
-        E *y = static_cast<E *>(p.out) + (s.row0 + node) * p.out_stride + (kvh * p.group + e) * D;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            y[i * 32 + lane] = from_f32<E>(xs[warp * D + i * 32 + lane]);
-    }
-    if (splits > 1)
-        cl.sync();                                        // shared memory stays until all have read
 }
 
 template <class E, int D, int BITS, int NT, bool SPLIT>
-cudaError_t launch_tiles(const KvAttendParams &p, int splits, cudaStream_t st) {
+cudaError_t launch_tiles(const KvAttendParams &p, KvAttendSpace ws, cudaStream_t st) {
     using M = Smem<D, BITS, NT, SPLIT>;
     auto *kern = attend_tiles<E, D, BITS, NT, SPLIT>;
     static PerDevice ready;
     const cudaError_t e = ready.once([&] {
-        cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               M::bytes);
-        if (err == cudaSuccess)
-            err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        return err;
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, M::bytes);
     });
     if (e != cudaSuccess)
         return e;
-    const int rows = p.max_nodes * p.group, row_tiles = (rows + M::rows - 1) / M::rows;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(splits, p.c.kv_heads * row_tiles, p.B);
-    cfg.blockDim = dim3(32 * kWarps);
-    cfg.dynamicSmemBytes = M::bytes;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = splits;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, p, row_tiles);
+    return launch_pdl(kern, dim3(ws.most / M::warps), dim3(32 * M::warps), (size_t)M::bytes, st, p,
+                      ws);
+}
+
+// Workers of a launch on `sms` SMs.
+template <int D, int BITS> int workers_on(int sms, bool split, int rows) {
+    if (rows <= 8)
+        return sms * (split ? Smem<D, BITS, 1, true>::warps : Smem<D, BITS, 1, false>::warps);
+    return sms * (split ? Smem<D, BITS, 2, true>::warps : Smem<D, BITS, 2, false>::warps);
 }
 
 template <class E, int D, int BITS, bool SPLIT>
-cudaError_t launch_rows(const KvAttendParams &p, int splits, cudaStream_t st) {
-    const int rows = p.max_nodes * p.group;
-    if (rows <= 8)
-        return launch_tiles<E, D, BITS, 1, SPLIT>(p, splits, st);
-    return launch_tiles<E, D, BITS, 2, SPLIT>(p, splits, st);
+cudaError_t launch_rows(const KvAttendParams &p, const KvAttendSpace &ws, cudaStream_t st) {
+    if (p.max_nodes * p.group <= 8)
+        return launch_tiles<E, D, BITS, 1, SPLIT>(p, ws, st);
+    return launch_tiles<E, D, BITS, 2, SPLIT>(p, ws, st);
 }
 
 template <int BITS>
-cudaError_t launch_bits(const KvAttendParams &p, int dtype, int splits, cudaStream_t st) {
+cudaError_t launch_bits(const KvAttendParams &p, const KvAttendSpace &ws, int dtype,
+                        cudaStream_t st) {
     if (dtype == OQ_BF16)
-        return p.c.d == 128 ? launch_rows<__nv_bfloat16, 128, BITS, false>(p, splits, st)
-                            : launch_rows<__nv_bfloat16, 256, BITS, false>(p, splits, st);
-    return p.c.d == 128 ? launch_rows<__half, 128, BITS, true>(p, splits, st)
-                        : launch_rows<__half, 256, BITS, true>(p, splits, st);
+        return p.c.d == 128 ? launch_rows<__nv_bfloat16, 128, BITS, false>(p, ws, st)
+                            : launch_rows<__nv_bfloat16, 256, BITS, false>(p, ws, st);
+    return p.c.d == 128 ? launch_rows<__half, 128, BITS, true>(p, ws, st)
+                        : launch_rows<__half, 256, BITS, true>(p, ws, st);
+}
+
+template <int BITS> int workers_bits(const KvAttendParams &p, int dtype, int sms) {
+    const int rows = p.max_nodes * p.group;
+    return p.c.d == 128 ? workers_on<128, BITS>(sms, dtype != OQ_BF16, rows)
+                        : workers_on<256, BITS>(sms, dtype != OQ_BF16, rows);
 }
 
 }  // namespace attend

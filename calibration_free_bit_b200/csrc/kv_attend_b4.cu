@@ -3,8 +3,13 @@
 
 namespace oq {
 
-cudaError_t launch_kv_attend_b4(const KvAttendParams &p, int dtype, int splits, cudaStream_t st) {
-    return attend::launch_bits<4>(p, dtype, splits, st);
+cudaError_t launch_kv_attend_b4(const KvAttendParams &p, const KvAttendSpace &ws, int dtype,
+                                cudaStream_t st) {
+    return attend::launch_bits<4>(p, ws, dtype, st);
+}
+
+int kv_attend_workers_b4(const KvAttendParams &p, int dtype, int sms) {
+    return attend::workers_bits<4>(p, dtype, sms);
 }
 
 }  // namespace oq

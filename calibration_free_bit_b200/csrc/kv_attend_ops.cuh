@@ -86,68 +86,108 @@ __device__ __forceinline__ Units units_of(const KvAttendParams &p, int b, Seq *s
     return u;
 }
 
-// Total units, by a whole warp; with `first`, the units before each sequence to first[0 .. B].
-template <int TOKENS, int ROWS>
-__device__ __forceinline__ long long count_units(const KvAttendParams &p, long long *first) {
-    const int lane = threadIdx.x & 31;
-    long long base = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        long long n = 0;
-        if (b0 + lane < p.B) {
-            Seq s;
-            const Units u = units_of<TOKENS, ROWS>(p, b0 + lane, &s, first != nullptr);
-            n = (long long)u.tiles * u.segments;
-        }
-        long long sum = n;
-#pragma unroll
-        for (int k = 1; k < 32; k <<= 1) {
-            const long long o = __shfl_up_sync(0xffffffffu, sum, k);
-            sum += lane >= k ? o : 0;
-        }
-        if (first != nullptr && b0 + lane < p.B)
-            first[b0 + lane] = base + sum - n;
-        base += __shfl_sync(0xffffffffu, sum, 31);
-    }
-    if (first != nullptr && lane == 0)
-        first[p.B] = base;
-    return base;
-}
-
-// The sequence that unit u is in, by a whole warp, and the units before it.
-template <int TOKENS, int ROWS>
-__device__ __forceinline__ int find_sequence(const KvAttendParams &p, long long u,
-                                             long long *before) {
-    const int lane = threadIdx.x & 31;
-    long long base = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        long long n = 0;
-        if (b0 + lane < p.B) {
-            Seq s;
-            const Units w = units_of<TOKENS, ROWS>(p, b0 + lane, &s, false);
-            n = (long long)w.tiles * w.segments;
-        }
-        long long sum = n;
-#pragma unroll
-        for (int k = 1; k < 32; k <<= 1) {
-            const long long o = __shfl_up_sync(0xffffffffu, sum, k);
-            sum += lane >= k ? o : 0;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, base + sum > u);
-        if (past) {
-            const int at = __ffs(past) - 1;
-            *before = base + __shfl_sync(0xffffffffu, sum - n, at);
-            return b0 + at;
-        }
-        base += __shfl_sync(0xffffffffu, sum, 31);
-    }
-    *before = base;
-    return p.B;
-}
-
 // Workers that share U units: `most`, fewer while one has less than `least` units.
 __device__ __forceinline__ long long workers_for(long long U, int most, int least) {
     const long long w = (U + least - 1) / least;
     return w < 1 ? 1 : (w < most ? w : most);
+}
+
+// A worker's range of units, and the sequence that it starts in (with the units before that).
+struct Walk {
+    long long u, u1, before;
+    int b;
+};
+
+// Worker `worker`'s range, by a whole warp.  With `tell`, the units before each sequence go to
+// ws.first[0 .. B] and unusable sequences are reported: one warp of the launch does that.
+template <int TOKENS, int ROWS>
+__device__ __forceinline__ Walk take_range(const KvAttendParams &p, const KvAttendSpace &ws,
+                                           long long worker, bool tell) {
+    const int lane = threadIdx.x & 31, each = (p.B + 31) / 32;
+    auto count = [&](int b, bool t) -> long long {
+        if (b >= p.B)
+            return 0;
+        Seq s;
+        const Units u = units_of<TOKENS, ROWS>(p, b, &s, t);
+        return (long long)u.tiles * u.segments;
+    };
+    // a lane has `each` sequences in a row
+    long long mine = 0;
+    for (int k = 0; k < each; ++k)
+        mine += count(lane * each + k, tell);
+    long long upto = mine;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, upto, k);
+        upto += lane >= k ? o : 0;
+    }
+    const long long U = __shfl_sync(0xffffffffu, upto, 31);
+    if (tell) {
+        long long at = upto - mine;
+        for (int k = 0; k < each && lane * each + k < p.B; ++k) {
+            ws.first[lane * each + k] = at;
+            at += count(lane * each + k, false);
+        }
+        if (lane == 0)
+            ws.first[p.B] = U;
+    }
+    const long long W = workers_for(U, ws.most, ws.least);
+    Walk w = {0, 0, 0, 0};
+    if (worker >= W || U == 0)
+        return w;
+    w.u = worker * U / W;
+    w.u1 = (worker + 1) * U / W;
+    const int owner = __ffs(__ballot_sync(0xffffffffu, upto > w.u)) - 1;
+    w.before = __shfl_sync(0xffffffffu, upto - mine, owner);
+    // within the owner's sequences, 32 at a time
+    for (int b0 = owner * each;; b0 += 32) {
+        const bool in = b0 + lane < (owner + 1) * each;
+        const long long n = in ? count(b0 + lane, false) : 0;
+        long long sum = n;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+            const long long o = __shfl_up_sync(0xffffffffu, sum, k);
+            sum += lane >= k ? o : 0;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, w.before + sum > w.u);
+        if (past) {
+            const int at = __ffs(past) - 1;
+            w.before += __shfl_sync(0xffffffffu, sum - n, at);
+            w.b = b0 + at;
+            return w;
+        }
+        w.before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+}
+
+// The next piece of a range: a run of tiles of one segment.
+struct Piece {
+    Seq s;
+    int b, seg, tile0, n, kvh, row_base, nrows, total;
+};
+template <int TOKENS, int ROWS>
+__device__ __forceinline__ bool next_piece(const KvAttendParams &p, Walk &w, Piece &q) {
+    while (w.u < w.u1) {
+        const Units un = units_of<TOKENS, ROWS>(p, w.b, &q.s, false);
+        const long long all = (long long)un.tiles * un.segments;
+        if (w.u >= w.before + all) {
+            w.before += all;
+            ++w.b;
+            continue;
+        }
+        q.b = w.b;
+        q.seg = (int)((w.u - w.before) / un.tiles);
+        q.tile0 = (int)((w.u - w.before) - (long long)q.seg * un.tiles);
+        q.n = (int)min((long long)(un.tiles - q.tile0), w.u1 - w.u);
+        const int row_tiles = un.segments / p.c.kv_heads;
+        q.kvh = q.seg / row_tiles;
+        q.row_base = (q.seg - q.kvh * row_tiles) * ROWS;
+        q.nrows = min(ROWS, q.s.nodes * p.group - q.row_base);
+        q.total = q.s.prefix + q.s.nodes;
+        w.u += q.n;
+        return true;
+    }
+    return false;
 }
 
 }  // namespace attend

@@ -80,11 +80,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-struct Work {
-    long long u0, u1, before;
-    int b;
-};
-
 }  // namespace wide
 
 template <class E, int BITS>
@@ -99,7 +94,7 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
     auto bar = [&](int i) { return bars + 8u * i; };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + S::bars_at + 112);
     volatile int *gone = reinterpret_cast<volatile int *>(sm + S::bars_at + 116);
-    Work *work = reinterpret_cast<Work *>(sm + S::work_at);
+    Walk *work = reinterpret_cast<Walk *>(sm + S::work_at);
     float *vn_s = reinterpret_cast<float *>(sm + S::vn_at);
     float *kexp_s = reinterpret_cast<float *>(sm + S::kexp_at);
     float *vmax_s = reinterpret_cast<float *>(sm + S::vmax_at);
@@ -129,15 +124,7 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(smem_u32(tmem_slot)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-        const long long U =
-            count_units<kTokens, kRows>(p, blockIdx.x == 0 ? ws.first : nullptr);
-        const long long W = workers_for(U, gridDim.x, ws.least);
-        Work w = {0, 0, 0, 0};
-        if (blockIdx.x < W) {
-            w.u0 = blockIdx.x * U / W;
-            w.u1 = (blockIdx.x + 1) * U / W;
-            w.b = find_sequence<kTokens, kRows>(p, w.u0, &w.before);
-        }
+        const Walk w = take_range<kTokens, kRows>(p, ws, blockIdx.x, blockIdx.x == 0);
         if (lane == 0)
             *work = w;
     }
@@ -155,52 +142,20 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
         }
     };
 
-    // The pieces of this worker's range, one after another, as every warp sees them.
-    struct Piece {
-        Seq s;
-        int b, seg, tile0, n, kvh, row_base, nrows, total;
-    };
-    struct Walk {
-        long long u, u1, before;
-        int b;
-    };
-    auto next = [&](Walk &w, Piece &q) -> bool {
-        while (w.u < w.u1) {
-            const Units un = units_of<kTokens, kRows>(p, w.b, &q.s, false);
-            const long long all = (long long)un.tiles * un.segments;
-            if (w.u >= w.before + all) {
-                w.before += all;
-                ++w.b;
-                continue;
-            }
-            q.b = w.b;
-            q.seg = (int)((w.u - w.before) / un.tiles);
-            q.tile0 = (int)((w.u - w.before) - (long long)q.seg * un.tiles);
-            q.n = (int)min((long long)(un.tiles - q.tile0), w.u1 - w.u);
-            const int row_tiles = un.segments / p.c.kv_heads;
-            q.kvh = q.seg / row_tiles;
-            q.row_base = (q.seg - q.kvh * row_tiles) * kRows;
-            q.nrows = min(kRows, q.s.nodes * p.group - q.row_base);
-            q.total = q.s.prefix + q.s.nodes;
-            w.u += q.n;
-            return true;
-        }
-        return false;
-    };
     auto meet = [&] {
         __syncwarp();
         tc_fence_before();
         asm volatile("bar.sync 0, %0;" ::"n"(kWorking) : "memory");
         tc_fence_after();
     };
-    Walk walk = {work->u0, work->u1, work->before, work->b};
+    Walk walk = *work;
     Piece q;
     uint32_t used[2] = {0, 0};                       // units so far of either group
 
     if (warp < kSoftWarps) {
         // ---------------- softmax: group `me` has units me, me + 2, ... ----------------
         uint32_t pieces = 0;
-        while (next(walk, q)) {
+        while (next_piece<kTokens, kRows>(p, walk, q)) {
             const Seq &s = q.s;
             const int n = q.n, tile0 = q.tile0, nrows = q.nrows;
             // the rotation to K's first stage (the raw queries go to V's)
@@ -460,7 +415,7 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
     } else if (warp < kSoftWarps + kDecWarps) {
         // ---------------- decoders: half a token's key row or value row a thread ----------------
         const int dt = threadIdx.x - 32 * kSoftWarps;
-        while (next(walk, q)) {
+        while (next_piece<kTokens, kRows>(p, walk, q)) {
             const int n = q.n, tile0 = q.tile0, total = q.total, kvh = q.kvh, b = q.b;
             const int ch = dt & 15;
 #pragma unroll
@@ -597,7 +552,7 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
         const int which = warp - kSoftWarps - kDecWarps;
         if (which >= 2)
             return;
-        while (next(walk, q)) {
+        while (next_piece<kTokens, kRows>(p, walk, q)) {
             const int n = q.n;
             meet();
             if (which == 0 && lane == 0) {
