@@ -27,6 +27,9 @@
 // 2^14: what a token adds is resolved down to 2^-31 of the largest.  With SPLIT (fp16 outputs) query
 // and weights enter as a sum of two fp16 numbers, so that only the centroids' rounding is left.
 #pragma once
+#ifndef KW
+#define KW 16
+#endif
 
 #include "kv_attend_ops.cuh"
 #include "kv_internal.h"
@@ -65,7 +68,7 @@ template <int D, int BITS> struct Shape {
     static constexpr int vu = v_shared ? 2 : vw;      // words used
 };
 
-// One step's 16 tokens: codes and norms as this lane needs them.
+// One unit's 16 tokens: codes and norms as this lane needs them.
 template <int D, int BITS> struct Tile {
     using S = Shape<D, BITS>;
     uint32_t k[2][S::kw];        // key rows of tokens g, g + 8: elements c D/4 ..
@@ -73,42 +76,37 @@ template <int D, int BITS> struct Tile {
     float kn[2], vn[2];          // norms of tokens g, g + 8
     bool ok;                     // the page exists
 
-    __device__ __forceinline__ void load(const KvAttendParams &p, int page, int at, int kvh, int g,
+    // (codes of a missing page stay as they are: they are not seen, and the norms are 0)
+    __device__ __forceinline__ void keys(const KvAttendParams &p, int page, int at, int kvh, int g,
                                          int c) {
         ok = page >= 0 && page < p.c.pages;
-        if (!ok) {
+        kn[0] = kn[1] = vn[0] = vn[1] = 0.f;
+        if (ok) {
+            const long long row = (((long long)page * p.c.kv_heads + kvh) << p.c.page_log2) + at;
+            const uint8_t *kr = p.c.codes[0] + row * S::row_bytes + g * S::row_bytes + c * S::k_bytes;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                kn[i] = vn[i] = 0.f;
-#pragma unroll
-                for (int j = 0; j < S::kw; ++j)
-                    k[i][j] = 0;
+                load_words<S::kw, S::k_bytes>(k[i], kr + 8 * i * S::row_bytes);
+                kn[i] = __ldg(p.c.norms[0] + row + g + 8 * i);
+                vn[i] = __ldg(p.c.norms[1] + row + g + 8 * i);
             }
+        }
+    }
+    __device__ __forceinline__ void values(const KvAttendParams &p, int page, int at, int kvh,
+                                           int g, int c) {
+        if (page >= 0 && page < p.c.pages) {
+            const long long row = (((long long)page * p.c.kv_heads + kvh) << p.c.page_log2) + at;
+            const uint8_t *vr = p.c.codes[1] + row * S::row_bytes + 2 * c * S::row_bytes +
+                                (S::v_shared ? g >> 1 : g) * S::v_bytes;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < S::vw; ++j)
-                    v[i][j] = 0;
-            return;
+                load_words<S::vw, S::v_bytes>(v[i],
+                                              vr + ((i & 1) + 8 * (i >> 1)) * S::row_bytes);
         }
-        const long long row = (((long long)page * p.c.kv_heads + kvh) << p.c.page_log2) + at;
-        const uint8_t *kr = p.c.codes[0] + row * S::row_bytes;
-        const uint8_t *vr = p.c.codes[1] + row * S::row_bytes;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            load_words<S::kw, S::k_bytes>(k[i], kr + (g + 8 * i) * S::row_bytes + c * S::k_bytes);
-            kn[i] = __ldg(p.c.norms[0] + row + g + 8 * i);
-            vn[i] = __ldg(p.c.norms[1] + row + g + 8 * i);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            load_words<S::vw, S::v_bytes>(
-                v[i], vr + (2 * c + (i & 1) + 8 * (i >> 1)) * S::row_bytes +
-                          (S::v_shared ? g >> 1 : g) * S::v_bytes);
     }
 
     // The words of value row i that hold this lane's elements.
-    __device__ __forceinline__ void values(int i, int g, uint32_t (&w)[S::vu]) const {
+    __device__ __forceinline__ void share(int i, int g, uint32_t (&w)[S::vu]) const {
         if constexpr (S::v_shared) {                 // 48 of 96 bits
             w[0] = (g & 1) ? (v[i][1] >> 16) | (v[i][2] << 16) : v[i][0];
             w[1] = (g & 1) ? v[i][2] >> 16 : v[i][1];
@@ -122,16 +120,14 @@ template <int D, int BITS> struct Tile {
 
 template <int D, int BITS, int NT, bool SPLIT> struct Smem {
     // Warps of the one CTA on an SM: as many as its registers hold.
-    static constexpr int warps = D == 128 && NT == 1 ? (SPLIT || BITS == 8 ? 12 : 16) : 8;
+    static constexpr int warps = D == 128 && NT == 1 ? (SPLIT || BITS == 8 ? 12 : KW) : 8;   // KW
     static constexpr int rows = 8 * NT;
     // queries stay in shared memory where registers do not hold them beside the accumulators
     static constexpr bool q_shared = D == 256 && NT == 2;
-    static constexpr int q_half = rows * D;                                  // halves
-    // a warp's own: queries, a row being rotated, masks, score factors
-    static constexpr int x_at = q_half * 2 * (SPLIT ? 2 : 1);
-    static constexpr int mask_at = x_at + D * 4;
-    static constexpr int scale_at = mask_at + rows * 8;
-    static constexpr int own = (scale_at + rows * 4 + 15) / 16 * 16;
+    static constexpr int q_words = rows * D / 4 * (SPLIT ? 2 : 1);           // uint2
+    // a warp's own: queries (q_shared) and masks
+    static constexpr int mask_at = q_shared ? q_words * 8 : 0;
+    static constexpr int own = mask_at + rows * 8;
     static constexpr int bytes = Lut<BITS, true>::bytes + warps * own;
 };
 
@@ -140,99 +136,41 @@ __global__ void __launch_bounds__(32 * Smem<D, BITS, NT, SPLIT>::warps, 1)
 attend_tiles(const KvAttendParams p, const KvAttendSpace ws) {
     using S = Shape<D, BITS>;
     using M = Smem<D, BITS, NT, SPLIT>;
-    constexpr int N = D / 32, KS = D / 16;
+    constexpr int KS = D / 16;
     extern __shared__ __align__(128) unsigned char sm[];
     unsigned char *lut = sm;
 
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     unsigned char *own = sm + Lut<BITS, true>::bytes + warp * M::own;
-    __half *qh = reinterpret_cast<__half *>(own);
-    float *xs = reinterpret_cast<float *>(own + M::x_at);
     unsigned long long *masks = reinterpret_cast<unsigned long long *>(own + M::mask_at);
-    float *qscale = reinterpret_cast<float *>(own + M::scale_at);
     fill_lut<BITS, true>(lut, p.lut);
-    uint32_t ent[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        ent[i] = p.ent[lane * N + i];
     __syncthreads();
     pdl_wait();
     const uint32_t col = lut_column<BITS>(lane);
     // neighbouring workers on different SMs: few units reach all of them
     const long long worker = (long long)warp * gridDim.x + blockIdx.x;
-    Walk walk = take_range<16, M::rows>(p, ws, worker, worker == 0);
+    Walk walk = take_range(p, ws, worker);
     Piece piece;
-    while (next_piece<16, M::rows>(p, walk, piece)) {
+    while (next_piece<NarrowForm<NT>>(p, walk, piece)) {
     const Seq &s = piece.s;
-    const int kvh = piece.kvh, row_base = piece.row_base, nrows = piece.nrows;
-    // the first tiles are on their way while the queries are rotated
+    const int kvh = piece.kvh, nrows = piece.nrows;
     const int last = piece.tile0 + piece.n;
     const int *table = p.table + (long long)piece.b * p.table_width;
     const int in_page = (1 << p.c.page_log2) - 1;
     int t = piece.tile0;
-    Tile<D, BITS> ping, pong;
-    int page = 0;
+    Tile<D, BITS> cur;
     bool bad_page = false;
-    ping.load(p, table[(t << 4) >> p.c.page_log2], (t << 4) & in_page, kvh, g, c);
-    if (t + 1 < last)
-        page = table[((t + 1) << 4) >> p.c.page_log2];
+    // a tile's place: its page now, where its rows are when they are loaded
+    auto place = [&](int t) -> int { return t < last ? __ldg(table + ((t << 4) >> p.c.page_log2)) : -1; };
+    int page = place(t), page1 = place(t + 1);
+    cur.keys(p, page, (t << 4) & in_page, kvh, g, c);
+    cur.values(p, page, (t << 4) & in_page, kvh, g, c);
 
-    // ---- rotated queries, fp16 over a power of two a row ----
-    __syncwarp();
-    for (int r = 0; r < M::rows; ++r) {
-        float z[N];
-        if (r < nrows) {
-            const int node = (row_base + r) / p.group, e = (row_base + r) - node * p.group;
-            const long long row = s.row0 + node;
-            const E *q = static_cast<const E *>(p.q) + row * p.q_stride + (kvh * p.group + e) * D;
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                xs[i * 32 + lane] = to_f32(q[i * 32 + lane]);
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float v = xs[ent[i] & 0x7fffu];
-                z[i] = (ent[i] & 0x8000u) ? -v : v;
-            }
-            warp_wht<D>(z, p.h, lane);
-            if (lane == 0)
-                masks[r] = p.mask ? (unsigned long long)p.mask[row] : (2ull << node) - 1ull;
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                z[i] = 0.f;
-            if (lane == 0)
-                masks[r] = 0;
-        }
-        float big = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            big = fmaxf(big, fabsf(z[i]));
-#pragma unroll
-        for (int k = 16; k; k >>= 1)
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, k));
-        // 2^e <= big < 2^(e+1); values over 2^e stay below 2 (2^e and its inverse are normal)
-        uint32_t ex = (__float_as_uint(big) >> 23) & 255u;
-        ex = ex < 1u ? 1u : (ex > 253u ? 253u : ex);
-        const float up = __uint_as_float(ex << 23), down = __uint_as_float((254u - ex) << 23);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float v = z[i] * down;
-            const __half hi = __float2half_rn(v);
-            // as the lanes take it: [row / 8][step][lane][4], lane = 4 (row % 8) + quarter
-            const int x = lane * N + i, y = x % (D / 4);
-            const int to = (((r >> 3) * KS + (y >> 2)) * 32 + (r & 7) * 4 + x / (D / 4)) * 4 + (y & 3);
-            qh[to] = hi;
-            if constexpr (SPLIT)
-                qh[M::q_half + to] = __float2half_rn(v - __half2float(hi));
-        }
-        if (lane == 0)
-            qscale[r] = up * p.qk_scale;
-        __syncwarp();
-    }
-    // B operands of S^T = K Q^T: row n = g, elements c D/4 + 4 ks + {0, 1}, {2, 3}
-    const uint2 *qsm = reinterpret_cast<const uint2 *>(qh) + lane;
+    // B operands of S^T = K Q^T: row n = g, elements c D/4 + 4 ks + {0, 1}, {2, 3} (rotate_queries)
+    const long long sigma = (long long)piece.b * ws.segments + piece.seg;
+    const uint2 *qg = ws.queries + sigma * M::q_words + lane;
+    const uint2 *qsm = reinterpret_cast<const uint2 *>(own) + lane;
     uint2 qf[M::q_shared ? 1 : NT][M::q_shared ? 1 : KS];
     uint2 ql[SPLIT && !M::q_shared ? NT : 1][SPLIT && !M::q_shared ? KS : 1];
     if constexpr (!M::q_shared) {
@@ -240,17 +178,29 @@ attend_tiles(const KvAttendParams p, const KvAttendSpace ws) {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                qf[n][ks] = qsm[(n * KS + ks) * 32];
+                qf[n][ks] = __ldcg(qg + (n * KS + ks) * 32);
                 if constexpr (SPLIT)
-                    ql[n][ks] = qsm[M::q_half / 4 + (n * KS + ks) * 32];
+                    ql[n][ks] = __ldcg(qg + ((NT + n) * KS + ks) * 32);
             }
+    } else {
+        __syncwarp();
+        for (int i = 0; i < M::q_words / 32; ++i)
+            reinterpret_cast<uint2 *>(own)[i * 32 + lane] = __ldcg(qg + i * 32);
     }
     float qs[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        qs[n][0] = qscale[8 * n + 2 * c];
-        qs[n][1] = qscale[8 * n + 2 * c + 1];
+        qs[n][0] = __ldcg(ws.factors + sigma * M::rows + 8 * n + 2 * c);
+        qs[n][1] = __ldcg(ws.factors + sigma * M::rows + 8 * n + 2 * c + 1);
     }
+    __syncwarp();
+    if (lane < M::rows) {
+        const int node = (piece.row_base + lane) / p.group;
+        masks[lane] = lane >= nrows ? 0ull
+                      : p.mask      ? (unsigned long long)p.mask[s.row0 + node]
+                                    : (2ull << node) - 1ull;
+    }
+    __syncwarp();
 
     float acc[NT][KS][4];
     float m[NT][2], l[NT][2];                     // reference and sum
@@ -267,8 +217,8 @@ attend_tiles(const KvAttendParams p, const KvAttendSpace ws) {
             m[n][i] = kNone, l[n][i] = 0.f, vs[n][i] = 0.f, vinv[n][i] = 0.f;
     }
 
-    // One step: 16 tokens from token 16 t on.
-    auto step = [&](const Tile<D, BITS> &cur, int t) {
+    for (; t < last; ++t) {
+        const int page2 = place(t + 2);
         // S^T = K Q^T
         float st[NT][4];
 #pragma unroll
@@ -287,12 +237,17 @@ attend_tiles(const KvAttendParams p, const KvAttendSpace ws) {
                                       : qf[M::q_shared ? 0 : n][M::q_shared ? 0 : ks];
                 mma16816(st[n], a, q.x, q.y);
                 if constexpr (SPLIT) {
-                    q = M::q_shared ? qsm[M::q_half / 4 + (n * KS + ks) * 32]
+                    q = M::q_shared ? qsm[((NT + n) * KS + ks) * 32]
                                     : ql[M::q_shared ? 0 : n][M::q_shared ? 0 : ks];
                     mma16816(st[n], a, q.x, q.y);
                 }
             }
         }
+        // the next unit's keys are under way from here, its values from the end of this one: each a
+        // part of a unit ahead of its use, in the registers that this unit has done with
+        const float kn[2] = {cur.kn[0], cur.kn[1]}, vn[2] = {cur.vn[0], cur.vn[1]};
+        const bool ok = cur.ok;
+        cur.keys(p, page1, ((t + 1) << 4) & in_page, kvh, g, c);
         // scores of tokens g, g + 8 and rows 2c, 2c + 1, in powers of two
         bool grow = false;
         const int tok = t << 4;
@@ -300,23 +255,23 @@ attend_tiles(const KvAttendParams p, const KvAttendSpace ws) {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                st[n][i] *= cur.kn[i >> 1] * qs[n][i & 1];
-        if (!cur.ok || tok + 16 > s.prefix) {             // the page is missing, or the tile has nodes
-            bad_page |= !cur.ok;
+                st[n][i] *= kn[i >> 1] * qs[n][i & 1];
+        if (!ok || tok + 16 > s.prefix) {             // the page is missing, or the tile has nodes
+            bad_page |= !ok;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int node = tok + g + 8 * (i >> 1) - s.prefix;
-                    const bool see = cur.ok && (node < 0 || (node < s.nodes &&
+                    const bool see = ok && (node < 0 || (node < s.nodes &&
                                      ((masks[8 * n + 2 * c + (i & 1)] >> node) & 1ull)));
                     if (!see)
                         st[n][i] = -CUDART_INF_F;
                     else
-                        grow |= cur.vn[i >> 1] > vs[n][i & 1];
+                        grow |= vn[i >> 1] > vs[n][i & 1];
                 }
         } else {
-            const float v = fmaxf(cur.vn[0], cur.vn[1]);
+            const float v = fmaxf(vn[0], vn[1]);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 grow |= v > vs[n][0] || v > vs[n][1];
@@ -333,8 +288,8 @@ attend_tiles(const KvAttendParams p, const KvAttendSpace ws) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     float up = fmaxf(st[n][i], st[n][2 + i]);
-                    float v = fmaxf(st[n][i] > -CUDART_INF_F ? cur.vn[0] : 0.f,
-                                    st[n][2 + i] > -CUDART_INF_F ? cur.vn[1] : 0.f);
+                    float v = fmaxf(st[n][i] > -CUDART_INF_F ? vn[0] : 0.f,
+                                    st[n][2 + i] > -CUDART_INF_F ? vn[1] : 0.f);
 #pragma unroll
                     for (int k = 4; k < 32; k <<= 1) {
                         up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, k));
@@ -370,9 +325,9 @@ attend_tiles(const KvAttendParams p, const KvAttendSpace ws) {
             for (int i = 0; i < 4; ++i) {
                 const float e = ex2(st[n][i] - m[n][i & 1]);
                 l[n][i & 1] += e;
-                w[i] = e * (cur.vn[i >> 1] * vinv[n][i & 1]);
+                w[i] = e * (vn[i >> 1] * vinv[n][i & 1]);
             }
-            if (!cur.ok || tok + 16 > s.prefix) {         // what is not seen may have any norm
+            if (!ok || tok + 16 > s.prefix) {         // what is not seen may have any norm
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (st[n][i] == -CUDART_INF_F)
@@ -390,7 +345,7 @@ attend_tiles(const KvAttendParams p, const KvAttendSpace ws) {
         uint32_t vw[4][S::vu];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            cur.values(i, g, vw[i]);
+            cur.share(i, g, vw[i]);
         mixed<BITS>(vw[0], vw[1]);
         mixed<BITS>(vw[2], vw[3]);
 #pragma unroll
@@ -409,22 +364,8 @@ attend_tiles(const KvAttendParams p, const KvAttendSpace ws) {
                 }
             }
         }
-    };
-    // the tile after t, and the page of the one after that
-    auto fetch = [&](Tile<D, BITS> &to, int t) {
-        if (t + 1 < last) {
-            to.load(p, page, ((t + 1) << 4) & in_page, kvh, g, c);
-            if (t + 2 < last)
-                page = table[((t + 2) << 4) >> p.c.page_log2];
-        }
-    };
-    for (; t < last; t += 2) {
-        fetch(pong, t);
-        step(ping, t);
-        if (t + 1 >= last)
-            break;
-        fetch(ping, t + 1);
-        step(pong, t + 1);
+        cur.values(p, page1, ((t + 1) << 4) & in_page, kvh, g, c);
+        page1 = page2;
     }
     if (bad_page && lane == 0)
         atomicOr(p.err, AT_ERR_PAGE);

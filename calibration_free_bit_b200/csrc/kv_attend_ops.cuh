@@ -68,22 +68,26 @@ constexpr float kNone = -1e30f;                      // reference of a row that 
 
 // ---- work lists ----
 // A segment is one sequence's tile of rows of one key head; its units are the sequence's tiles of
-// tokens.  The units of all segments in a row (sequence, key head, row tile) are shared out evenly
-// to W workers, a contiguous range each, whatever the lengths: worker w has units w U / W to
-// (w + 1) U / W.  A worker's part of a segment is a piece; piece (segment s, worker w) has slot
-// s + w of the workspace (one of the two grows from a piece to the next, so slots are distinct),
-// where segments count as if every sequence had the most rows.
+// tokens, and before them `Extra` that stand for the time that a segment's setting up takes.  The
+// units of all segments in a row (sequence, key head, row tile) are shared out evenly to W workers,
+// a contiguous range each, whatever the lengths: worker w has units w U / W to (w + 1) U / W.  What
+// a worker has of a segment's tiles is a piece; piece (segment s, worker w) has slot s + w of the
+// workspace (one of the two grows from a piece to the next, so slots are distinct), where segments
+// count as if every sequence had the most rows.
 struct Units {
     int tiles, segments;          // of one sequence; 0 segments: nothing to do
 };
-template <int TOKENS, int ROWS>
+template <class Form>             // Form::tokens, rows, extra
 __device__ __forceinline__ Units units_of(const KvAttendParams &p, int b, Seq *s, bool tell) {
     Units u = {0, 0};
     if (load_seq(p, b, s, tell) && s->nodes > 0) {
-        u.tiles = (s->prefix + s->nodes + TOKENS - 1) / TOKENS;
-        u.segments = p.c.kv_heads * ((s->nodes * p.group + ROWS - 1) / ROWS);
+        u.tiles = (s->prefix + s->nodes + Form::tokens - 1) / Form::tokens;
+        u.segments = p.c.kv_heads * ((s->nodes * p.group + Form::rows - 1) / Form::rows);
     }
     return u;
+}
+template <class Form> __device__ __forceinline__ long long all_units(const Units &u) {
+    return (long long)(u.tiles + Form::extra) * u.segments;
 }
 
 // Workers that share U units: `most`, fewer while one has less than `least` units.
@@ -92,72 +96,60 @@ __device__ __forceinline__ long long workers_for(long long U, int most, int leas
     return w < 1 ? 1 : (w < most ? w : most);
 }
 
-// A worker's range of units, and the sequence that it starts in (with the units before that).
-struct Walk {
-    long long u, u1, before;
-    int b;
-};
-
-// Worker `worker`'s range, by a whole warp.  With `tell`, the units before each sequence go to
-// ws.first[0 .. B] and unusable sequences are reported: one warp of the launch does that.
-template <int TOKENS, int ROWS>
-__device__ __forceinline__ Walk take_range(const KvAttendParams &p, const KvAttendSpace &ws,
-                                           long long worker, bool tell) {
-    const int lane = threadIdx.x & 31, each = (p.B + 31) / 32;
-    auto count = [&](int b, bool t) -> long long {
-        if (b >= p.B)
-            return 0;
-        Seq s;
-        const Units u = units_of<TOKENS, ROWS>(p, b, &s, t);
-        return (long long)u.tiles * u.segments;
-    };
-    // a lane has `each` sequences in a row
-    long long mine = 0;
-    for (int k = 0; k < each; ++k)
-        mine += count(lane * each + k, tell);
-    long long upto = mine;
-#pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, upto, k);
-        upto += lane >= k ? o : 0;
-    }
-    const long long U = __shfl_sync(0xffffffffu, upto, 31);
-    if (tell) {
-        long long at = upto - mine;
-        for (int k = 0; k < each && lane * each + k < p.B; ++k) {
-            ws.first[lane * each + k] = at;
-            at += count(lane * each + k, false);
+// By one warp of a launch: the units before each sequence to ws.first[0 .. B], and unusable
+// sequences are reported.
+template <class Form>
+__device__ __forceinline__ void list_units(const KvAttendParams &p, const KvAttendSpace &ws) {
+    const int lane = threadIdx.x & 31;
+    long long base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        long long n = 0;
+        if (b0 + lane < p.B) {
+            Seq s;
+            n = all_units<Form>(units_of<Form>(p, b0 + lane, &s, true));
         }
-        if (lane == 0)
-            ws.first[p.B] = U;
-    }
-    const long long W = workers_for(U, ws.most, ws.least);
-    Walk w = {0, 0, 0, 0};
-    if (worker >= W || U == 0)
-        return w;
-    w.u = worker * U / W;
-    w.u1 = (worker + 1) * U / W;
-    const int owner = __ffs(__ballot_sync(0xffffffffu, upto > w.u)) - 1;
-    w.before = __shfl_sync(0xffffffffu, upto - mine, owner);
-    // within the owner's sequences, 32 at a time
-    for (int b0 = owner * each;; b0 += 32) {
-        const bool in = b0 + lane < (owner + 1) * each;
-        const long long n = in ? count(b0 + lane, false) : 0;
         long long sum = n;
 #pragma unroll
         for (int k = 1; k < 32; k <<= 1) {
             const long long o = __shfl_up_sync(0xffffffffu, sum, k);
             sum += lane >= k ? o : 0;
         }
-        const unsigned past = __ballot_sync(0xffffffffu, w.before + sum > w.u);
-        if (past) {
-            const int at = __ffs(past) - 1;
-            w.before += __shfl_sync(0xffffffffu, sum - n, at);
-            w.b = b0 + at;
-            return w;
-        }
-        w.before += __shfl_sync(0xffffffffu, sum, 31);
+        if (b0 + lane < p.B)
+            ws.first[b0 + lane] = base + sum - n;
+        base += __shfl_sync(0xffffffffu, sum, 31);
     }
+    if (lane == 0)
+        ws.first[p.B] = base;
+}
+
+// A worker's range of units, and the sequence that it starts in (with the units before that).
+struct Walk {
+    long long u, u1, before;
+    int b;
+};
+
+// Worker `worker`'s range from ws.first, by a whole warp.
+__device__ __forceinline__ Walk take_range(const KvAttendParams &p, const KvAttendSpace &ws,
+                                           long long worker) {
+    const int lane = threadIdx.x & 31;
+    const long long U = ws.first[p.B], W = workers_for(U, ws.most, ws.least);
+    Walk w = {0, 0, 0, 0};
+    if (worker >= W || U == 0)
+        return w;
+    w.u = worker * U / W;
+    w.u1 = (worker + 1) * U / W;
+    // the last sequence with first[b] <= u, in [lo, hi): 32 places at a time
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32;
+        const int at = lo + lane * step;
+        const unsigned in = __ballot_sync(0xffffffffu, at < hi && ws.first[at < hi ? at : lo] <= w.u);
+        lo += (31 - __clz(in)) * step;                // lane 0's place always is
+        hi = min(hi, lo + step);
+    }
+    w.b = lo;
+    w.before = ws.first[lo];
+    return w;
 }
 
 // The next piece of a range: a run of tiles of one segment.
@@ -165,30 +157,43 @@ struct Piece {
     Seq s;
     int b, seg, tile0, n, kvh, row_base, nrows, total;
 };
-template <int TOKENS, int ROWS>
+template <class Form>
 __device__ __forceinline__ bool next_piece(const KvAttendParams &p, Walk &w, Piece &q) {
     while (w.u < w.u1) {
-        const Units un = units_of<TOKENS, ROWS>(p, w.b, &q.s, false);
-        const long long all = (long long)un.tiles * un.segments;
+        const Units un = units_of<Form>(p, w.b, &q.s, false);
+        const long long all = all_units<Form>(un);
         if (w.u >= w.before + all) {
             w.before += all;
             ++w.b;
             continue;
         }
+        const int len = un.tiles + Form::extra;
         q.b = w.b;
-        q.seg = (int)((w.u - w.before) / un.tiles);
-        q.tile0 = (int)((w.u - w.before) - (long long)q.seg * un.tiles);
-        q.n = (int)min((long long)(un.tiles - q.tile0), w.u1 - w.u);
+        q.seg = (int)((w.u - w.before) / len);
+        const int from = (int)((w.u - w.before) - (long long)q.seg * len);
+        const int n = (int)min((long long)(len - from), w.u1 - w.u);
+        w.u += n;
+        q.tile0 = max(from - Form::extra, 0);
+        q.n = from + n - Form::extra - q.tile0;
+        if (q.n <= 0)
+            continue;                                 // none of its tiles
         const int row_tiles = un.segments / p.c.kv_heads;
         q.kvh = q.seg / row_tiles;
-        q.row_base = (q.seg - q.kvh * row_tiles) * ROWS;
-        q.nrows = min(ROWS, q.s.nodes * p.group - q.row_base);
+        q.row_base = (q.seg - q.kvh * row_tiles) * Form::rows;
+        q.nrows = min(Form::rows, q.s.nodes * p.group - q.row_base);
         q.total = q.s.prefix + q.s.nodes;
-        w.u += q.n;
         return true;
     }
     return false;
 }
+
+// The forms: tiles of many rows (kv_wide.cuh) and of 8 NT (kv_attend.cuh).
+struct WideForm {
+    static constexpr int tokens = 128, rows = 128, extra = 2;
+};
+template <int NT> struct NarrowForm {
+    static constexpr int tokens = 16, rows = 8 * NT, extra = 4;
+};
 
 }  // namespace attend
 }  // namespace oq

@@ -116,13 +116,12 @@ struct KvAttendSpace {
     float *part;                  // [slots][rows][d] sums of a piece's rows
     float *stat;                  // [slots][2][rows] references and weights' sums
     long long *first;             // [B + 1] units before each sequence
+    uint2 *queries;               // few rows: [segments of all][rows of a tile][d] rotated, as the
+                                  // lanes take them (kv_attend.cu, rotate_queries)
+    float *factors;               // [segments of all][rows of a tile] of their scores
     int rows;                     // rows of a slot: the tile's, or all a sequence can have
     int segments;                 // segments of a sequence with the most rows
     int most, least;              // workers, and units that one has at least
-    static size_t stat_at(long long slots, int rows, int d) { return (size_t)slots * rows * d * 4; }
-    static size_t first_at(long long slots, int rows, int d) {
-        return stat_at(slots, rows, d) + ((size_t)slots * rows * 8 + 15) / 16 * 16;
-    }
 };
 // Many rows a key head, heads of 128 (kv_wide.cuh).
 cudaError_t launch_kv_wide(const KvAttendParams &p, const KvAttendSpace &ws, int dtype,

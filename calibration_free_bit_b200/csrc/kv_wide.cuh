@@ -124,7 +124,7 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(smem_u32(tmem_slot)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-        const Walk w = take_range<kTokens, kRows>(p, ws, blockIdx.x, blockIdx.x == 0);
+        const Walk w = take_range(p, ws, blockIdx.x);
         if (lane == 0)
             *work = w;
     }
@@ -155,7 +155,7 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
     if (warp < kSoftWarps) {
         // ---------------- softmax: group `me` has units me, me + 2, ... ----------------
         uint32_t pieces = 0;
-        while (next_piece<kTokens, kRows>(p, walk, q)) {
+        while (next_piece<WideForm>(p, walk, q)) {
             const Seq &s = q.s;
             const int n = q.n, tile0 = q.tile0, nrows = q.nrows;
             // the rotation to K's first stage (the raw queries go to V's)
@@ -415,7 +415,7 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
     } else if (warp < kSoftWarps + kDecWarps) {
         // ---------------- decoders: half a token's key row or value row a thread ----------------
         const int dt = threadIdx.x - 32 * kSoftWarps;
-        while (next_piece<kTokens, kRows>(p, walk, q)) {
+        while (next_piece<WideForm>(p, walk, q)) {
             const int n = q.n, tile0 = q.tile0, total = q.total, kvh = q.kvh, b = q.b;
             const int ch = dt & 15;
 #pragma unroll
@@ -552,7 +552,7 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
         const int which = warp - kSoftWarps - kDecWarps;
         if (which >= 2)
             return;
-        while (next_piece<kTokens, kRows>(p, walk, q)) {
+        while (next_piece<WideForm>(p, walk, q)) {
             const int n = q.n;
             meet();
             if (which == 0 && lane == 0) {
