@@ -11,14 +11,15 @@ namespace {
 __device__ unsigned int g_attend_err;
 
 constexpr int kJoinWarps = 4;
+// Tiles of 16 tokens, over all segments, up to which clusters take a call.
+constexpr long long kNearTiles = 16384;
 
-// Before the other two kernels of a call: its work list and, for tiles of few rows, the rotated
-// queries, one warp a row of a tile (rows that no query fills are zeros).  A query is kept as fp16
-// over the power of two below its largest element; with SPLIT also what that leaves, as fp16.
+// Before the other two kernels of a call with few rows: its work list and the rotated queries, one
+// warp a row of a tile (rows that no query fills are zeros).
 template <class E, int D, int NT, bool SPLIT>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 rotate_queries(const KvAttendParams p, const KvAttendSpace ws) {
-    constexpr int N = D / 32, KS = D / 16, R = 8 * NT;
+    constexpr int N = D / 32, R = 8 * NT;
     __shared__ float xs[kJoinWarps][D];
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
@@ -35,52 +36,13 @@ rotate_queries(const KvAttendParams p, const KvAttendSpace ws) {
     if (seg >= un.segments)
         return;
     const int row_tiles = un.segments / p.c.kv_heads, kvh = seg / row_tiles;
-    const int i0 = (seg - kvh * row_tiles) * R + r;          // of the key head's rows
-    float z[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        z[i] = 0.f;
-    if (i0 < s.nodes * p.group) {
-        const int node = i0 / p.group, e = i0 - node * p.group;
-        const E *q = static_cast<const E *>(p.q) + (long long)(s.row0 + node) * p.q_stride +
-                     (kvh * p.group + e) * D;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            xs[warp][i * 32 + lane] = to_f32(q[i * 32 + lane]);
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float v = xs[warp][ent[i] & 0x7fffu];
-            z[i] = (ent[i] & 0x8000u) ? -v : v;
-        }
-        warp_wht<D>(z, p.h, lane);
-    }
-    float big = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        big = fmaxf(big, fabsf(z[i]));
-#pragma unroll
-    for (int k = 16; k; k >>= 1)
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, k));
-    // 2^e <= big < 2^(e+1); values over 2^e stay below 2 (2^e and its inverse are normal)
-    uint32_t ex = (__float_as_uint(big) >> 23) & 255u;
-    ex = ex < 1u ? 1u : (ex > 253u ? 253u : ex);
-    const float up = __uint_as_float(ex << 23), down = __uint_as_float((254u - ex) << 23);
+    const int i = (seg - kvh * row_tiles) * R + r;           // of the key head's rows
     const long long sigma = (long long)b * ws.segments + seg;
-    __half *to = reinterpret_cast<__half *>(ws.queries) + sigma * R * D * (SPLIT ? 2 : 1);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const float v = z[i] * down;
-        const __half hi = __float2half_rn(v);
-        // [row / 8][step][lane][4], lane = 4 (row % 8) + quarter of the row
-        const int x = lane * N + i, y = x % (D / 4);
-        const int o = (((r >> 3) * KS + (y >> 2)) * 32 + (r & 7) * 4 + x / (D / 4)) * 4 + (y & 3);
-        to[o] = hi;
-        if constexpr (SPLIT)
-            to[R * D + o] = __float2half_rn(v - __half2float(hi));
-    }
+    const float f = rotate_row<E, D, SPLIT>(
+        p, s, kvh, i, i < s.nodes * p.group, ent, xs[warp], r, NT,
+        reinterpret_cast<__half *>(ws.queries) + sigma * R * D * (SPLIT ? 2 : 1));
     if (lane == 0)
-        ws.factors[sigma * R + r] = up * p.qk_scale;
+        ws.factors[sigma * R + r] = f;
 }
 
 template <class Form>
@@ -90,12 +52,15 @@ __global__ void __launch_bounds__(32) list_work(const KvAttendParams p, const Kv
     list_units<Form>(p, ws);
 }
 
-// One warp a row: o = R^T (sum of its pieces) over the sum of their weights.
-template <class E, int D, class Form>
+// The sum of a row's pieces, and of their weights: WARPS warps take every WARPS-th piece and add up
+// in a fixed order.  One warp a row where there are many rows; four where there are few, which have
+// many pieces.
+template <class E, int D, class Form, int WARPS>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 join_pieces(const KvAttendParams p, const KvAttendSpace ws) {
-    constexpr int N = D / 32;
-    __shared__ float xs[kJoinWarps][D];
+    constexpr int N = D / 32, ROWS = kJoinWarps / WARPS;
+    __shared__ float4 sums[kJoinWarps][D / 4];
+    __shared__ float totals[kJoinWarps];
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
     uint32_t ent[N];
@@ -104,72 +69,82 @@ join_pieces(const KvAttendParams p, const KvAttendSpace ws) {
         ent[i] = p.ent[lane * N + i];
     pdl_wait();
     Seq s;
+    const long long U = ws.first[p.B], first = ws.first[b];
     const Units un = units_of<Form>(p, b, &s, false);
-    const int row = blockIdx.x * kJoinWarps + warp;          // node * q_heads + head
+    const int row = blockIdx.x * ROWS + warp / WARPS;        // node * q_heads + head
     const int node = row / p.q_heads, head = row - node * p.q_heads;
-    if (un.segments == 0 || node >= s.nodes)
+    const bool real = un.segments > 0 && node < s.nodes;
+    if (WARPS == 1 && !real)
         return;
-    const int kvh = head / p.group, at = node * p.group + head - kvh * p.group;
-    const int seg = kvh * (un.segments / p.c.kv_heads) + at / Form::rows, r = at % Form::rows;
-    const long long U = ws.first[p.B], W = workers_for(U, ws.most, ws.least);
-    const long long start = ws.first[b] + (long long)seg * (un.tiles + Form::extra) + Form::extra;
-    // the workers that have its first and its last tile
-    const int w0 = (int)(((start + 1) * W - 1) / U);
-    const int w1 = (int)(((start + un.tiles) * W - 1) / U);
-    const long long slot0 = (long long)b * ws.segments + seg;
-    float mx = kNone;
-    for (int w = w0 + lane; w <= w1; w += 32)
-        mx = fmaxf(mx, ws.stat[(slot0 + w) * 2 * ws.rows + r]);
-#pragma unroll
-    for (int k = 16; k; k >>= 1)
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
     float o[N], sum = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i)
         o[i] = 0.f;
-    // 32 pieces' factors at a time, a lane each; then their rows, eight under way
-    for (int w = w0; w <= w1; w += 32) {
-        float f = 0.f;
-        if (w + lane <= w1) {
-            const float *st = ws.stat + (slot0 + w + lane) * 2 * ws.rows + r;
-            f = ex2(st[0] - mx);
+    const int kvh = head / p.group, at = node * p.group + head - kvh * p.group;
+    if (real) {
+        const int seg = kvh * (un.segments / p.c.kv_heads) + at / Form::rows, r = at % Form::rows;
+        const long long W = workers_for(U, ws.most, ws.least);
+        const long long start = first + (long long)seg * (un.tiles + Form::extra) + Form::extra;
+        // the workers that have its first and its last tile
+        const int w0 = (int)(((start + 1) * W - 1) / U);
+        const int w1 = (int)(((start + un.tiles) * W - 1) / U);
+        const long long slot0 = (long long)b * ws.segments + seg;
+        float mx = kNone;
+        for (int w = w0 + lane; w <= w1; w += 32)
+            mx = fmaxf(mx, ws.stat[(slot0 + w) * 2 * ws.rows + r]);
+#pragma unroll
+        for (int k = 16; k; k >>= 1)
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+#pragma unroll 4
+        for (int w = w0 + warp % WARPS; w <= w1; w += WARPS) {
+            const float *st = ws.stat + (slot0 + w) * 2 * ws.rows + r;
+            const float f = ex2(st[0] - mx);
             sum += f * st[ws.rows];
-        }
-        const int n = min(32, w1 - w + 1);
-        const float *src = ws.part + ((slot0 + w) * ws.rows + r) * D + lane * N;
-#pragma unroll 8
-        for (int k = 0; k < n; ++k) {
-            const float fk = __shfl_sync(0xffffffffu, f, k);
-            const float4 *v4 = reinterpret_cast<const float4 *>(src + (long long)k * ws.rows * D);
+            const float4 *src = reinterpret_cast<const float4 *>(
+                ws.part + ((slot0 + w) * ws.rows + r) * D + lane * N);
 #pragma unroll
             for (int i = 0; i < N; i += 4) {
-                const float4 v = v4[i / 4];
-                o[i] += fk * v.x, o[i + 1] += fk * v.y, o[i + 2] += fk * v.z, o[i + 3] += fk * v.w;
+                const float4 v = src[i / 4];
+                o[i] += f * v.x, o[i + 1] += f * v.y, o[i + 2] += f * v.z, o[i + 3] += f * v.w;
             }
         }
     }
+    if constexpr (WARPS > 1) {
 #pragma unroll
-    for (int k = 16; k; k >>= 1)
-        sum += __shfl_xor_sync(0xffffffffu, sum, k);
-    warp_wht<D>(o, p.h, lane);
-    const float inv = sum == 0.f ? 0.f : p.o_scale / sum;    // nothing seen: zeros
+        for (int i = 0; i < N; i += 4)
+            sums[warp][lane * (N / 4) + i / 4] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        if (lane == 0)
+            totals[warp] = sum;
+        __syncthreads();
+        if (warp % WARPS > 0 || !real)
+            return;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        xs[warp][ent[i] & 0x7fffu] = inv * ((ent[i] & 0x8000u) ? -o[i] : o[i]);
-    __syncwarp();
-    E *y = static_cast<E *>(p.out) + (s.row0 + node) * p.out_stride + head * D;
+        for (int w = 1; w < WARPS; ++w) {
+            sum += totals[warp + w];
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        y[i * 32 + lane] = from_f32<E>(xs[warp][i * 32 + lane]);
+            for (int i = 0; i < N; i += 4) {
+                const float4 v = sums[warp + w][lane * (N / 4) + i / 4];
+                o[i] += v.x, o[i + 1] += v.y, o[i + 2] += v.z, o[i + 3] += v.w;
+            }
+        }
+    }
+    finish_row<E, D>(p, s, kvh, at, ent, reinterpret_cast<float *>(sums[warp]), o, sum);
+}
+
+template <class E, int D, class Form>
+cudaError_t join_as(const KvAttendParams &p, const KvAttendSpace &ws, cudaStream_t st) {
+    const int rows = p.max_nodes * p.q_heads;
+    const dim3 block(32 * kJoinWarps);
+    if ((long long)rows * p.B >= 2048)
+        return launch_pdl(join_pieces<E, D, Form, 1>,
+                          dim3((rows + kJoinWarps - 1) / kJoinWarps, p.B), block, 0, st, p, ws);
+    return launch_pdl(join_pieces<E, D, Form, kJoinWarps>, dim3(rows, p.B), block, 0, st, p, ws);
 }
 
 template <int D, class Form>
 cudaError_t join(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, cudaStream_t st) {
-    const dim3 grid((p.max_nodes * p.q_heads + kJoinWarps - 1) / kJoinWarps, p.B);
-    if (dtype == OQ_BF16)
-        return launch_pdl(join_pieces<__nv_bfloat16, D, Form>, grid, dim3(32 * kJoinWarps), 0, st,
-                          p, ws);
-    return launch_pdl(join_pieces<__half, D, Form>, grid, dim3(32 * kJoinWarps), 0, st, p, ws);
+    return dtype == OQ_BF16 ? join_as<__nv_bfloat16, D, Form>(p, ws, st)
+                            : join_as<__half, D, Form>(p, ws, st);
 }
 
 #define OQ_BY_BITS(bits, call)  \
@@ -186,14 +161,14 @@ cudaError_t join(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, cu
         return call(8);         \
     }
 
-int narrow_workers(const KvAttendParams &p, int dtype, int sms) {
-#define OQ_CALL(B) kv_attend_workers_b##B(p, dtype, sms)
+int narrow_workers(const KvAttendParams &p, int sms) {
+#define OQ_CALL(B) kv_attend_workers_b##B(p, sms)
     OQ_BY_BITS(p.c.bits, OQ_CALL)
 #undef OQ_CALL
 }
-cudaError_t launch_narrow(const KvAttendParams &p, const KvAttendSpace &ws, int dtype,
+cudaError_t launch_narrow(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, int splits,
                           cudaStream_t st) {
-#define OQ_CALL(B) launch_kv_attend_b##B(p, ws, dtype, st)
+#define OQ_CALL(B) launch_kv_attend_b##B(p, ws, dtype, splits, st)
     OQ_BY_BITS(p.c.bits, OQ_CALL)
 #undef OQ_CALL
 }
@@ -214,7 +189,7 @@ cudaError_t run_narrow(const KvAttendParams &p, const KvAttendSpace &ws, int dty
             ? launch_pdl(rotate_queries<__nv_bfloat16, D, NT, false>, grid, block, 0, st, p, ws)
             : launch_pdl(rotate_queries<__half, D, NT, true>, grid, block, 0, st, p, ws);
     if (e == cudaSuccess)
-        e = launch_narrow(p, ws, dtype, st);
+        e = launch_narrow(p, ws, dtype, 0, st);
     return e == cudaSuccess ? join<D, NarrowForm<NT>>(p, ws, dtype, st) : e;
 }
 
@@ -226,10 +201,12 @@ cudaError_t run_wide(const KvAttendParams &p, const KvAttendSpace &ws, int dtype
 }
 
 // How a call runs: tiles of 128 rows (kv_wide.cuh) for more than 16 rows a key head of 128, else
-// of 8 or 16 (kv_attend.cuh); and where its workspace's arrays lie.
+// of 8 or 16 (kv_attend.cuh), the latter by clusters where all tokens that the page tables can hold
+// are little work; and where its workspace's arrays lie.
 struct Plan {
     bool wide;
     int tile;                     // rows of a tile
+    int splits;                   // of a cluster; 0: workers
     size_t stat_at, first_at, queries_at, factors_at, bytes;
     KvAttendSpace ws;
 };
@@ -241,17 +218,26 @@ Plan plan_for(const KvAttendParams &p, int dtype, int num_sms) {
     a.tile = a.wide ? 128 : rows <= 8 ? 8 : 16;
     a.ws.rows = rows < a.tile ? rows : a.tile;
     a.ws.segments = p.c.kv_heads * ((rows + a.tile - 1) / a.tile);
-    a.ws.most = a.wide ? num_sms : narrow_workers(p, dtype, num_sms);
+    const long long all = (long long)p.B * a.ws.segments;
+    const long long tokens = (long long)p.table_width << p.c.page_log2;
+    if (!a.wide && all <= num_sms && all * tokens <= 16ll * kNearTiles) {
+        // two CTAs an SM at most, and a tile for every warp
+        a.splits = 1;
+        while (a.splits < 16 && all * a.splits <= num_sms && tokens >= 256ll * a.splits)
+            a.splits *= 2;
+        return a;
+    }
+    a.ws.most = a.wide ? num_sms : narrow_workers(p, num_sms);
     // a wide worker is an SM, a narrow one a warp, which should not be set up for less than this
     a.ws.least = a.wide ? 1 : 4;
-    const size_t all = (size_t)p.B * a.ws.segments, slots = all + a.ws.most;
+    const size_t slots = (size_t)all + a.ws.most;
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     a.stat_at = up(slots * a.ws.rows * p.c.d * 4);
     a.first_at = a.stat_at + up(slots * a.ws.rows * 8);
     a.queries_at = a.first_at + up((size_t)(p.B + 1) * 8);
     a.factors_at =
-        a.queries_at + (a.wide ? 0 : up(all * a.tile * p.c.d * (dtype == OQ_BF16 ? 2 : 4)));
-    a.bytes = a.factors_at + (a.wide ? 0 : up(all * a.tile * 4));
+        a.queries_at + (a.wide ? 0 : up((size_t)all * a.tile * p.c.d * (dtype == OQ_BF16 ? 2 : 4)));
+    a.bytes = a.factors_at + (a.wide ? 0 : up((size_t)all * a.tile * 4));
     return a;
 }
 
@@ -284,6 +270,8 @@ cudaError_t launch_kv_attend(const KvAttendParams &params, void *space, int dtyp
     a.ws.factors = reinterpret_cast<float *>(w + a.factors_at);
     if (a.wide)
         return attend::run_wide(p, a.ws, dtype, st);
+    if (a.splits > 0)
+        return attend::launch_narrow(p, a.ws, dtype, a.splits, st);
     if (p.c.d == 128)
         return a.tile == 8 ? attend::run_narrow<128, 1>(p, a.ws, dtype, st)
                            : attend::run_narrow<128, 2>(p, a.ws, dtype, st);

@@ -10,9 +10,11 @@
 // What bounds it is the cache's bytes (a token of one head: two rows of codes and two norms), and
 // right behind them shared memory: two codes a lookup.  So:
 //   - the rows of one key head (its query heads times the nodes) share a pass over its tokens, in
-//     tiles of 8 NT rows; a unit of work is 16 tokens of a tile, a worker is one warp, all warps of
-//     all SMs have the same number of units, and no warp waits for another.  What a warp has of a
-//     segment goes to the workspace; a second kernel joins the pieces in a fixed order;
+//     tiles of 8 NT rows; a unit of work is 16 tokens of a tile, taken by one warp.  Much work
+//     (attend_tiles): all warps of all SMs have the same number of units, none waits for another,
+//     what a warp has of a segment goes to the workspace, and a second kernel joins the pieces in a
+//     fixed order.  Little work (attend_near): a cluster of CTAs takes a segment, and its warps meet
+//     in shared memory, in one launch without a workspace;
 //   - codes go from global memory straight to the registers of the lane that decodes them, 16 bytes
 //     and less at a time, a unit ahead of their use, and through a table in shared memory with a
 //     column a lane (no bank conflicts) into the operand of a matrix instruction;
@@ -24,12 +26,11 @@
 // Scores, softmax statistics and sums are fp32.  fp16 enters in three places: the rotated query
 // (over a power of two of its own), the centroids (times alpha, see build_kv_lut) and the weights
 // p s_v, which are taken relative to a power of two above the row's largest s_v and times 2^6 to
-// 2^14: what a token adds is resolved down to 2^-31 of the largest.  With SPLIT (fp16 outputs) query
-// and weights enter as a sum of two fp16 numbers, so that only the centroids' rounding is left.
+// 2^14: what a token adds is resolved down to 2^-31 of the largest.  With SPLIT (fp16 outputs) a
+// query enters as a sum of two fp16 numbers: its rounding is the one that scores multiply.
 #pragma once
-#ifndef KW
-#define KW 16
-#endif
+
+#include <cooperative_groups.h>
 
 #include "kv_attend_ops.cuh"
 #include "kv_internal.h"
@@ -118,114 +119,109 @@ template <int D, int BITS> struct Tile {
     }
 };
 
-template <int D, int BITS, int NT, bool SPLIT> struct Smem {
-    // Warps of the one CTA on an SM: as many as its registers hold.
-    static constexpr int warps = D == 128 && NT == 1 ? (SPLIT || BITS == 8 ? 12 : KW) : 8;   // KW
-    static constexpr int rows = 8 * NT;
-    // queries stay in shared memory where registers do not hold them beside the accumulators
-    static constexpr bool q_shared = D == 256 && NT == 2;
-    static constexpr int q_words = rows * D / 4 * (SPLIT ? 2 : 1);           // uint2
-    // a warp's own: queries (q_shared) and masks
-    static constexpr int mask_at = q_shared ? q_words * 8 : 0;
-    static constexpr int own = mask_at + rows * 8;
-    static constexpr int bytes = Lut<BITS, true>::bytes + warps * own;
+// A warp's queries: the B operands of S^T = K Q^T (row n = g, elements c D/4 + 4 ks + {0, 1}, {2, 3}),
+// in registers, or in shared memory where those do not hold them beside the accumulators.
+template <int D, int NT, bool SPLIT> struct Queries {
+    static constexpr int KS = D / 16;
+    static constexpr bool shared = D == 256 && NT == 2;
+    static constexpr int words = NT * KS * 32 * (SPLIT ? 2 : 1);     // uint2 of a tile
+    uint2 f[shared ? 1 : NT * KS * (SPLIT ? 2 : 1)];
+    const uint2 *sm;                                                 // at this lane
+    __device__ __forceinline__ void take(const uint2 *from) {       // at this lane
+        sm = from;
+        if constexpr (!shared) {
+#pragma unroll
+            for (int i = 0; i < NT * KS * (SPLIT ? 2 : 1); ++i)
+                f[i] = from[i * 32];
+        }
+    }
+    __device__ __forceinline__ uint2 operator()(int part, int n, int ks) const {
+        const int i = (part * NT + n) * KS + ks;
+        return shared ? sm[i * 32] : f[shared ? 0 : i];
+    }
 };
 
-template <class E, int D, int BITS, int NT, bool SPLIT>
-__global__ void __launch_bounds__(32 * Smem<D, BITS, NT, SPLIT>::warps, 1)
-attend_tiles(const KvAttendParams p, const KvAttendSpace ws) {
-    using S = Shape<D, BITS>;
-    using M = Smem<D, BITS, NT, SPLIT>;
-    constexpr int KS = D / 16;
-    extern __shared__ __align__(128) unsigned char sm[];
-    unsigned char *lut = sm;
-
-    pdl_trigger();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    unsigned char *own = sm + Lut<BITS, true>::bytes + warp * M::own;
-    unsigned long long *masks = reinterpret_cast<unsigned long long *>(own + M::mask_at);
-    fill_lut<BITS, true>(lut, p.lut);
-    __syncthreads();
-    pdl_wait();
-    const uint32_t col = lut_column<BITS>(lane);
-    // neighbouring workers on different SMs: few units reach all of them
-    const long long worker = (long long)warp * gridDim.x + blockIdx.x;
-    Walk walk = take_range(p, ws, worker);
-    Piece piece;
-    while (next_piece<NarrowForm<NT>>(p, walk, piece)) {
-    const Seq &s = piece.s;
-    const int kvh = piece.kvh, nrows = piece.nrows;
-    const int last = piece.tile0 + piece.n;
-    const int *table = p.table + (long long)piece.b * p.table_width;
-    const int in_page = (1 << p.c.page_log2) - 1;
-    int t = piece.tile0;
-    Tile<D, BITS> cur;
-    bool bad_page = false;
-    // a tile's place: its page now, where its rows are when they are loaded
-    auto place = [&](int t) -> int { return t < last ? __ldg(table + ((t << 4) >> p.c.page_log2)) : -1; };
-    int page = place(t), page1 = place(t + 1);
-    cur.keys(p, page, (t << 4) & in_page, kvh, g, c);
-    cur.values(p, page, (t << 4) & in_page, kvh, g, c);
-
-    // B operands of S^T = K Q^T: row n = g, elements c D/4 + 4 ks + {0, 1}, {2, 3} (rotate_queries)
-    const long long sigma = (long long)piece.b * ws.segments + piece.seg;
-    const uint2 *qg = ws.queries + sigma * M::q_words + lane;
-    const uint2 *qsm = reinterpret_cast<const uint2 *>(own) + lane;
-    uint2 qf[M::q_shared ? 1 : NT][M::q_shared ? 1 : KS];
-    uint2 ql[SPLIT && !M::q_shared ? NT : 1][SPLIT && !M::q_shared ? KS : 1];
-    if constexpr (!M::q_shared) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                qf[n][ks] = __ldcg(qg + (n * KS + ks) * 32);
-                if constexpr (SPLIT)
-                    ql[n][ks] = __ldcg(qg + ((NT + n) * KS + ks) * 32);
-            }
-    } else {
-        __syncwarp();
-        for (int i = 0; i < M::q_words / 32; ++i)
-            reinterpret_cast<uint2 *>(own)[i * 32 + lane] = __ldcg(qg + i * 32);
-    }
-    float qs[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        qs[n][0] = __ldcg(ws.factors + sigma * M::rows + 8 * n + 2 * c);
-        qs[n][1] = __ldcg(ws.factors + sigma * M::rows + 8 * n + 2 * c + 1);
-    }
-    __syncwarp();
-    if (lane < M::rows) {
-        const int node = (piece.row_base + lane) / p.group;
-        masks[lane] = lane >= nrows ? 0ull
-                      : p.mask      ? (unsigned long long)p.mask[s.row0 + node]
-                                    : (2ull << node) - 1ull;
-    }
-    __syncwarp();
-
+// What a warp has summed up of a segment, for rows 2c, 2c + 1 (and 8 n on).
+template <int D, int NT> struct Sums {
+    static constexpr int KS = D / 16;
     float acc[NT][KS][4];
     float m[NT][2], l[NT][2];                     // reference and sum
     float vs[NT][2], vinv[NT][2];                 // power of two over s_v, kWeightScale over it
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int j = 0; j < KS; ++j)
+            for (int j = 0; j < KS; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                acc[n][j][i] = 0.f;
+                for (int i = 0; i < 4; ++i)
+                    acc[n][j][i] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            m[n][i] = kNone, l[n][i] = 0.f, vs[n][i] = 0.f, vinv[n][i] = 0.f;
+            for (int i = 0; i < 2; ++i)
+                m[n][i] = kNone, l[n][i] = 0.f, vs[n][i] = 0.f, vinv[n][i] = 0.f;
+        }
     }
+    // l over all lanes, acc in units of one.
+    __device__ __forceinline__ void finish() {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int k = 4; k < 32; k <<= 1)
+                    l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], k);
+                const float f = vs[n][i] * (1.0f / kWeightScale);
+#pragma unroll
+                for (int j = 0; j < KS; ++j) {
+                    acc[n][j][i] *= f;
+                    acc[n][j][2 + i] *= f;
+                }
+            }
+    }
+};
 
-    for (; t < last; ++t) {
-        const int page2 = place(t + 2);
-        // S^T = K Q^T
-        float st[NT][4];
+// Tiles t, t + stride, ... below `last` of one segment, by a warp.  `start` is called once the first
+// tiles are on their way, and fills `q`, `qs` (score factors of rows 2c, 2c + 1) and `masks`.
+template <int D, int BITS, int NT, bool SPLIT, class Start>
+__device__ __forceinline__ void walk_tiles(const KvAttendParams &p, const unsigned char *lut,
+                                           const Seq &s, int b, int kvh, int t, int stride, int last,
+                                           Queries<D, NT, SPLIT> &q, float (&qs)[NT][2],
+                                           const unsigned long long *masks, Sums<D, NT> &o,
+                                           Start start) {
+    using S = Shape<D, BITS>;
+    constexpr int KS = D / 16;
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const uint32_t col = lut_column<BITS>(lane);
+    const int *table = p.table + (long long)b * p.table_width;
+    const int in_page = (1 << p.c.page_log2) - 1;
+    Tile<D, BITS> cur;
+    bool bad_page = false;
+    auto place = [&](int t) -> int {              // a tile's page
+        return t < last ? __ldg(table + ((t << 4) >> p.c.page_log2)) : -1;
+    };
+    const int page = place(t);
+    int page1 = place(t + stride);
+    cur.keys(p, page, (t << 4) & in_page, kvh, g, c);
+    cur.values(p, page, (t << 4) & in_page, kvh, g, c);
+    start();
+
+    for (; t < last; t += stride) {
+        const int page2 = place(t + 2 * stride);
+        // the tile after the next on its way to the L2: a row of keys or values a lane
+        if (page2 >= 0 && page2 < p.c.pages) {
+            const long long row = (((long long)page2 * p.c.kv_heads + kvh) << p.c.page_log2) +
+                                  (((t + 2 * stride) << 4) & in_page) + (lane & 15);
+            const uint8_t *at = pick(p.c.codes, lane >> 4) + row * S::row_bytes;
+#pragma unroll
+            for (int k = 0; k < S::row_bytes; k += 128)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(at + k));
+        }
+        // S^T = K Q^T, in two sums
+        float st[NT][4], s2[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                st[n][i] = 0.f;
+                st[n][i] = s2[n][i] = 0.f;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             uint32_t a[4];
@@ -233,30 +229,29 @@ attend_tiles(const KvAttendParams p, const KvAttendSpace ws) {
             quad<BITS, true>(lut, cur.k[1], ks, col, a[1], a[3]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                uint2 q = M::q_shared ? qsm[(n * KS + ks) * 32]
-                                      : qf[M::q_shared ? 0 : n][M::q_shared ? 0 : ks];
-                mma16816(st[n], a, q.x, q.y);
+                uint2 w = q(0, n, ks);
+                mma16816((ks & 1) ? s2[n] : st[n], a, w.x, w.y);
                 if constexpr (SPLIT) {
-                    q = M::q_shared ? qsm[((NT + n) * KS + ks) * 32]
-                                    : ql[M::q_shared ? 0 : n][M::q_shared ? 0 : ks];
-                    mma16816(st[n], a, q.x, q.y);
+                    w = q(1, n, ks);
+                    mma16816((ks & 1) ? s2[n] : st[n], a, w.x, w.y);
                 }
             }
         }
-        // the next unit's keys are under way from here, its values from the end of this one: each a
-        // part of a unit ahead of its use, in the registers that this unit has done with
+        // the next tile's keys are under way from here, its values from the end of this one: each a
+        // part of a tile ahead of its use, in the registers that this tile has done with
         const float kn[2] = {cur.kn[0], cur.kn[1]}, vn[2] = {cur.vn[0], cur.vn[1]};
         const bool ok = cur.ok;
-        cur.keys(p, page1, ((t + 1) << 4) & in_page, kvh, g, c);
+        cur.keys(p, page1, ((t + stride) << 4) & in_page, kvh, g, c);
         // scores of tokens g, g + 8 and rows 2c, 2c + 1, in powers of two
         bool grow = false;
         const int tok = t << 4;
+        const bool edge = !ok || tok + 16 > s.prefix;     // the page is missing, or it has nodes
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                st[n][i] *= kn[i >> 1] * qs[n][i & 1];
-        if (!ok || tok + 16 > s.prefix) {             // the page is missing, or the tile has nodes
+                st[n][i] = (st[n][i] + s2[n][i]) * (kn[i >> 1] * qs[n][i & 1]);
+        if (edge) {
             bad_page |= !ok;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -268,19 +263,19 @@ attend_tiles(const KvAttendParams p, const KvAttendSpace ws) {
                     if (!see)
                         st[n][i] = -CUDART_INF_F;
                     else
-                        grow |= vn[i >> 1] > vs[n][i & 1];
+                        grow |= vn[i >> 1] > o.vs[n][i & 1];
                 }
         } else {
             const float v = fmaxf(vn[0], vn[1]);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                grow |= v > vs[n][0] || v > vs[n][1];
+                grow |= v > o.vs[n][0] || v > o.vs[n][1];
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                grow |= fmaxf(st[n][i], st[n][2 + i]) > m[n][i] + kSlack;
+                grow |= fmaxf(st[n][i], st[n][2 + i]) > o.m[n][i] + kSlack;
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -295,51 +290,44 @@ attend_tiles(const KvAttendParams p, const KvAttendSpace ws) {
                         up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, k));
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, k));
                     }
-                    up = fmaxf(up, m[n][i]);
-                    f[i] = ex2(m[n][i] - up);
-                    m[n][i] = up;
-                    l[n][i] *= f[i];
-                    if (v > vs[n][i]) {
-                        // the power of two above, with room for a quarter more, in [2^-100, 2^127]
-                        const uint32_t p2 =
-                            (__float_as_uint(v * 1.25f) & 0x7f800000u) + 0x00800000u;
-                        const float nv = __uint_as_float(min(max(p2, 27u << 23), 254u << 23));
-                        f[i] *= vs[n][i] / nv;
-                        vs[n][i] = nv;
-                        vinv[n][i] = kWeightScale / nv;
+                    up = fmaxf(up, o.m[n][i]);
+                    f[i] = ex2(o.m[n][i] - up);
+                    o.m[n][i] = up;
+                    o.l[n][i] *= f[i];
+                    if (v > o.vs[n][i]) {
+                        const float nv = norm_scale(v);
+                        f[i] *= o.vs[n][i] / nv;
+                        o.vs[n][i] = nv;
+                        o.vinv[n][i] = kWeightScale / nv;
                     }
                 }
 #pragma unroll
                 for (int j = 0; j < KS; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        acc[n][j][i] *= f[i & 1];
+                        o.acc[n][j][i] *= f[i & 1];
             }
         }
         // weights
-        uint32_t pb[NT][2], pl[SPLIT ? NT : 1][2];
+        uint32_t pb[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float e = ex2(st[n][i] - m[n][i & 1]);
-                l[n][i & 1] += e;
-                w[i] = e * (vn[i >> 1] * vinv[n][i & 1]);
+                const float e = ex2(st[n][i] - o.m[n][i & 1]);
+                o.l[n][i & 1] += e;
+                w[i] = e * (vn[i >> 1] * o.vinv[n][i & 1]);
             }
-            if (!ok || tok + 16 > s.prefix) {         // what is not seen may have any norm
+            if (edge) {                               // what is not seen may have any norm
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (st[n][i] == -CUDART_INF_F)
                         w[i] = 0.f;
             }
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint32_t hi = half2_bits(w[2 * k], w[2 * k + 1]);
-                pb[n][k] = transpose8x8(hi);
-                if constexpr (SPLIT)
-                    pl[n][k] = transpose8x8(half2_rest(w[2 * k], w[2 * k + 1], hi));
-            }
+            for (int k = 0; k < 2; ++k)
+                pb[n][k] = transpose8x8(half2_bits(w[2 * k], w[2 * k + 1]));
         }
         // O^T += V^T P^T: rows of tile j are elements g D/8 + 2j and 2j + 1
         uint32_t vw[4][S::vu];
@@ -357,49 +345,281 @@ attend_tiles(const KvAttendParams p, const KvAttendSpace ws) {
             for (int h = 0; h < 2; ++h) {
                 const uint32_t a[4] = {x[2 * h], x[2 * h + 1], y[2 * h], y[2 * h + 1]};
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    mma16816(acc[n][j + h], a, pb[n][0], pb[n][1]);
-                    if constexpr (SPLIT)
-                        mma16816(acc[n][j + h], a, pl[n][0], pl[n][1]);
-                }
+                for (int n = 0; n < NT; ++n)
+                    mma16816(o.acc[n][j + h], a, pb[n][0], pb[n][1]);
             }
         }
-        cur.values(p, page1, ((t + 1) << 4) & in_page, kvh, g, c);
+        cur.values(p, page1, ((t + stride) << 4) & in_page, kvh, g, c);
         page1 = page2;
     }
     if (bad_page && lane == 0)
         atomicOr(p.err, AT_ERR_PAGE);
+}
 
-    // ---- the piece goes to its slot ----
-    const long long slot = (long long)piece.b * ws.segments + piece.seg + worker;
+__device__ __forceinline__ unsigned long long mask_of(const KvAttendParams &p, const Seq &s,
+                                                      int row, int nrows, int row_base) {
+    if (row >= nrows)
+        return 0ull;
+    const int node = (row_base + row) / p.group;
+    return p.mask ? (unsigned long long)p.mask[s.row0 + node] : (2ull << node) - 1ull;
+}
+
+// ---- much work: a worker a warp ----
+template <int D, int BITS, int NT, bool SPLIT> struct Stream {
+    // Warps of the one CTA on an SM.  (64 single tokens over contexts to 8191, 4 bits: 8, 10, 12, 16,
+    // 20 warps take 128, 113, 99, 103, 113 us: 16 and more have too few registers to load ahead.)
+    static constexpr int warps = D == 128 && NT == 1 ? 12 : 8;
+    static constexpr int rows = 8 * NT;
+    using Q = Queries<D, NT, SPLIT>;
+    static constexpr int mask_at = Q::shared ? Q::words * 8 : 0;     // of a warp's own memory
+    static constexpr int own = mask_at + rows * 8;
+    static constexpr int bytes = Lut<BITS, true>::bytes + warps * own;
+};
+
+template <int D, int BITS, int NT, bool SPLIT>
+__global__ void __launch_bounds__(32 * Stream<D, BITS, NT, SPLIT>::warps, 1)
+attend_tiles(const KvAttendParams p, const KvAttendSpace ws) {
+    using M = Stream<D, BITS, NT, SPLIT>;
+    using Q = Queries<D, NT, SPLIT>;
+    constexpr int KS = D / 16;
+    extern __shared__ __align__(128) unsigned char sm[];
+    pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    unsigned char *own = sm + Lut<BITS, true>::bytes + warp * M::own;
+    unsigned long long *masks = reinterpret_cast<unsigned long long *>(own + M::mask_at);
+    fill_lut<BITS, true>(sm, p.lut);
+    __syncthreads();
+    pdl_wait();
+    // neighbouring workers on different SMs: few units reach all of them
+    const long long worker = (long long)warp * gridDim.x + blockIdx.x;
+    Walk walk = take_range(p, ws, worker);
+    Piece piece;
+    while (next_piece<NarrowForm<NT>>(p, walk, piece)) {
+        Q q;
+        float qs[NT][2];
+        Sums<D, NT> o;
+        o.clear();
+        walk_tiles<D, BITS, NT, SPLIT>(
+            p, sm, piece.s, piece.b, piece.kvh, piece.tile0, 1, piece.tile0 + piece.n, q, qs, masks,
+            o, [&] {
+                const long long seg = (long long)piece.b * ws.segments + piece.seg;
+                const uint2 *from = ws.queries + seg * Q::words + lane;
+                __syncwarp();
+                if constexpr (Q::shared) {
+                    for (int i = 0; i < Q::words / 32; ++i)
+                        reinterpret_cast<uint2 *>(own)[i * 32 + lane] = from[i * 32];
+                    from = reinterpret_cast<const uint2 *>(own) + lane;
+                }
+                if (lane < M::rows)
+                    masks[lane] = mask_of(p, piece.s, lane, piece.nrows, piece.row_base);
+                __syncwarp();
+                q.take(from);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+                    for (int i = 0; i < 2; ++i)
+                        qs[n][i] = ws.factors[seg * M::rows + 8 * n + 2 * c + i];
+            });
+        // ---- the piece goes to its slot ----
+        o.finish();
+        const long long slot = (long long)piece.b * ws.segments + piece.seg + worker;
 #pragma unroll
-            for (int k = 4; k < 32; k <<= 1)
-                l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], k);
-            const int r = 8 * n + 2 * c + i;
-            if (r >= nrows)
-                continue;
-            if (g == 0) {
-                ws.stat[slot * 2 * ws.rows + r] = m[n][i];
-                ws.stat[(slot * 2 + 1) * ws.rows + r] = l[n][i];
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = 8 * n + 2 * c + i;
+                if (r >= piece.nrows)
+                    continue;
+                if (g == 0) {
+                    ws.stat[slot * 2 * ws.rows + r] = o.m[n][i];
+                    ws.stat[(slot * 2 + 1) * ws.rows + r] = o.l[n][i];
+                }
+                float4 *dst =
+                    reinterpret_cast<float4 *>(ws.part + (slot * ws.rows + r) * D + g * (D / 8));
+#pragma unroll
+                for (int j = 0; j < KS; j += 2)
+                    dst[j / 2] = make_float4(o.acc[n][j][i], o.acc[n][j][2 + i],
+                                             o.acc[n][j + 1][i], o.acc[n][j + 1][2 + i]);
             }
-            const float f = vs[n][i] * (1.0f / kWeightScale);
-            float4 *dst = reinterpret_cast<float4 *>(ws.part + (slot * ws.rows + r) * D + g * (D / 8));
-#pragma unroll
-            for (int j = 0; j < KS; j += 2)
-                dst[j / 2] = make_float4(acc[n][j][i] * f, acc[n][j][2 + i] * f,
-                                         acc[n][j + 1][i] * f, acc[n][j + 1][2 + i] * f);
-        }
     }
 }
 
+// ---- little work: a cluster a segment ----
+template <int D, int BITS, int NT, bool SPLIT> struct Near {
+    static constexpr int warps = 8, rows = 8 * NT;
+    using Q = Queries<D, NT, SPLIT>;
+    static constexpr int part = (D / 16) * NT * 4 * 128 + NT * 4 * 128;      // a warp's sums
+    static constexpr int fin_stride = D + 4;                                 // floats
+    static constexpr int most(int a, int b) { return a > b ? a : b; }
+    // the table, then the warps' sums, then the block's
+    static constexpr int big = most(most(Lut<BITS, true>::bytes, warps / 2 * part),
+                                    rows * fin_stride * 4);
+    static constexpr int q_at = big;
+    static constexpr int x_at = q_at + Q::words * 8;                         // [warps][D] floats
+    static constexpr int mask_at = x_at + warps * D * 4;
+    static constexpr int stat_at = mask_at + rows * 8;                       // factor, m, l: [rows]
+    static constexpr int bytes = stat_at + rows * 12;
+};
+
 template <class E, int D, int BITS, int NT, bool SPLIT>
-cudaError_t launch_tiles(const KvAttendParams &p, KvAttendSpace ws, cudaStream_t st) {
-    using M = Smem<D, BITS, NT, SPLIT>;
-    auto *kern = attend_tiles<E, D, BITS, NT, SPLIT>;
+__global__ void __launch_bounds__(32 * Near<D, BITS, NT, SPLIT>::warps)
+attend_near(const KvAttendParams p, const int row_tiles) {
+    using M = Near<D, BITS, NT, SPLIT>;
+    using Q = Queries<D, NT, SPLIT>;
+    constexpr int N = D / 32, KS = D / 16;
+    extern __shared__ __align__(128) unsigned char sm[];
+    namespace cg = cooperative_groups;
+    uint2 *qm = reinterpret_cast<uint2 *>(sm + M::q_at);
+    float *xs = reinterpret_cast<float *>(sm + M::x_at);
+    unsigned long long *masks = reinterpret_cast<unsigned long long *>(sm + M::mask_at);
+    float *factor = reinterpret_cast<float *>(sm + M::stat_at);
+    float *row_m = factor + M::rows, *row_l = row_m + M::rows;
+
+    pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int rank = blockIdx.x, splits = gridDim.x;       // the cluster is the whole x dimension
+    const int kvh = blockIdx.y / row_tiles, row_base = (blockIdx.y - kvh * row_tiles) * M::rows;
+    const int b = blockIdx.z;
+    fill_lut<BITS, true>(sm, p.lut);
+    uint32_t ent[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        ent[i] = p.ent[lane * N + i];
+    pdl_wait();
+    Seq s;
+    if (!load_seq(p, b, &s, blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0))
+        return;                                            // the whole cluster returns
+    const int nrows = min(M::rows, s.nodes * p.group - row_base);
+    if (nrows <= 0)
+        return;
+    const int tiles = (s.prefix + s.nodes + 15) >> 4, share = (tiles + splits - 1) / splits;
+    Q q;
+    float qs[NT][2];
+    Sums<D, NT> o;
+    o.clear();
+    walk_tiles<D, BITS, NT, SPLIT>(
+        p, sm, s, b, kvh, rank * share + warp, M::warps, min(tiles, (rank + 1) * share), q, qs,
+        masks, o, [&] {
+            for (int r = warp; r < M::rows; r += M::warps) {
+                const float f = rotate_row<E, D, SPLIT>(p, s, kvh, row_base + r, r < nrows, ent,
+                                                        xs + warp * D, r, NT,
+                                                        reinterpret_cast<__half *>(qm));
+                if (lane == 0) {
+                    factor[r] = f;
+                    masks[r] = mask_of(p, s, r, nrows, row_base);
+                }
+            }
+            __syncthreads();                               // and the table is complete
+            q.take(qm + lane);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    qs[n][i] = factor[8 * n + 2 * c + i];
+        });
+    o.finish();
+    // ---- the block's warps meet ----
+#pragma unroll
+    for (int half = M::warps / 2; half >= 1; half >>= 1) {
+        __syncthreads();                                  // the table / the last round is done with
+        float *mine = reinterpret_cast<float *>(sm + (warp & (half - 1)) * M::part) + lane;
+        if (warp >= half && warp < 2 * half) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int j = 0; j < KS; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mine[((n * KS + j) * 4 + i) * 32] = o.acc[n][j][i];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    mine[(NT * KS * 4 + n * 4 + i) * 32] = o.m[n][i];
+                    mine[(NT * KS * 4 + n * 4 + 2 + i) * 32] = o.l[n][i];
+                }
+            }
+        }
+        __syncthreads();
+        if (warp < half) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float f[2], h[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float om = mine[(NT * KS * 4 + n * 4 + i) * 32];
+                    const float ol = mine[(NT * KS * 4 + n * 4 + 2 + i) * 32];
+                    const float mn = fmaxf(o.m[n][i], om);
+                    f[i] = ex2(o.m[n][i] - mn);
+                    h[i] = ex2(om - mn);
+                    o.m[n][i] = mn;
+                    o.l[n][i] = o.l[n][i] * f[i] + ol * h[i];
+                }
+#pragma unroll
+                for (int j = 0; j < KS; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        o.acc[n][j][i] = o.acc[n][j][i] * f[i & 1] +
+                                         mine[((n * KS + j) * 4 + i) * 32] * h[i & 1];
+            }
+        }
+    }
+    __syncthreads();
+    float *fin = reinterpret_cast<float *>(sm);           // [rows][fin_stride]
+    if (warp == 0) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = 8 * n + 2 * c + i;
+#pragma unroll
+                for (int j = 0; j < KS; ++j) {
+                    fin[r * M::fin_stride + g * (D / 8) + 2 * j] = o.acc[n][j][i];
+                    fin[r * M::fin_stride + g * (D / 8) + 2 * j + 1] = o.acc[n][j][2 + i];
+                }
+                if (g == 0) {
+                    row_m[r] = o.m[n][i];
+                    row_l[r] = o.l[n][i];
+                }
+            }
+    }
+    // ---- the cluster's blocks meet: rank k finishes rows k, k + splits, ... ----
+    cg::cluster_group cl = cg::this_cluster();
+    cl.sync();
+    for (int r = rank + splits * warp; r < nrows; r += splits * M::warps) {
+        // a lane each of the ranks' references and sums, then their rows in turn
+        const float mk = lane < splits ? *cl.map_shared_rank(row_m + r, lane) : kNone;
+        float mx = mk;
+#pragma unroll
+        for (int k = 16; k; k >>= 1)
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+        const float f = ex2(mk - mx);
+        float sum = lane < splits ? f * *cl.map_shared_rank(row_l + r, lane) : 0.f;
+#pragma unroll
+        for (int k = 16; k; k >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, k);
+        float x[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            x[i] = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < splits; ++k) {
+            const float fk = __shfl_sync(0xffffffffu, f, k);
+            const float4 *src = reinterpret_cast<const float4 *>(
+                cl.map_shared_rank(fin + r * M::fin_stride + lane * N, k));
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                const float4 v = src[i / 4];
+                x[i] += fk * v.x, x[i + 1] += fk * v.y, x[i + 2] += fk * v.z, x[i + 3] += fk * v.w;
+            }
+        }
+        finish_row<E, D>(p, s, kvh, row_base + r, ent, xs + warp * D, x, sum);
+    }
+    cl.sync();                                            // shared memory stays until all have read
+}
+
+template <int D, int BITS, int NT, bool SPLIT>
+cudaError_t launch_stream(const KvAttendParams &p, const KvAttendSpace &ws, cudaStream_t st) {
+    using M = Stream<D, BITS, NT, SPLIT>;
+    auto *kern = attend_tiles<D, BITS, NT, SPLIT>;
     static PerDevice ready;
     const cudaError_t e = ready.once([&] {
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, M::bytes);
@@ -410,34 +630,65 @@ cudaError_t launch_tiles(const KvAttendParams &p, KvAttendSpace ws, cudaStream_t
                       ws);
 }
 
-// Workers of a launch on `sms` SMs.
-template <int D, int BITS> int workers_on(int sms, bool split, int rows) {
-    if (rows <= 8)
-        return sms * (split ? Smem<D, BITS, 1, true>::warps : Smem<D, BITS, 1, false>::warps);
-    return sms * (split ? Smem<D, BITS, 2, true>::warps : Smem<D, BITS, 2, false>::warps);
+template <class E, int D, int BITS, int NT, bool SPLIT>
+cudaError_t launch_near(const KvAttendParams &p, int splits, cudaStream_t st) {
+    using M = Near<D, BITS, NT, SPLIT>;
+    auto *kern = attend_near<E, D, BITS, NT, SPLIT>;
+    static PerDevice ready;
+    const cudaError_t e = ready.once([&] {
+        cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               M::bytes);
+        if (err == cudaSuccess)
+            err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        return err;
+    });
+    if (e != cudaSuccess)
+        return e;
+    const int row_tiles = (p.max_nodes * p.group + M::rows - 1) / M::rows;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(splits, p.c.kv_heads * row_tiles, p.B);
+    cfg.blockDim = dim3(32 * M::warps);
+    cfg.dynamicSmemBytes = M::bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, p, row_tiles);
 }
 
-template <class E, int D, int BITS, bool SPLIT>
-cudaError_t launch_rows(const KvAttendParams &p, const KvAttendSpace &ws, cudaStream_t st) {
-    if (p.max_nodes * p.group <= 8)
-        return launch_tiles<E, D, BITS, 1, SPLIT>(p, ws, st);
-    return launch_tiles<E, D, BITS, 2, SPLIT>(p, ws, st);
+template <int BITS, int D, int NT>
+cudaError_t launch_tile(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, int splits,
+                        cudaStream_t st) {
+    if (splits > 0)
+        return dtype == OQ_BF16 ? launch_near<__nv_bfloat16, D, BITS, NT, false>(p, splits, st)
+                                : launch_near<__half, D, BITS, NT, true>(p, splits, st);
+    return dtype == OQ_BF16 ? launch_stream<D, BITS, NT, false>(p, ws, st)
+                            : launch_stream<D, BITS, NT, true>(p, ws, st);
 }
 
 template <int BITS>
-cudaError_t launch_bits(const KvAttendParams &p, const KvAttendSpace &ws, int dtype,
+cudaError_t launch_bits(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, int splits,
                         cudaStream_t st) {
-    if (dtype == OQ_BF16)
-        return p.c.d == 128 ? launch_rows<__nv_bfloat16, 128, BITS, false>(p, ws, st)
-                            : launch_rows<__nv_bfloat16, 256, BITS, false>(p, ws, st);
-    return p.c.d == 128 ? launch_rows<__half, 128, BITS, true>(p, ws, st)
-                        : launch_rows<__half, 256, BITS, true>(p, ws, st);
+    const bool one = p.max_nodes * p.group <= 8;
+    if (p.c.d == 128)
+        return one ? launch_tile<BITS, 128, 1>(p, ws, dtype, splits, st)
+                   : launch_tile<BITS, 128, 2>(p, ws, dtype, splits, st);
+    return one ? launch_tile<BITS, 256, 1>(p, ws, dtype, splits, st)
+               : launch_tile<BITS, 256, 2>(p, ws, dtype, splits, st);
 }
 
-template <int BITS> int workers_bits(const KvAttendParams &p, int dtype, int sms) {
-    const int rows = p.max_nodes * p.group;
-    return p.c.d == 128 ? workers_on<128, BITS>(sms, dtype != OQ_BF16, rows)
-                        : workers_on<256, BITS>(sms, dtype != OQ_BF16, rows);
+// Workers of attend_tiles on `sms` SMs.
+template <int BITS> int workers_bits(const KvAttendParams &p, int sms) {
+    const bool one = p.max_nodes * p.group <= 8;
+    if (p.c.d == 128)
+        return sms * (one ? Stream<128, BITS, 1, false>::warps : Stream<128, BITS, 2, false>::warps);
+    return sms * (one ? Stream<256, BITS, 1, false>::warps : Stream<256, BITS, 2, false>::warps);
 }
 
 }  // namespace attend

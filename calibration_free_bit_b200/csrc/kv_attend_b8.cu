@@ -4,12 +4,12 @@
 namespace oq {
 
 cudaError_t launch_kv_attend_b8(const KvAttendParams &p, const KvAttendSpace &ws, int dtype,
-                                cudaStream_t st) {
-    return attend::launch_bits<8>(p, ws, dtype, st);
+                                int splits, cudaStream_t st) {
+    return attend::launch_bits<8>(p, ws, dtype, splits, st);
 }
 
-int kv_attend_workers_b8(const KvAttendParams &p, int dtype, int sms) {
-    return attend::workers_bits<8>(p, dtype, sms);
+int kv_attend_workers_b8(const KvAttendParams &p, int sms) {
+    return attend::workers_bits<8>(p, sms);
 }
 
 }  // namespace oq

@@ -66,6 +66,90 @@ __device__ __forceinline__ uint32_t half2_rest(float a, float b, uint32_t hi) {
 constexpr float kSlack = 8.0f, kWeightScale = 64.0f;
 constexpr float kNone = -1e30f;                      // reference of a row that has seen nothing
 
+// The power of two above a norm, with room for a quarter more, in [2^-100, 2^127].
+__device__ __forceinline__ float norm_scale(float v) {
+    const uint32_t p2 = (__float_as_uint(v * 1.25f) & 0x7f800000u) + 0x00800000u;
+    return __uint_as_float(min(max(p2, 27u << 23), 254u << 23));
+}
+
+// ---- rows ----
+// Row r of a tile of 8 nt: the rotated query of the key head's row `at` (zeros without one), by a
+// warp, as fp16 over the power of two below its largest element; with SPLIT also what that leaves.
+// It goes to `to` as the lanes of a matrix instruction take it, [part][row / 8][step][lane][4] with
+// lane = 4 (row % 8) + quarter of the row.  Returns the factor of its scores.
+template <class E, int D, bool SPLIT>
+__device__ __forceinline__ float rotate_row(const KvAttendParams &p, const Seq &s, int kvh, int at,
+                                            bool real, const uint32_t (&ent)[D / 32], float *xs,
+                                            int r, int nt, __half *to) {
+    constexpr int N = D / 32, KS = D / 16;
+    const int lane = threadIdx.x & 31;
+    float z[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        z[i] = 0.f;
+    if (real) {
+        const int node = at / p.group, e = at - node * p.group;
+        const E *q = static_cast<const E *>(p.q) + (long long)(s.row0 + node) * p.q_stride +
+                     (kvh * p.group + e) * D;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            xs[i * 32 + lane] = to_f32(q[i * 32 + lane]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float v = xs[ent[i] & 0x7fffu];
+            z[i] = (ent[i] & 0x8000u) ? -v : v;
+        }
+        warp_wht<D>(z, p.h, lane);
+        __syncwarp();
+    }
+    float big = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        big = fmaxf(big, fabsf(z[i]));
+#pragma unroll
+    for (int k = 16; k; k >>= 1)
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, k));
+    // 2^e <= big < 2^(e+1); values over 2^e stay below 2 (2^e and its inverse are normal)
+    uint32_t ex = (__float_as_uint(big) >> 23) & 255u;
+    ex = ex < 1u ? 1u : (ex > 253u ? 253u : ex);
+    const float up = __uint_as_float(ex << 23), down = __uint_as_float((254u - ex) << 23);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float v = z[i] * down;
+        const __half hi = __float2half_rn(v);
+        const int x = lane * N + i, y = x % (D / 4);
+        const int o = (((r >> 3) * KS + (y >> 2)) * 32 + (r & 7) * 4 + x / (D / 4)) * 4 + (y & 3);
+        to[o] = hi;
+        if constexpr (SPLIT)
+            to[nt * 8 * D + o] = __float2half_rn(v - __half2float(hi));
+    }
+    return up * p.qk_scale;
+}
+
+// The key head's row `at` from its sums (lane l has elements l D/32 on) and its weights' sum: R^T,
+// and out.  A row that saw nothing gives zeros.
+template <class E, int D>
+__device__ __forceinline__ void finish_row(const KvAttendParams &p, const Seq &s, int kvh, int at,
+                                           const uint32_t (&ent)[D / 32], float *xs,
+                                           float (&o)[D / 32], float sum) {
+    constexpr int N = D / 32;
+    const int lane = threadIdx.x & 31;
+    warp_wht<D>(o, p.h, lane);
+    const float inv = sum == 0.f ? 0.f : p.o_scale / sum;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        xs[ent[i] & 0x7fffu] = inv * ((ent[i] & 0x8000u) ? -o[i] : o[i]);
+    __syncwarp();
+    const int node = at / p.group, e = at - node * p.group;
+    E *y = static_cast<E *>(p.out) + (long long)(s.row0 + node) * p.out_stride +
+           (kvh * p.group + e) * D;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        y[i * 32 + lane] = from_f32<E>(xs[i * 32 + lane]);
+}
+
 // ---- work lists ----
 // A segment is one sequence's tile of rows of one key head; its units are the sequence's tiles of
 // tokens, and before them `Extra` that stand for the time that a segment's setting up takes.  The

@@ -131,18 +131,19 @@ cudaError_t launch_kv_wide_b3(const KvAttendParams &p, const KvAttendSpace &ws, 
 cudaError_t launch_kv_wide_b4(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, cudaStream_t st);
 cudaError_t launch_kv_wide_b6(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, cudaStream_t st);
 cudaError_t launch_kv_wide_b8(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, cudaStream_t st);
-// Few rows a key head, or heads of 256 (kv_attend.cuh); the number of its workers.
-cudaError_t launch_kv_attend_b2(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, cudaStream_t st);
-int kv_attend_workers_b2(const KvAttendParams &p, int dtype, int sms);
-cudaError_t launch_kv_attend_b3(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, cudaStream_t st);
-int kv_attend_workers_b3(const KvAttendParams &p, int dtype, int sms);
-cudaError_t launch_kv_attend_b4(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, cudaStream_t st);
-int kv_attend_workers_b4(const KvAttendParams &p, int dtype, int sms);
-cudaError_t launch_kv_attend_b6(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, cudaStream_t st);
-int kv_attend_workers_b6(const KvAttendParams &p, int dtype, int sms);
-cudaError_t launch_kv_attend_b8(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, cudaStream_t st);
-int kv_attend_workers_b8(const KvAttendParams &p, int dtype, int sms);
-// Device memory that launch_kv_attend needs for a call (given to it as `space`).
+// Few rows a key head, or heads of 256 (kv_attend.cuh): in one launch, a cluster of `splits` CTAs a
+// segment, or with splits = 0 by workers (their number on `sms` SMs) with a workspace.
+cudaError_t launch_kv_attend_b2(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, int splits, cudaStream_t st);
+int kv_attend_workers_b2(const KvAttendParams &p, int sms);
+cudaError_t launch_kv_attend_b3(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, int splits, cudaStream_t st);
+int kv_attend_workers_b3(const KvAttendParams &p, int sms);
+cudaError_t launch_kv_attend_b4(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, int splits, cudaStream_t st);
+int kv_attend_workers_b4(const KvAttendParams &p, int sms);
+cudaError_t launch_kv_attend_b6(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, int splits, cudaStream_t st);
+int kv_attend_workers_b6(const KvAttendParams &p, int sms);
+cudaError_t launch_kv_attend_b8(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, int splits, cudaStream_t st);
+int kv_attend_workers_b8(const KvAttendParams &p, int sms);
+// Device memory that launch_kv_attend needs for a call, 0 for none (given to it as `space`).
 size_t kv_attend_space(const KvAttendParams &p, int dtype, int num_sms);
 cudaError_t launch_kv_attend(const KvAttendParams &p, void *space, int dtype, cudaStream_t st,
                              int num_sms, std::string *why);

@@ -275,10 +275,7 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                     m = up;
                     l *= fac;
                     if (vtop > vs) {
-                        // the power of two above, with room for a quarter more, in [2^-100, 2^127]
-                        const uint32_t p2 =
-                            (__float_as_uint(vtop * 1.25f) & 0x7f800000u) + 0x00800000u;
-                        const float nv = __uint_as_float(min(max(p2, 27u << 23), 254u << 23));
+                        const float nv = norm_scale(vtop);
                         fac *= vs / nv;
                         vs = nv;
                         vinv = kWeightScale / nv;

@@ -502,18 +502,21 @@ int oq_kv_attend(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cach
     if (p.c.d == 128 &&
         (rc = rotation_matrix(rw, dtype == OQ_BF16 ? RMAT_BF16 : RMAT_F16, dev, &p.r_img)) != OQ_OK)
         return rc;
-    cudaMemPool_t pool = device_pool(dev, di, &rc);
-    if (!pool)
-        return rc;
     void *space = nullptr;
-    cudaError_t e =
-        cudaMallocFromPoolAsync(&space, oq::kv_attend_space(p, dtype, di->sms), pool, st);
-    if (e != cudaSuccess)
-        return fail_cuda(e, "oq_kv_attend: workspace allocation");
+    const size_t need = oq::kv_attend_space(p, dtype, di->sms);
+    cudaError_t e = cudaSuccess;
+    if (need > 0) {
+        cudaMemPool_t pool = device_pool(dev, di, &rc);
+        if (!pool)
+            return rc;
+        e = cudaMallocFromPoolAsync(&space, need, pool, st);
+        if (e != cudaSuccess)
+            return fail_cuda(e, "oq_kv_attend: workspace allocation");
+    }
     e = timed(OQ_KERNEL_KV_ATTEND, st, [&] {
         return oq::launch_kv_attend(p, space, dtype, st, di->sms, &why);
     });
-    const cudaError_t e2 = cudaFreeAsync(space, st);
+    const cudaError_t e2 = space ? cudaFreeAsync(space, st) : cudaSuccess;
     if (e != cudaSuccess)
         return fail_cuda(e, why.c_str());
     if (e2 != cudaSuccess)
