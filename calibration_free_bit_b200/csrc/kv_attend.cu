@@ -201,7 +201,7 @@ cudaError_t run_wide(const KvAttendParams &p, const KvAttendSpace &ws, int dtype
 }
 
 // How a call runs: tiles of 128 rows (kv_wide.cuh) for more than 16 rows a key head of 128, else
-// of 8 or 16 (kv_attend.cuh), the latter by clusters where all tokens that the page tables can hold
+// of 8 or, of heads of 128, 16 (kv_attend.cuh), the latter by clusters where all tokens that the page tables can hold
 // are little work; and where its workspace's arrays lie.
 struct Plan {
     bool wide;
@@ -215,7 +215,7 @@ Plan plan_for(const KvAttendParams &p, int dtype, int num_sms) {
     Plan a = {};
     const int rows = p.max_nodes * p.group;
     a.wide = p.c.d == 128 && rows > 16;
-    a.tile = a.wide ? 128 : rows <= 8 ? 8 : 16;
+    a.tile = a.wide ? 128 : rows <= 8 || p.c.d == 256 ? 8 : 16;
     a.ws.rows = rows < a.tile ? rows : a.tile;
     a.ws.segments = p.c.kv_heads * ((rows + a.tile - 1) / a.tile);
     const long long all = (long long)p.B * a.ws.segments;
@@ -275,8 +275,7 @@ cudaError_t launch_kv_attend(const KvAttendParams &params, void *space, int dtyp
     if (p.c.d == 128)
         return a.tile == 8 ? attend::run_narrow<128, 1>(p, a.ws, dtype, st)
                            : attend::run_narrow<128, 2>(p, a.ws, dtype, st);
-    return a.tile == 8 ? attend::run_narrow<256, 1>(p, a.ws, dtype, st)
-                       : attend::run_narrow<256, 2>(p, a.ws, dtype, st);
+    return attend::run_narrow<256, 1>(p, a.ws, dtype, st);
 }
 
 cudaError_t read_and_clear_attend_error(unsigned *out, cudaStream_t st) {

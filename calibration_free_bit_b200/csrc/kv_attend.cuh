@@ -15,9 +15,10 @@
 //     what a warp has of a segment goes to the workspace, and a second kernel joins the pieces in a
 //     fixed order.  Little work (attend_near): a cluster of CTAs takes a segment, and its warps meet
 //     in shared memory, in one launch without a workspace;
-//   - codes go from global memory straight to the registers of the lane that decodes them, 16 bytes
-//     and less at a time, a unit ahead of their use, and through a table in shared memory with a
-//     column a lane (no bank conflicts) into the operand of a matrix instruction;
+//   - a warp's tiles come into its own ring in shared memory by bulk copies (a tile's rows of a head
+//     lie together), several tiles ahead of their use, without a load instruction or a register; a
+//     lane's codes go through a table in shared memory with a column a lane (no bank conflicts)
+//     into the operand of a matrix instruction;
 //   - products are transposed, S^T = K Q^T and O^T = V^T P^T (mma.sync m16n8k16): the 16-wide side
 //     is the cache, so 8 rows fill an instruction and an accumulator takes 32 registers.  The
 //     instruction's order of a row's elements is free as long as both operands agree, which is how
@@ -29,13 +30,18 @@
 // 2^14: what a token adds is resolved down to 2^-31 of the largest.  With SPLIT (fp16 outputs) a
 // query enters as a sum of two fp16 numbers: its rounding is the one that scores multiply.
 #pragma once
+#ifndef KW
+#define KW 12
+#endif
 
 #include <cooperative_groups.h>
 
+#include "k1_ops.cuh"
 #include "kv_attend_ops.cuh"
 #include "kv_internal.h"
 #include "kv_lut.cuh"
 #include "kv_ops.cuh"
+#include "sm100_common.cuh"
 
 namespace oq {
 namespace attend {
@@ -69,75 +75,116 @@ template <int D, int BITS> struct Shape {
     static constexpr int vu = v_shared ? 2 : vw;      // words used
 };
 
-// One unit's 16 tokens: codes and norms as this lane needs them.
-template <int D, int BITS> struct Tile {
+// A warp's ring of tiles in shared memory: 16 key rows, 16 value rows and their norms each, brought in
+// by bulk copies as many tiles ahead as there are slots.
+// Row j of a tile's matrices is token order(j) of its 16: the four value rows that a warp reads in one
+// go then lie together.
+__device__ __forceinline__ int order(int j) { return (j & 8) + ((j & 7) >> 1) + ((j & 1) << 2); }
+
+template <int D, int BITS, int SLOTS> struct Ring {
     using S = Shape<D, BITS>;
-    uint32_t k[2][S::kw];        // key rows of tokens g, g + 8: elements c D/4 ..
-    uint32_t v[4][S::vw];        // value rows of tokens 2c, 2c+1, 2c+8, 2c+9: elements g D/8 ..
-    float kn[2], vn[2];          // norms of tokens g, g + 8
-    bool ok;                     // the page exists
+    static constexpr int rows = 16 * S::row_bytes;
+    static constexpr int slot = 2 * rows + 128;       // keys, values, their norms
+    static constexpr int bytes = SLOTS * (slot + 16); // barriers and flags behind the slots
+    unsigned char *sm;
+    uint32_t at, bar0;                                // addresses of the slots, of the barriers
+    uint32_t put, got;                                // tiles so far
 
-    // (codes of a missing page stay as they are: they are not seen, and the norms are 0)
-    __device__ __forceinline__ void keys(const KvAttendParams &p, int page, int at, int kvh, int g,
-                                         int c) {
-        ok = page >= 0 && page < p.c.pages;
-        kn[0] = kn[1] = vn[0] = vn[1] = 0.f;
-        if (ok) {
-            const long long row = (((long long)page * p.c.kv_heads + kvh) << p.c.page_log2) + at;
-            const uint8_t *kr = p.c.codes[0] + row * S::row_bytes + g * S::row_bytes + c * S::k_bytes;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                load_words<S::kw, S::k_bytes>(k[i], kr + 8 * i * S::row_bytes);
-                kn[i] = __ldg(p.c.norms[0] + row + g + 8 * i);
-                vn[i] = __ldg(p.c.norms[1] + row + g + 8 * i);
-            }
+    __device__ __forceinline__ void init(unsigned char *own) {
+        sm = own;
+        at = sm100::smem_u32(own);
+        bar0 = at + SLOTS * slot;
+        put = got = 0;
+        if ((threadIdx.x & 31) == 0) {
+            for (int i = 0; i < SLOTS; ++i)
+                sm100::mbar_init(bar0 + 16 * i, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
+        __syncwarp();
     }
-    __device__ __forceinline__ void values(const KvAttendParams &p, int page, int at, int kvh,
-                                           int g, int c) {
-        if (page >= 0 && page < p.c.pages) {
-            const long long row = (((long long)page * p.c.kv_heads + kvh) << p.c.page_log2) + at;
-            const uint8_t *vr = p.c.codes[1] + row * S::row_bytes + 2 * c * S::row_bytes +
-                                (S::v_shared ? g >> 1 : g) * S::v_bytes;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                load_words<S::vw, S::v_bytes>(v[i],
-                                              vr + ((i & 1) + 8 * (i >> 1)) * S::row_bytes);
+    // The next slot takes the tile of tokens `in` .. `in` + 15 of a page (lane 0; the slot's last
+    // readers are done).
+    __device__ __forceinline__ void fetch(const KvAttendParams &p, int page, int in, int kvh) {
+        const uint32_t i = put++ % SLOTS, bar = bar0 + 16 * i;
+        if ((threadIdx.x & 31) != 0)
+            return;
+        const bool ok = page >= 0 && page < p.c.pages;
+        *reinterpret_cast<int *>(sm + SLOTS * slot + 16 * i + 8) = ok;
+        if (!ok) {
+            sm100::mbar_arrive(bar);
+            return;
         }
+        const long long row = (((long long)page * p.c.kv_heads + kvh) << p.c.page_log2) + in;
+        const uint32_t to = at + i * slot;
+        sm100::mbar_expect_tx(bar, slot);
+        k1ops::bulk_copy(to, p.c.codes[0] + row * S::row_bytes, rows, bar);
+        k1ops::bulk_copy(to + rows, p.c.codes[1] + row * S::row_bytes, rows, bar);
+        k1ops::bulk_copy(to + 2 * rows, p.c.norms[0] + row, 64, bar);
+        k1ops::bulk_copy(to + 2 * rows + 64, p.c.norms[1] + row, 64, bar);
     }
-
-    // The words of value row i that hold this lane's elements.
-    __device__ __forceinline__ void share(int i, int g, uint32_t (&w)[S::vu]) const {
-        if constexpr (S::v_shared) {                 // 48 of 96 bits
-            w[0] = (g & 1) ? (v[i][1] >> 16) | (v[i][2] << 16) : v[i][0];
-            w[1] = (g & 1) ? v[i][2] >> 16 : v[i][1];
-        } else {
-#pragma unroll
-            for (int j = 0; j < S::vw; ++j)
-                w[j] = v[i][j];
+    // Wait for the oldest tile; its slot.  (A wait that gives up is recorded, and not repeated.)
+    __device__ __forceinline__ const unsigned char *take(const KvAttendParams &p, bool &ok,
+                                                         bool &dead) {
+        const uint32_t i = got % SLOTS;
+        if (!dead && !sm100::mbar_wait(bar0 + 16 * i, (got / SLOTS) & 1u)) {
+            dead = true;
+            atomicOr(p.err, AT_ERR_WAIT);
         }
+        ++got;
+        ok = *reinterpret_cast<const volatile int *>(sm + SLOTS * slot + 16 * i + 8) != 0;
+        return sm + i * slot;
     }
 };
 
-// A warp's queries: the B operands of S^T = K Q^T (row n = g, elements c D/4 + 4 ks + {0, 1}, {2, 3}),
-// in registers, or in shared memory where those do not hold them beside the accumulators.
+// Words of shared memory, in the widest loads that ALIGN bytes allow.
+template <int W, int ALIGN>
+__device__ __forceinline__ void take_words(uint32_t (&w)[W], const unsigned char *p) {
+    if constexpr (ALIGN % 16 == 0 && W % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < W; i += 4) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p + 4 * i);
+            w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+        }
+    } else if constexpr (ALIGN % 8 == 0 && W % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < W; i += 2) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p + 4 * i);
+            w[i] = v.x, w[i + 1] = v.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            w[i] = *reinterpret_cast<const uint32_t *>(p + 4 * i);
+    }
+}
+
+// This lane's elements (g D/8 on) of a value row.
+template <int D, int BITS>
+__device__ __forceinline__ void take_share(uint32_t (&w)[Shape<D, BITS>::vu],
+                                           const unsigned char *row, int g) {
+    using S = Shape<D, BITS>;
+    if constexpr (S::v_shared) {                     // 48 of the 96 bits of two lanes
+        uint32_t v[3];
+        take_words<3, 4>(v, row + (g >> 1) * S::v_bytes);
+        w[0] = (g & 1) ? (v[1] >> 16) | (v[2] << 16) : v[0];
+        w[1] = (g & 1) ? v[2] >> 16 : v[1];
+    } else {
+        take_words<S::vu, S::v_bytes>(w, row + g * S::v_bytes);
+    }
+}
+
+// A warp's queries: the B operands of S^T = K Q^T (row n = g, elements c D/4 + 4 ks + {0, 1}, {2, 3}).
 template <int D, int NT, bool SPLIT> struct Queries {
     static constexpr int KS = D / 16;
-    static constexpr bool shared = D == 256 && NT == 2;
     static constexpr int words = NT * KS * 32 * (SPLIT ? 2 : 1);     // uint2 of a tile
-    uint2 f[shared ? 1 : NT * KS * (SPLIT ? 2 : 1)];
-    const uint2 *sm;                                                 // at this lane
+    uint2 f[NT * KS * (SPLIT ? 2 : 1)];
     __device__ __forceinline__ void take(const uint2 *from) {       // at this lane
-        sm = from;
-        if constexpr (!shared) {
 #pragma unroll
-            for (int i = 0; i < NT * KS * (SPLIT ? 2 : 1); ++i)
-                f[i] = from[i * 32];
-        }
+        for (int i = 0; i < NT * KS * (SPLIT ? 2 : 1); ++i)
+            f[i] = from[i * 32];
     }
     __device__ __forceinline__ uint2 operator()(int part, int n, int ks) const {
-        const int i = (part * NT + n) * KS + ks;
-        return shared ? sm[i * 32] : f[shared ? 0 : i];
+        return f[(part * NT + n) * KS + ks];
     }
 };
 
@@ -181,39 +228,42 @@ template <int D, int NT> struct Sums {
 
 // Tiles t, t + stride, ... below `last` of one segment, by a warp.  `start` is called once the first
 // tiles are on their way, and fills `q`, `qs` (score factors of rows 2c, 2c + 1) and `masks`.
-template <int D, int BITS, int NT, bool SPLIT, class Start>
+template <int D, int BITS, int NT, bool SPLIT, int SLOTS, class Start>
 __device__ __forceinline__ void walk_tiles(const KvAttendParams &p, const unsigned char *lut,
-                                           const Seq &s, int b, int kvh, int t, int stride, int last,
-                                           Queries<D, NT, SPLIT> &q, float (&qs)[NT][2],
-                                           const unsigned long long *masks, Sums<D, NT> &o,
-                                           Start start) {
+                                           Ring<D, BITS, SLOTS> &ring, const Seq &s, int b, int kvh,
+                                           int t, int stride, int last, Queries<D, NT, SPLIT> &q,
+                                           float (&qs)[NT][2], const unsigned long long *masks,
+                                           Sums<D, NT> &o, Start start) {
     using S = Shape<D, BITS>;
     constexpr int KS = D / 16;
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const uint32_t col = lut_column<BITS>(lane);
     const int *table = p.table + (long long)b * p.table_width;
     const int in_page = (1 << p.c.page_log2) - 1;
-    Tile<D, BITS> cur;
-    bool bad_page = false;
+    bool bad_page = false, dead = false;
     auto place = [&](int t) -> int {              // a tile's page
         return t < last ? __ldg(table + ((t << 4) >> p.c.page_log2)) : -1;
     };
-    const int page = place(t);
-    int page1 = place(t + stride);
-    cur.keys(p, page, (t << 4) & in_page, kvh, g, c);
-    cur.values(p, page, (t << 4) & in_page, kvh, g, c);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < SLOTS; ++k)
+        if (t + k * stride < last)
+            ring.fetch(p, place(t + k * stride), ((t + k * stride) << 4) & in_page, kvh);
+    int page = place(t + SLOTS * stride);
     start();
 
     for (; t < last; t += stride) {
-        const int page2 = place(t + 2 * stride);
-        // the tile after the next on its way to the L2: a row of keys or values a lane
-        if (page2 >= 0 && page2 < p.c.pages) {
-            const long long row = (((long long)page2 * p.c.kv_heads + kvh) << p.c.page_log2) +
-                                  (((t + 2 * stride) << 4) & in_page) + (lane & 15);
-            const uint8_t *at = pick(p.c.codes, lane >> 4) + row * S::row_bytes;
+        const int ahead = t + SLOTS * stride, page1 = place(ahead + stride);
+        bool ok;
+        const unsigned char *tile = ring.take(p, ok, dead);
+        uint32_t kr[2][S::kw];
+        float kn[2], vn[2];
 #pragma unroll
-            for (int k = 0; k < S::row_bytes; k += 128)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(at + k));
+        for (int i = 0; i < 2; ++i) {
+            const int j = order(g) + 8 * i;
+            take_words<S::kw, S::k_bytes>(kr[i], tile + j * S::row_bytes + c * S::k_bytes);
+            kn[i] = *reinterpret_cast<const float *>(tile + 2 * Ring<D, BITS, SLOTS>::rows + 4 * j);
+            vn[i] = *reinterpret_cast<const float *>(tile + 2 * Ring<D, BITS, SLOTS>::rows + 64 + 4 * j);
         }
         // S^T = K Q^T, in two sums
         float st[NT][4], s2[NT][4];
@@ -225,8 +275,8 @@ __device__ __forceinline__ void walk_tiles(const KvAttendParams &p, const unsign
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             uint32_t a[4];
-            quad<BITS, true>(lut, cur.k[0], ks, col, a[0], a[2]);
-            quad<BITS, true>(lut, cur.k[1], ks, col, a[1], a[3]);
+            quad<BITS, true>(lut, kr[0], ks, col, a[0], a[2]);
+            quad<BITS, true>(lut, kr[1], ks, col, a[1], a[3]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 uint2 w = q(0, n, ks);
@@ -237,12 +287,7 @@ __device__ __forceinline__ void walk_tiles(const KvAttendParams &p, const unsign
                 }
             }
         }
-        // the next tile's keys are under way from here, its values from the end of this one: each a
-        // part of a tile ahead of its use, in the registers that this tile has done with
-        const float kn[2] = {cur.kn[0], cur.kn[1]}, vn[2] = {cur.vn[0], cur.vn[1]};
-        const bool ok = cur.ok;
-        cur.keys(p, page1, ((t + stride) << 4) & in_page, kvh, g, c);
-        // scores of tokens g, g + 8 and rows 2c, 2c + 1, in powers of two
+        // scores of tokens order(g), + 8 and rows 2c, 2c + 1, in powers of two
         bool grow = false;
         const int tok = t << 4;
         const bool edge = !ok || tok + 16 > s.prefix;     // the page is missing, or it has nodes
@@ -252,12 +297,13 @@ __device__ __forceinline__ void walk_tiles(const KvAttendParams &p, const unsign
             for (int i = 0; i < 4; ++i)
                 st[n][i] = (st[n][i] + s2[n][i]) * (kn[i >> 1] * qs[n][i & 1]);
         if (edge) {
+            // (a missing page's slot has what was there before: finite codes, any norms)
             bad_page |= !ok;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int node = tok + g + 8 * (i >> 1) - s.prefix;
+                    const int node = tok + order(g) + 8 * (i >> 1) - s.prefix;
                     const bool see = ok && (node < 0 || (node < s.nodes &&
                                      ((masks[8 * n + 2 * c + (i & 1)] >> node) & 1ull)));
                     if (!see)
@@ -333,7 +379,12 @@ __device__ __forceinline__ void walk_tiles(const KvAttendParams &p, const unsign
         uint32_t vw[4][S::vu];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            cur.share(i, g, vw[i]);
+            take_share<D, BITS>(vw[i], tile + Ring<D, BITS, SLOTS>::rows +
+                                           (c + 4 * (i & 1) + 8 * (i >> 1)) * S::row_bytes, g);
+        __syncwarp();                                 // all have read the slot
+        if (ahead < last)
+            ring.fetch(p, page, (ahead << 4) & in_page, kvh);
+        page = page1;
         mixed<BITS>(vw[0], vw[1]);
         mixed<BITS>(vw[2], vw[3]);
 #pragma unroll
@@ -349,8 +400,6 @@ __device__ __forceinline__ void walk_tiles(const KvAttendParams &p, const unsign
                     mma16816(o.acc[n][j + h], a, pb[n][0], pb[n][1]);
             }
         }
-        cur.values(p, page1, ((t + stride) << 4) & in_page, kvh, g, c);
-        page1 = page2;
     }
     if (bad_page && lane == 0)
         atomicOr(p.err, AT_ERR_PAGE);
@@ -366,14 +415,19 @@ __device__ __forceinline__ unsigned long long mask_of(const KvAttendParams &p, c
 
 // ---- much work: a worker a warp ----
 template <int D, int BITS, int NT, bool SPLIT> struct Stream {
-    // Warps of the one CTA on an SM.  (64 single tokens over contexts to 8191, 4 bits: 8, 10, 12, 16,
-    // 20 warps take 128, 113, 99, 103, 113 us: 16 and more have too few registers to load ahead.)
-    static constexpr int warps = D == 128 && NT == 1 ? 12 : 8;
+    // Warps of the one CTA on an SM.
+    static constexpr int warps = D == 128 && NT == 1 ? KW : 8;
     static constexpr int rows = 8 * NT;
-    using Q = Queries<D, NT, SPLIT>;
-    static constexpr int mask_at = Q::shared ? Q::words * 8 : 0;     // of a warp's own memory
-    static constexpr int own = mask_at + rows * 8;
+    // a warp's own memory: masks, and the ring of as many slots as there is room for
+    static constexpr int ring_at = rows * 8;
+    static constexpr int room = (225 * 1024 - Lut<BITS, true>::bytes) / warps - ring_at;
+    static constexpr int slots_in(int bytes) {
+        return bytes >= Ring<D, BITS, 4>::bytes ? 4 : bytes >= Ring<D, BITS, 3>::bytes ? 3 : 2;
+    }
+    static constexpr int slots = slots_in(room);
+    static constexpr int own = (ring_at + Ring<D, BITS, slots>::bytes + 15) / 16 * 16;
     static constexpr int bytes = Lut<BITS, true>::bytes + warps * own;
+    static_assert(bytes <= 227 * 1024, "shared memory");
 };
 
 template <int D, int BITS, int NT, bool SPLIT>
@@ -386,8 +440,10 @@ attend_tiles(const KvAttendParams p, const KvAttendSpace ws) {
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     unsigned char *own = sm + Lut<BITS, true>::bytes + warp * M::own;
-    unsigned long long *masks = reinterpret_cast<unsigned long long *>(own + M::mask_at);
+    unsigned long long *masks = reinterpret_cast<unsigned long long *>(own);
     fill_lut<BITS, true>(sm, p.lut);
+    Ring<D, BITS, M::slots> ring;
+    ring.init(own + M::ring_at);
     __syncthreads();
     pdl_wait();
     // neighbouring workers on different SMs: few units reach all of them
@@ -400,16 +456,11 @@ attend_tiles(const KvAttendParams p, const KvAttendSpace ws) {
         Sums<D, NT> o;
         o.clear();
         walk_tiles<D, BITS, NT, SPLIT>(
-            p, sm, piece.s, piece.b, piece.kvh, piece.tile0, 1, piece.tile0 + piece.n, q, qs, masks,
+            p, sm, ring, piece.s, piece.b, piece.kvh, piece.tile0, 1, piece.tile0 + piece.n, q, qs, masks,
             o, [&] {
                 const long long seg = (long long)piece.b * ws.segments + piece.seg;
                 const uint2 *from = ws.queries + seg * Q::words + lane;
                 __syncwarp();
-                if constexpr (Q::shared) {
-                    for (int i = 0; i < Q::words / 32; ++i)
-                        reinterpret_cast<uint2 *>(own)[i * 32 + lane] = from[i * 32];
-                    from = reinterpret_cast<const uint2 *>(own) + lane;
-                }
                 if (lane < M::rows)
                     masks[lane] = mask_of(p, piece.s, lane, piece.nrows, piece.row_base);
                 __syncwarp();
@@ -458,7 +509,9 @@ template <int D, int BITS, int NT, bool SPLIT> struct Near {
     static constexpr int x_at = q_at + Q::words * 8;                         // [warps][D] floats
     static constexpr int mask_at = x_at + warps * D * 4;
     static constexpr int stat_at = mask_at + rows * 8;                       // factor, m, l: [rows]
-    static constexpr int bytes = stat_at + rows * 12;
+    static constexpr int ring_at = (stat_at + rows * 12 + 15) / 16 * 16;
+    static constexpr int bytes = ring_at + warps * Ring<D, BITS, 2>::bytes;
+    static_assert(bytes <= 227 * 1024, "shared memory");
 };
 
 template <class E, int D, int BITS, int NT, bool SPLIT>
@@ -481,6 +534,8 @@ attend_near(const KvAttendParams p, const int row_tiles) {
     const int kvh = blockIdx.y / row_tiles, row_base = (blockIdx.y - kvh * row_tiles) * M::rows;
     const int b = blockIdx.z;
     fill_lut<BITS, true>(sm, p.lut);
+    Ring<D, BITS, 2> ring;
+    ring.init(sm + M::ring_at + warp * Ring<D, BITS, 2>::bytes);
     uint32_t ent[N];
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -498,7 +553,7 @@ attend_near(const KvAttendParams p, const int row_tiles) {
     Sums<D, NT> o;
     o.clear();
     walk_tiles<D, BITS, NT, SPLIT>(
-        p, sm, s, b, kvh, rank * share + warp, M::warps, min(tiles, (rank + 1) * share), q, qs,
+        p, sm, ring, s, b, kvh, rank * share + warp, M::warps, min(tiles, (rank + 1) * share), q, qs,
         masks, o, [&] {
             for (int r = warp; r < M::rows; r += M::warps) {
                 const float f = rotate_row<E, D, SPLIT>(p, s, kvh, row_base + r, r < nrows, ent,
@@ -672,23 +727,22 @@ cudaError_t launch_tile(const KvAttendParams &p, const KvAttendSpace &ws, int dt
                             : launch_stream<D, BITS, NT, true>(p, ws, st);
 }
 
+// Heads of 256 have no registers for two tiles of 8 rows.
 template <int BITS>
 cudaError_t launch_bits(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, int splits,
                         cudaStream_t st) {
-    const bool one = p.max_nodes * p.group <= 8;
-    if (p.c.d == 128)
-        return one ? launch_tile<BITS, 128, 1>(p, ws, dtype, splits, st)
-                   : launch_tile<BITS, 128, 2>(p, ws, dtype, splits, st);
-    return one ? launch_tile<BITS, 256, 1>(p, ws, dtype, splits, st)
-               : launch_tile<BITS, 256, 2>(p, ws, dtype, splits, st);
+    if (p.c.d == 256)
+        return launch_tile<BITS, 256, 1>(p, ws, dtype, splits, st);
+    return p.max_nodes * p.group <= 8 ? launch_tile<BITS, 128, 1>(p, ws, dtype, splits, st)
+                                      : launch_tile<BITS, 128, 2>(p, ws, dtype, splits, st);
 }
 
 // Workers of attend_tiles on `sms` SMs.
 template <int BITS> int workers_bits(const KvAttendParams &p, int sms) {
-    const bool one = p.max_nodes * p.group <= 8;
-    if (p.c.d == 128)
-        return sms * (one ? Stream<128, BITS, 1, false>::warps : Stream<128, BITS, 2, false>::warps);
-    return sms * (one ? Stream<256, BITS, 1, false>::warps : Stream<256, BITS, 2, false>::warps);
+    if (p.c.d == 256)
+        return sms * Stream<256, BITS, 1, false>::warps;
+    return sms * (p.max_nodes * p.group <= 8 ? Stream<128, BITS, 1, false>::warps
+                                             : Stream<128, BITS, 2, false>::warps);
 }
 
 }  // namespace attend

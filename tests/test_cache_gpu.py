@@ -395,7 +395,7 @@ class Serving:
     """A cache filled with random codes, ragged sequences, and the oracle's view of them."""
 
     def __init__(self, oq, prefixes, nodes, hq, hk, d, h, bits, page, dtype, seed, size=1.5,
-                 extra_rows=0):
+                 extra_rows=0, columns=0):
         self.oq, self.hq, self.hk, self.d, self.page, self.dtype = oq, hq, hk, d, page, dtype
         rng = np.random.default_rng(seed)
         self.prefixes, self.nodes, self.bits = list(prefixes), list(nodes), bits
@@ -403,7 +403,7 @@ class Serving:
         need = [-(-t // page) for t in total]
         pages = sum(need) + 3
         order = rng.permutation(pages)
-        self.table = np.full((len(total), max(need + [1]) + 1), -1, dtype=np.int32)
+        self.table = np.full((len(total), max(need + [1]) + 1 + columns), -1, dtype=np.int32)
         at = 0
         for b, n in enumerate(need):
             self.table[b, :n] = order[at:at + n]
@@ -523,11 +523,18 @@ ATTEND = [
 ]
 
 
+# A page table that could hold this many tokens more makes a call one of much work, which is shared
+# out to all SMs (few rows), instead of one for clusters.
+ROOMY = 1 << 19
+
+
 @pytest.mark.parametrize("case", range(len(ATTEND)))
 @pytest.mark.parametrize("tree", [False, True])
-def test_attend_matches_fp64(oq, case, tree):
+@pytest.mark.parametrize("roomy", [False, True])
+def test_attend_matches_fp64(oq, case, tree, roomy):
     prefixes, nodes, hq, hk, d, h, bits, page, dtype = ATTEND[case]
-    s = Serving(oq, prefixes, nodes, hq, hk, d, h, bits, page, dtype, seed=case)
+    s = Serving(oq, prefixes, nodes, hq, hk, d, h, bits, page, dtype, seed=case,
+                columns=ROOMY // page if roomy else 0)
     if tree:
         s.trees()
     s.hide(float("nan"))
@@ -539,17 +546,21 @@ def test_attend_matches_fp64(oq, case, tree):
 @pytest.mark.parametrize("d,bits,dtype,nodes", [(128, 4, BF16, 1), (256, 3, F16, 1),
                                                 (128, 8, BF16, 40)])
 @pytest.mark.parametrize("hidden", [float("inf"), 3e38])
-def test_hidden_tokens_weigh_nothing(oq, d, bits, dtype, nodes, hidden):
-    s = Serving(oq, [37, 250], [nodes, nodes], 8, 2, d, 128, bits, 16, dtype, seed=3).trees()
+@pytest.mark.parametrize("roomy", [False, True])
+def test_hidden_tokens_weigh_nothing(oq, d, bits, dtype, nodes, hidden, roomy):
+    s = Serving(oq, [37, 250], [nodes, nodes], 8, 2, d, 128, bits, 16, dtype, seed=3,
+                columns=ROOMY // 16 if roomy else 0).trees()
     s.hide(hidden)
     out = oq.oq_kv_attend(**s.gpu())
     oq.oq_check()
     close(out, s.want(), dtype)
 
 
-@pytest.mark.parametrize("nodes", [[1, 1, 1], [5, 9, 1], [50, 64, 3]])
-def test_rows_that_see_nothing_give_zeros(oq, nodes):
-    s = Serving(oq, [0, 40, 0], nodes, 8, 2, 128, 128, 4, 16, BF16, seed=7).trees(empty=0.5)
+@pytest.mark.parametrize("nodes", [[1, 1, 1], [2, 4, 1], [5, 9, 1], [50, 64, 3]])
+@pytest.mark.parametrize("roomy", [False, True])
+def test_rows_that_see_nothing_give_zeros(oq, nodes, roomy):
+    s = Serving(oq, [0, 40, 0], nodes, 8, 2, 128, 128, 4, 16, BF16, seed=7,
+                columns=ROOMY // 16 if roomy else 0).trees(empty=0.5)
     s.mask[:nodes[0]] = 0
     s.hide(float("nan"))
     out = oq.oq_kv_attend(**s.gpu())
@@ -558,20 +569,24 @@ def test_rows_that_see_nothing_give_zeros(oq, nodes):
     close(out, s.want(), BF16)
 
 
-def test_sequences_without_rows_and_rows_behind_the_last(oq):
-    s = Serving(oq, [9, 100, 33, 0], [0, 3, 0, 2], 4, 2, 128, 128, 4, 16, BF16, seed=8,
-                extra_rows=6)
+@pytest.mark.parametrize("nodes,roomy", [([0, 3, 0, 2], False), ([0, 3, 0, 2], True),
+                                         ([0, 40, 0, 13], False), ([0, 0, 0, 0], True)])
+def test_sequences_without_rows_and_rows_behind_the_last(oq, nodes, roomy):
+    s = Serving(oq, [9, 100, 33, 0], nodes, 4, 2, 128, 128, 4, 16, BF16, seed=8,
+                extra_rows=6, columns=ROOMY // 16 if roomy else 0)
     a = s.gpu()
     out = torch.full_like(a["q"], 42.0)
     oq.oq_kv_attend(**a, out=out)
     oq.oq_check()
     assert torch.all(out[s.rows:] == 42.0)
-    close(out[:s.rows], s.want(), BF16)
+    if s.rows:
+        close(out[:s.rows], s.want(), BF16)
 
 
-@pytest.mark.parametrize("nodes", [1, 24])
-def test_sequences_that_do_not_fit_are_skipped_and_reported(oq, nodes):
-    s = Serving(oq, [20, 50, 60], [nodes] * 3, 4, 2, 128, 128, 4, 16, BF16, seed=9)
+@pytest.mark.parametrize("nodes,roomy", [(1, False), (1, True), (24, False)])
+def test_sequences_that_do_not_fit_are_skipped_and_reported(oq, nodes, roomy):
+    s = Serving(oq, [20, 50, 60], [nodes] * 3, 4, 2, 128, 128, 4, 16, BF16, seed=9,
+                columns=ROOMY // 16 if roomy else 0)
     good = oq.oq_kv_attend(**s.gpu())
     oq.oq_check()
 
@@ -636,10 +651,40 @@ def test_one_hot_softmax_and_value_sizes(oq):
     assert np.all(err <= 0.06 * np.linalg.norm(want, axis=-1))
 
 
-@pytest.mark.parametrize("B,nodes", [(3, 1), (2, 20)])
-def test_results_do_not_depend_on_the_batch_or_the_run(oq, B, nodes):
-    """The same rows alone, in a batch, and again: the same bits (no atomics decide an order)."""
-    s = Serving(oq, [333, 1500, 64][:B], [nodes] * B, 8, 2, 128, 128, 4, 16, BF16, seed=13).trees()
+@pytest.mark.parametrize("lengths,heads,nodes,bits,dtype", [
+    ([3000, 17, 900, 4097, 0, 1, 2222, 128], 2, 1, 4, BF16),       # all SMs share ragged lengths
+    ([2500, 1300], 2, 3, 3, F16),
+    ([5000, 700], 1, 2, 8, BF16),
+    ([3111, 40, 1290], 1, 33, 4, BF16),                            # many rows, many pieces
+    ([2900, 128], 1, 64, 8, F16),
+    ([4500], 1, 40, 2, BF16),
+    ([1500, 3000], 1, 24, 6, BF16),
+    ([2000, 64], 1, 17, 3, F16),
+])
+def test_long_and_ragged_contexts(oq, lengths, heads, nodes, bits, dtype):
+    """Contexts that many workers share: every piece of every row finds its place."""
+    s = Serving(oq, lengths, [nodes] * len(lengths), 2 * heads, heads, 128, 64, bits, 16, dtype,
+                seed=40 + nodes, columns=ROOMY // 16).trees()
+    s.hide(float("nan"))
+    out = oq.oq_kv_attend(**s.gpu())
+    oq.oq_check()
+    close(out, s.want(), dtype)
+
+
+@pytest.mark.parametrize("d,bits", [(256, 4), (256, 8)])
+def test_wide_heads_over_long_contexts(oq, d, bits):
+    s = Serving(oq, [1800, 33, 700], [6, 1, 4], 4, 1, d, 128, bits, 32, BF16, seed=50,
+                columns=ROOMY // 32).trees()
+    out = oq.oq_kv_attend(**s.gpu())
+    oq.oq_check()
+    close(out, s.want(), BF16)
+
+
+@pytest.mark.parametrize("B,nodes,roomy", [(3, 1, False), (3, 1, True), (2, 20, False)])
+def test_results_do_not_depend_on_the_run(oq, B, nodes, roomy):
+    """The same call again: the same bits (no atomics decide an order)."""
+    s = Serving(oq, [333, 1500, 64][:B], [nodes] * B, 8, 2, 128, 128, 4, 16, BF16, seed=13,
+                columns=ROOMY // 16 if roomy else 0).trees()
     a = s.gpu()
     out = oq.oq_kv_attend(**a)
     for _ in range(5):
@@ -648,9 +693,9 @@ def test_results_do_not_depend_on_the_batch_or_the_run(oq, B, nodes):
 
 
 def test_two_streams_and_a_captured_graph(oq):
-    """Calls on two streams at once, and a graph replayed while another call runs."""
-    cases = [Serving(oq, [900, 40], [n, n], 8, 2, 128, 128, 4, 16, BF16, seed=20 + n).trees()
-             for n in (1, 17)]
+    """Calls on two streams at once, and two graphs replayed at once."""
+    cases = [Serving(oq, [900, 40], [n, n], 8, 2, 128, 128, 4, 16, BF16, seed=20 + n,
+                     columns=ROOMY // 16).trees() for n in (1, 17)]
     args = [c.gpu() for c in cases]
     want = [oq.oq_kv_attend(**a) for a in args]
     torch.cuda.synchronize()
