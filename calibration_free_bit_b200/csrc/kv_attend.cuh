@@ -15,10 +15,10 @@
 //     what a warp has of a segment goes to the workspace, and a second kernel joins the pieces in a
 //     fixed order.  Little work (attend_near): a cluster of CTAs takes a segment, and its warps meet
 //     in shared memory, in one launch without a workspace;
-//   - a warp's tiles come into its own ring in shared memory by bulk copies (a tile's rows of a head
-//     lie together), several tiles ahead of their use, without a load instruction or a register; a
-//     lane's codes go through a table in shared memory with a column a lane (no bank conflicts)
-//     into the operand of a matrix instruction;
+//   - a warp's tiles come into its own ring in shared memory by asynchronous copies (a tile's rows
+//     of a head lie together), several tiles ahead of their use, without a register; a lane's codes
+//     go through a table in shared memory with a column a lane (no bank conflicts) into the operand
+//     of a matrix instruction;
 //   - products are transposed, S^T = K Q^T and O^T = V^T P^T (mma.sync m16n8k16): the 16-wide side
 //     is the cache, so 8 rows fill an instruction and an accumulator takes 32 registers.  The
 //     instruction's order of a row's elements is free as long as both operands agree, which is how
@@ -30,9 +30,6 @@
 // 2^14: what a token adds is resolved down to 2^-31 of the largest.  With SPLIT (fp16 outputs) a
 // query enters as a sum of two fp16 numbers: its rounding is the one that scores multiply.
 #pragma once
-#ifndef KW
-#define KW 12
-#endif
 
 #include <cooperative_groups.h>
 
@@ -76,7 +73,10 @@ template <int D, int BITS> struct Shape {
 };
 
 // A warp's ring of tiles in shared memory: 16 key rows, 16 value rows and their norms each, brought in
-// by bulk copies as many tiles ahead as there are slots.
+// by asynchronous copies of 16 bytes a lane as many tiles ahead as there are slots.  (A tile's rows lie
+// together, so a lane's addresses cost little; bulk copies by one lane took 120 instructions a tile,
+// with nothing to do for the other lanes, and 102 us instead of 87 for
+// 64 sequences of 37 to 8191 tokens, 8 heads of 128, 4 bits, pages of 16.)
 // Row j of a tile's matrices is token order(j) of its 16: the four value rows that a warp reads in one
 // go then lie together.
 __device__ __forceinline__ int order(int j) { return (j & 8) + ((j & 7) >> 1) + ((j & 1) << 2); }
@@ -84,84 +84,79 @@ __device__ __forceinline__ int order(int j) { return (j & 8) + ((j & 7) >> 1) + 
 template <int D, int BITS, int SLOTS> struct Ring {
     using S = Shape<D, BITS>;
     static constexpr int rows = 16 * S::row_bytes;
-    static constexpr int slot = 2 * rows + 128;       // keys, values, their norms
-    static constexpr int bytes = SLOTS * (slot + 16); // barriers and flags behind the slots
-    unsigned char *sm;
-    uint32_t at, bar0;                                // addresses of the slots, of the barriers
-    uint32_t put, got;                                // tiles so far
+    static constexpr int kn_at = 2 * rows, vn_at = kn_at + 64;
+    static constexpr int slot = vn_at + 64;           // keys, values, their norms
+    static constexpr int bytes = SLOTS * slot;
+    uint32_t at, put, got;                            // address; offsets of the next to fill and read
+    uint32_t known;                                   // bit i: the page of the i-th last tile is one
 
-    __device__ __forceinline__ void init(unsigned char *own) {
-        sm = own;
-        at = sm100::smem_u32(own);
-        bar0 = at + SLOTS * slot;
-        put = got = 0;
-        if ((threadIdx.x & 31) == 0) {
-            for (int i = 0; i < SLOTS; ++i)
-                sm100::mbar_init(bar0 + 16 * i, 1);
-            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        }
-        __syncwarp();
+    __device__ __forceinline__ void init(uint32_t own) {
+        at = own;
+        put = got = known = 0;
     }
-    // The next slot takes the tile of tokens `in` .. `in` + 15 of a page (lane 0; the slot's last
-    // readers are done).
-    __device__ __forceinline__ void fetch(const KvAttendParams &p, int page, int in, int kvh) {
-        const uint32_t i = put++ % SLOTS, bar = bar0 + 16 * i;
-        if ((threadIdx.x & 31) != 0)
-            return;
+    __device__ __forceinline__ static void copy16(uint32_t to, const void *from) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    }
+    // The next slot (its last readers are done) takes 16 tokens of a page from `in` on.  A missing
+    // page leaves it as it was.
+    __device__ __forceinline__ void fetch(const KvAttendParams &p, int page, int in, int kvh,
+                                          int lane) {
         const bool ok = page >= 0 && page < p.c.pages;
-        *reinterpret_cast<int *>(sm + SLOTS * slot + 16 * i + 8) = ok;
-        if (!ok) {
-            sm100::mbar_arrive(bar);
-            return;
+        known = (known << 1) | (ok ? 1u : 0u);
+        if (ok) {
+            const uint32_t to = at + put + lane * 16;
+            const long long row =
+                (((long long)page * p.c.kv_heads + kvh) << p.c.page_log2) + in;
+            const uint8_t *k = p.c.codes[0] + row * S::row_bytes + lane * 16;
+            const uint8_t *v = p.c.codes[1] + row * S::row_bytes + lane * 16;
+#pragma unroll
+            for (int i = 0; i < rows; i += 512)
+                if (i + 512 <= rows || i + lane * 16 < rows) {
+                    copy16(to + i, k + i);
+                    copy16(to + rows + i, v + i);
+                }
+            if (lane < 8)
+                copy16(to + kn_at, pick(p.c.norms, lane >> 2) + row + (lane & 3) * 4);
         }
-        const long long row = (((long long)page * p.c.kv_heads + kvh) << p.c.page_log2) + in;
-        const uint32_t to = at + i * slot;
-        sm100::mbar_expect_tx(bar, slot);
-        k1ops::bulk_copy(to, p.c.codes[0] + row * S::row_bytes, rows, bar);
-        k1ops::bulk_copy(to + rows, p.c.codes[1] + row * S::row_bytes, rows, bar);
-        k1ops::bulk_copy(to + 2 * rows, p.c.norms[0] + row, 64, bar);
-        k1ops::bulk_copy(to + 2 * rows + 64, p.c.norms[1] + row, 64, bar);
+        put = put + slot == bytes ? 0 : put + slot;
     }
-    // Wait for the oldest tile; its slot.  (A wait that gives up is recorded, and not repeated.)
-    __device__ __forceinline__ const unsigned char *take(const KvAttendParams &p, bool &ok,
-                                                         bool &dead) {
-        const uint32_t i = got % SLOTS;
-        if (!dead && !sm100::mbar_wait(bar0 + 16 * i, (got / SLOTS) & 1u)) {
-            dead = true;
-            atomicOr(p.err, AT_ERR_WAIT);
-        }
-        ++got;
-        ok = *reinterpret_cast<const volatile int *>(sm + SLOTS * slot + 16 * i + 8) != 0;
-        return sm + i * slot;
+    __device__ __forceinline__ static void commit() {
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // The oldest slot of SLOTS: its address, and whether its page is one.
+    __device__ __forceinline__ uint32_t take(bool &ok) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 1) : "memory");
+        __syncwarp();
+        const uint32_t from = at + got;
+        ok = (known >> (SLOTS - 1)) & 1u;
+        got = got + slot == bytes ? 0 : got + slot;
+        return from;
     }
 };
 
 // Words of shared memory, in the widest loads that ALIGN bytes allow.
 template <int W, int ALIGN>
-__device__ __forceinline__ void take_words(uint32_t (&w)[W], const unsigned char *p) {
+__device__ __forceinline__ void take_words(uint32_t (&w)[W], uint32_t at) {
     if constexpr (ALIGN % 16 == 0 && W % 4 == 0) {
 #pragma unroll
-        for (int i = 0; i < W; i += 4) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(p + 4 * i);
-            w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
-        }
+        for (int i = 0; i < W; i += 4)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                         : "r"(at + 4 * i));
     } else if constexpr (ALIGN % 8 == 0 && W % 2 == 0) {
 #pragma unroll
-        for (int i = 0; i < W; i += 2) {
-            const uint2 v = *reinterpret_cast<const uint2 *>(p + 4 * i);
-            w[i] = v.x, w[i + 1] = v.y;
-        }
+        for (int i = 0; i < W; i += 2)
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[i]), "=r"(w[i + 1]) : "r"(at + 4 * i));
     } else {
 #pragma unroll
         for (int i = 0; i < W; ++i)
-            w[i] = *reinterpret_cast<const uint32_t *>(p + 4 * i);
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[i]) : "r"(at + 4 * i));
     }
 }
 
 // This lane's elements (g D/8 on) of a value row.
 template <int D, int BITS>
-__device__ __forceinline__ void take_share(uint32_t (&w)[Shape<D, BITS>::vu],
-                                           const unsigned char *row, int g) {
+__device__ __forceinline__ void take_share(uint32_t (&w)[Shape<D, BITS>::vu], uint32_t row, int g) {
     using S = Shape<D, BITS>;
     if constexpr (S::v_shared) {                     // 48 of the 96 bits of two lanes
         uint32_t v[3];
@@ -228,42 +223,49 @@ template <int D, int NT> struct Sums {
 
 // Tiles t, t + stride, ... below `last` of one segment, by a warp.  `start` is called once the first
 // tiles are on their way, and fills `q`, `qs` (score factors of rows 2c, 2c + 1) and `masks`.
-template <int D, int BITS, int NT, bool SPLIT, int SLOTS, class Start>
-__device__ __forceinline__ void walk_tiles(const KvAttendParams &p, const unsigned char *lut,
+// `col`: lut_column's.
+template <LutForm FORM, int D, int BITS, int NT, bool SPLIT, int SLOTS, class Start>
+__device__ __forceinline__ void walk_tiles(const KvAttendParams &p, uint32_t col,
                                            Ring<D, BITS, SLOTS> &ring, const Seq &s, int b, int kvh,
                                            int t, int stride, int last, Queries<D, NT, SPLIT> &q,
                                            float (&qs)[NT][2], const unsigned long long *masks,
                                            Sums<D, NT> &o, Start start) {
     using S = Shape<D, BITS>;
+    using R = Ring<D, BITS, SLOTS>;
     constexpr int KS = D / 16;
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const uint32_t col = lut_column<BITS>(lane);
     const int *table = p.table + (long long)b * p.table_width;
     const int in_page = (1 << p.c.page_log2) - 1;
-    bool bad_page = false, dead = false;
+    bool bad_page = false;
+    // where this lane's parts of a slot lie
+    const uint32_t k_off = order(g) * S::row_bytes + c * S::k_bytes, n_off = R::kn_at + 4 * order(g);
+    const uint32_t v_off = R::rows + c * S::row_bytes;
     auto place = [&](int t) -> int {              // a tile's page
         return t < last ? __ldg(table + ((t << 4) >> p.c.page_log2)) : -1;
     };
     __syncwarp();
-#pragma unroll
-    for (int k = 0; k < SLOTS; ++k)
-        if (t + k * stride < last)
-            ring.fetch(p, place(t + k * stride), ((t + k * stride) << 4) & in_page, kvh);
+    for (int k = 0; k < SLOTS; ++k) {
+        ring.fetch(p, place(t + k * stride), ((t + k * stride) << 4) & in_page, kvh, lane);
+        ring.commit();
+    }
     int page = place(t + SLOTS * stride);
     start();
 
     for (; t < last; t += stride) {
         const int ahead = t + SLOTS * stride, page1 = place(ahead + stride);
+        const int tok = t << 4;
         bool ok;
-        const unsigned char *tile = ring.take(p, ok, dead);
+        const uint32_t tile = ring.take(ok);
         uint32_t kr[2][S::kw];
         float kn[2], vn[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int j = order(g) + 8 * i;
-            take_words<S::kw, S::k_bytes>(kr[i], tile + j * S::row_bytes + c * S::k_bytes);
-            kn[i] = *reinterpret_cast<const float *>(tile + 2 * Ring<D, BITS, SLOTS>::rows + 4 * j);
-            vn[i] = *reinterpret_cast<const float *>(tile + 2 * Ring<D, BITS, SLOTS>::rows + 64 + 4 * j);
+            take_words<S::kw, S::k_bytes>(kr[i], tile + k_off + 8 * i * S::row_bytes);
+            uint32_t u[1];
+            take_words<1, 4>(u, tile + n_off + 32 * i);
+            kn[i] = __uint_as_float(u[0]);
+            take_words<1, 4>(u, tile + n_off + 32 * i + (R::vn_at - R::kn_at));
+            vn[i] = __uint_as_float(u[0]);
         }
         // S^T = K Q^T, in two sums
         float st[NT][4], s2[NT][4];
@@ -275,8 +277,8 @@ __device__ __forceinline__ void walk_tiles(const KvAttendParams &p, const unsign
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             uint32_t a[4];
-            quad<BITS, true>(lut, kr[0], ks, col, a[0], a[2]);
-            quad<BITS, true>(lut, kr[1], ks, col, a[1], a[3]);
+            quad<BITS, FORM>(kr[0], ks, col, a[0], a[2]);
+            quad<BITS, FORM>(kr[1], ks, col, a[1], a[3]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 uint2 w = q(0, n, ks);
@@ -289,7 +291,6 @@ __device__ __forceinline__ void walk_tiles(const KvAttendParams &p, const unsign
         }
         // scores of tokens order(g), + 8 and rows 2c, 2c + 1, in powers of two
         bool grow = false;
-        const int tok = t << 4;
         const bool edge = !ok || tok + 16 > s.prefix;     // the page is missing, or it has nodes
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -379,19 +380,18 @@ __device__ __forceinline__ void walk_tiles(const KvAttendParams &p, const unsign
         uint32_t vw[4][S::vu];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            take_share<D, BITS>(vw[i], tile + Ring<D, BITS, SLOTS>::rows +
-                                           (c + 4 * (i & 1) + 8 * (i >> 1)) * S::row_bytes, g);
+            take_share<D, BITS>(vw[i], tile + v_off + (4 * (i & 1) + 8 * (i >> 1)) * S::row_bytes, g);
         __syncwarp();                                 // all have read the slot
-        if (ahead < last)
-            ring.fetch(p, page, (ahead << 4) & in_page, kvh);
+        ring.fetch(p, page, (ahead << 4) & in_page, kvh, lane);
+        ring.commit();
         page = page1;
         mixed<BITS>(vw[0], vw[1]);
         mixed<BITS>(vw[2], vw[3]);
 #pragma unroll
         for (int j = 0; j < KS; j += 2) {
             uint32_t x[4], y[4];
-            quad_of_two<BITS, true>(lut, vw[0], vw[1], j / 2, col, x);
-            quad_of_two<BITS, true>(lut, vw[2], vw[3], j / 2, col, y);
+            quad_of_two<BITS, FORM>(vw[0], vw[1], j / 2, col, x);
+            quad_of_two<BITS, FORM>(vw[2], vw[3], j / 2, col, y);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint32_t a[4] = {x[2 * h], x[2 * h + 1], y[2 * h], y[2 * h + 1]};
@@ -414,20 +414,28 @@ __device__ __forceinline__ unsigned long long mask_of(const KvAttendParams &p, c
 }
 
 // ---- much work: a worker a warp ----
+// Shared memory by address (a CTA's own starts at 1024): a table of 64 KB, or of 8, at the first
+// multiple of its size, the warps' own parts (masks, ring) before and behind it.
 template <int D, int BITS, int NT, bool SPLIT> struct Stream {
-    // Warps of the one CTA on an SM.
-    static constexpr int warps = D == 128 && NT == 1 ? KW : 8;
+    // of the one CTA on an SM: as many as registers allow (12 took 106 us, 16 took 101)
+    static constexpr int warps = D == 128 && NT == 1 ? 16 : 8;
     static constexpr int rows = 8 * NT;
-    // a warp's own memory: masks, and the ring of as many slots as there is room for
-    static constexpr int ring_at = rows * 8;
-    static constexpr int room = (225 * 1024 - Lut<BITS, true>::bytes) / warps - ring_at;
-    static constexpr int slots_in(int bytes) {
-        return bytes >= Ring<D, BITS, 4>::bytes ? 4 : bytes >= Ring<D, BITS, 3>::bytes ? 3 : 2;
+    static constexpr int lut = Lut<BITS, WIDE>::bytes, lut_at = lut;
+    static constexpr int most = 227 * 1024 + kSharedStart;
+    template <int SLOTS> static constexpr int own_of() {
+        return (rows * 8 + Ring<D, BITS, SLOTS>::bytes + 127) / 128 * 128;
     }
-    static constexpr int slots = slots_in(room);
-    static constexpr int own = (ring_at + Ring<D, BITS, slots>::bytes + 15) / 16 * 16;
-    static constexpr int bytes = Lut<BITS, true>::bytes + warps * own;
-    static_assert(bytes <= 227 * 1024, "shared memory");
+    template <int SLOTS> static constexpr bool fits() {
+        return (lut_at - kSharedStart) / own_of<SLOTS>() + (most - lut_at - lut) / own_of<SLOTS>() >= warps;
+    }
+    static constexpr int slots = fits<4>() ? 4 : fits<3>() ? 3 : 2;
+    static constexpr int own = own_of<slots>(), before = (lut_at - kSharedStart) / own;
+    static constexpr int behind = warps > before ? warps - before : 0;
+    static constexpr int bytes = lut_at + lut + behind * own - kSharedStart;
+    static_assert(fits<slots>() && bytes <= 227 * 1024, "shared memory");
+    __device__ static int own_at(int warp) {
+        return warp < before ? kSharedStart + warp * own : lut_at + lut + (warp - before) * own;
+    }
 };
 
 template <int D, int BITS, int NT, bool SPLIT>
@@ -436,14 +444,20 @@ attend_tiles(const KvAttendParams p, const KvAttendSpace ws) {
     using M = Stream<D, BITS, NT, SPLIT>;
     using Q = Queries<D, NT, SPLIT>;
     constexpr int KS = D / 16;
-    extern __shared__ __align__(128) unsigned char sm[];
+    extern __shared__ __align__(1024) unsigned char raw[];
+    if (!starts_there(raw)) {                             // not where the layout expects it
+        if (threadIdx.x == 0)
+            atomicOr(p.err, AT_ERR_WAIT);
+        return;
+    }
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    unsigned char *own = sm + Lut<BITS, true>::bytes + warp * M::own;
-    unsigned long long *masks = reinterpret_cast<unsigned long long *>(own);
-    fill_lut<BITS, true>(sm, p.lut);
+    const int own = M::own_at(warp);
+    unsigned long long *masks = reinterpret_cast<unsigned long long *>(at_address(raw, own));
+    fill_lut<BITS, WIDE>(at_address(raw, M::lut_at), p.lut);
+    const uint32_t col = lut_column<BITS, WIDE>(M::lut_at, lane);
     Ring<D, BITS, M::slots> ring;
-    ring.init(own + M::ring_at);
+    ring.init(own + M::rows * 8);
     __syncthreads();
     pdl_wait();
     // neighbouring workers on different SMs: few units reach all of them
@@ -455,8 +469,8 @@ attend_tiles(const KvAttendParams p, const KvAttendSpace ws) {
         float qs[NT][2];
         Sums<D, NT> o;
         o.clear();
-        walk_tiles<D, BITS, NT, SPLIT>(
-            p, sm, ring, piece.s, piece.b, piece.kvh, piece.tile0, 1, piece.tile0 + piece.n, q, qs, masks,
+        walk_tiles<WIDE, D, BITS, NT, SPLIT>(
+            p, col, ring, piece.s, piece.b, piece.kvh, piece.tile0, 1, piece.tile0 + piece.n, q, qs, masks,
             o, [&] {
                 const long long seg = (long long)piece.b * ws.segments + piece.seg;
                 const uint2 *from = ws.queries + seg * Q::words + lane;
@@ -496,22 +510,25 @@ attend_tiles(const KvAttendParams p, const KvAttendSpace ws) {
 }
 
 // ---- little work: a cluster a segment ----
+// Shared memory by address, as above, with the smaller table: two CTAs fit on an SM.
 template <int D, int BITS, int NT, bool SPLIT> struct Near {
     static constexpr int warps = 8, rows = 8 * NT;
     using Q = Queries<D, NT, SPLIT>;
+    using R = Ring<D, BITS, 2>;
     static constexpr int part = (D / 16) * NT * 4 * 128 + NT * 4 * 128;      // a warp's sums
     static constexpr int fin_stride = D + 4;                                 // floats
     static constexpr int most(int a, int b) { return a > b ? a : b; }
-    // the table, then the warps' sums, then the block's
-    static constexpr int big = most(most(Lut<BITS, true>::bytes, warps / 2 * part),
-                                    rows * fin_stride * 4);
-    static constexpr int q_at = big;
+    static constexpr int q_at = kSharedStart;
     static constexpr int x_at = q_at + Q::words * 8;                         // [warps][D] floats
     static constexpr int mask_at = x_at + warps * D * 4;
     static constexpr int stat_at = mask_at + rows * 8;                       // factor, m, l: [rows]
-    static constexpr int ring_at = (stat_at + rows * 12 + 15) / 16 * 16;
-    static constexpr int bytes = ring_at + warps * Ring<D, BITS, 2>::bytes;
-    static_assert(bytes <= 227 * 1024, "shared memory");
+    static constexpr int lut_at = 32768;
+    // the table, then the warps' sums, then the block's
+    static constexpr int big = most(most(Lut<BITS, PLACED>::bytes, warps / 2 * part),
+                                    rows * fin_stride * 4);
+    static constexpr int ring_at = (lut_at + big + 127) / 128 * 128;
+    static constexpr int bytes = ring_at + warps * R::bytes - kSharedStart;
+    static_assert(stat_at + rows * 12 <= lut_at && bytes <= 227 * 1024, "shared memory");
 };
 
 template <class E, int D, int BITS, int NT, bool SPLIT>
@@ -520,12 +537,19 @@ attend_near(const KvAttendParams p, const int row_tiles) {
     using M = Near<D, BITS, NT, SPLIT>;
     using Q = Queries<D, NT, SPLIT>;
     constexpr int N = D / 32, KS = D / 16;
-    extern __shared__ __align__(128) unsigned char sm[];
+    extern __shared__ __align__(1024) unsigned char raw[];
     namespace cg = cooperative_groups;
-    uint2 *qm = reinterpret_cast<uint2 *>(sm + M::q_at);
-    float *xs = reinterpret_cast<float *>(sm + M::x_at);
-    unsigned long long *masks = reinterpret_cast<unsigned long long *>(sm + M::mask_at);
-    float *factor = reinterpret_cast<float *>(sm + M::stat_at);
+    if (!starts_there(raw)) {                             // not where the layout expects it
+        if (threadIdx.x == 0)
+            atomicOr(p.err, AT_ERR_WAIT);
+        cg::this_cluster().sync();                         // the others read this block's memory
+        cg::this_cluster().sync();
+        return;
+    }
+    uint2 *qm = reinterpret_cast<uint2 *>(at_address(raw, M::q_at));
+    float *xs = reinterpret_cast<float *>(at_address(raw, M::x_at));
+    unsigned long long *masks = reinterpret_cast<unsigned long long *>(at_address(raw, M::mask_at));
+    float *factor = reinterpret_cast<float *>(at_address(raw, M::stat_at));
     float *row_m = factor + M::rows, *row_l = row_m + M::rows;
 
     pdl_trigger();
@@ -533,9 +557,10 @@ attend_near(const KvAttendParams p, const int row_tiles) {
     const int rank = blockIdx.x, splits = gridDim.x;       // the cluster is the whole x dimension
     const int kvh = blockIdx.y / row_tiles, row_base = (blockIdx.y - kvh * row_tiles) * M::rows;
     const int b = blockIdx.z;
-    fill_lut<BITS, true>(sm, p.lut);
-    Ring<D, BITS, 2> ring;
-    ring.init(sm + M::ring_at + warp * Ring<D, BITS, 2>::bytes);
+    fill_lut<BITS, PLACED>(at_address(raw, M::lut_at), p.lut);
+    const uint32_t col = lut_column<BITS, PLACED>(rank_bits(raw) | M::lut_at, lane);
+    typename M::R ring;
+    ring.init(rank_bits(raw) | (M::ring_at + warp * M::R::bytes));
     uint32_t ent[N];
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -552,8 +577,8 @@ attend_near(const KvAttendParams p, const int row_tiles) {
     float qs[NT][2];
     Sums<D, NT> o;
     o.clear();
-    walk_tiles<D, BITS, NT, SPLIT>(
-        p, sm, ring, s, b, kvh, rank * share + warp, M::warps, min(tiles, (rank + 1) * share), q, qs,
+    walk_tiles<PLACED, D, BITS, NT, SPLIT>(
+        p, col, ring, s, b, kvh, rank * share + warp, M::warps, min(tiles, (rank + 1) * share), q, qs,
         masks, o, [&] {
             for (int r = warp; r < M::rows; r += M::warps) {
                 const float f = rotate_row<E, D, SPLIT>(p, s, kvh, row_base + r, r < nrows, ent,
@@ -577,7 +602,8 @@ attend_near(const KvAttendParams p, const int row_tiles) {
 #pragma unroll
     for (int half = M::warps / 2; half >= 1; half >>= 1) {
         __syncthreads();                                  // the table / the last round is done with
-        float *mine = reinterpret_cast<float *>(sm + (warp & (half - 1)) * M::part) + lane;
+        float *mine =
+            reinterpret_cast<float *>(at_address(raw, M::lut_at + (warp & (half - 1)) * M::part)) + lane;
         if (warp >= half && warp < 2 * half) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -618,7 +644,7 @@ attend_near(const KvAttendParams p, const int row_tiles) {
         }
     }
     __syncthreads();
-    float *fin = reinterpret_cast<float *>(sm);           // [rows][fin_stride]
+    float *fin = reinterpret_cast<float *>(at_address(raw, M::lut_at));   // [rows][fin_stride]
     if (warp == 0) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)

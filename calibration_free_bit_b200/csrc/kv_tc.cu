@@ -276,7 +276,7 @@ kv_write_tc(const KvWriteParams p, const uint4 *r_img, const int tbl_words, cons
 // ---- read ----
 template <int D, int BITS> struct ReadSmem {
     static constexpr int lut_at = Geo<D>::r_bytes;
-    static constexpr int a_at = lut_at + Lut<BITS, false>::bytes;              // 1024-byte aligned
+    static constexpr int a_at = lut_at + Lut<BITS, ANYWHERE>::bytes;              // 1024-byte aligned
     static constexpr int a_size = (Geo<D>::stage_bytes + 1023) / 1024 * 1024;
     static constexpr int end = a_at + Geo<D>::groups * a_size;
     // barriers and the tensor memory's address; at d = 256 in the last row's padding
@@ -307,7 +307,7 @@ kv_read_tc(const KvReadParams p, const uint4 *r_img, const int tiles) {
 
     pdl_trigger();
     unsigned char *lut = sm + R::lut_at;
-    fill_lut<BITS, false>(lut, p.lut);
+    fill_lut<BITS, ANYWHERE>(lut, p.lut);
     const uint32_t tmem0 = set_up<D>(sm, r_img, bars, slot_sm);
     pdl_wait();
 
@@ -317,7 +317,7 @@ kv_read_tc(const KvReadParams p, const uint4 *r_img, const int tiles) {
     unsigned char *a_sm = sm + R::a_at + grp * R::a_size;
     const uint32_t tmem = tmem0 + grp * D;
     const uint32_t my_tmem = tmem + ((uint32_t)(row & ~31) << 16) + part * 128;
-    const uint32_t col = lut_column<BITS>(lane);
+    const uint32_t col = lut_column<BITS, ANYWHERE>(base + R::lut_at, lane);
     const int heads = p.c.kv_heads, half_tiles = tiles / 2;
     const long long rows = (long long)p.T * heads;
     constexpr int words = 4 * BITS;                       // of this thread's 128 elements
@@ -368,8 +368,8 @@ kv_read_tc(const KvReadParams p, const uint4 *r_img, const int tiles) {
             uint4 v[4];
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
-                quad<BITS, false>(lut, codes, 2 * (k + h), col, v[h].x, v[h].y);
-                quad<BITS, false>(lut, codes, 2 * (k + h) + 1, col, v[h].z, v[h].w);
+                quad<BITS, ANYWHERE>(codes, 2 * (k + h), col, v[h].x, v[h].y);
+                quad<BITS, ANYWHERE>(codes, 2 * (k + h) + 1, col, v[h].z, v[h].w);
             }
 #pragma unroll
             for (int h = 0; h < 4; ++h)

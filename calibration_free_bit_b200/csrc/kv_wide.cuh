@@ -41,12 +41,10 @@ constexpr int kThreads = 32 * (kSoftWarps + kDecWarps + 4);
 constexpr int kWorking = 32 * (kSoftWarps + kDecWarps + 2);       // that meet at barrier 0
 constexpr int kTile = 128 * D * 2;                    // an operand: 32 KB
 
+// Shared memory by address (a CTA's own starts at 1024): the table at a multiple of its size, the
+// operands behind it at multiples of 1024.
 struct Smem {
-    static constexpr int q_at = 0;
-    static constexpr int k_at = kTile;                // two stages
-    static constexpr int v_at = 3 * kTile;            // two stages
-    static constexpr int lut_at = 5 * kTile;
-    static constexpr int vn_at = lut_at + 32768;      // [2][128] value norms
+    static constexpr int vn_at = kSharedStart;        // [2][128] value norms
     static constexpr int kexp_at = vn_at + 1024;      // [2][4] powers of two of the key norms
     static constexpr int vmax_at = kexp_at + 32;      // [2][4] largest value norms
     static constexpr int bad_at = vmax_at + 32;       // [2][4] tokens of missing pages
@@ -55,7 +53,12 @@ struct Smem {
     static constexpr int stat_at = mask_at + 1024;    // [2][3][128]: m, l, s_v scale
     static constexpr int work_at = stat_at + 3072;
     static constexpr int bars_at = work_at + 64;
-    static constexpr int bytes = bars_at + 128 + 1024;
+    static constexpr int lut_at = 32768;
+    static constexpr int q_at = 65536;
+    static constexpr int k_at = q_at + kTile;         // two stages
+    static constexpr int v_at = q_at + 3 * kTile;     // two stages
+    static constexpr int bytes = q_at + 5 * kTile - kSharedStart;
+    static_assert(bars_at + 128 <= lut_at && bytes <= 227 * 1024, "shared memory");
 };
 enum { B_K = 0, B_V = 2, B_S = 4, B_P = 6, B_PV = 8, B_Q = 10 };   // two each to B_Q
 
@@ -87,26 +90,29 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
 attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) {
     using namespace wide;
     using S = wide::Smem;
-    extern __shared__ unsigned char raw[];
-    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
-    unsigned char *sm = raw + (base - smem_u32(raw));
+    extern __shared__ __align__(1024) unsigned char raw[];
+    constexpr uint32_t base = 0;                      // offsets are addresses
+    if (!starts_there(raw)) {                         // not where the layout expects it
+        if (threadIdx.x == 0)
+            atomicOr(p.err, AT_ERR_WAIT);
+        return;
+    }
     const uint32_t bars = base + S::bars_at;
     auto bar = [&](int i) { return bars + 8u * i; };
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + S::bars_at + 112);
-    volatile int *gone = reinterpret_cast<volatile int *>(sm + S::bars_at + 116);
-    Walk *work = reinterpret_cast<Walk *>(sm + S::work_at);
-    float *vn_s = reinterpret_cast<float *>(sm + S::vn_at);
-    float *kexp_s = reinterpret_cast<float *>(sm + S::kexp_at);
-    float *vmax_s = reinterpret_cast<float *>(sm + S::vmax_at);
-    uint32_t *bad_s = reinterpret_cast<uint32_t *>(sm + S::bad_at);
-    float *qs_s = reinterpret_cast<float *>(sm + S::qs_at);
-    unsigned long long *mask_s = reinterpret_cast<unsigned long long *>(sm + S::mask_at);
-    float *stat_s = reinterpret_cast<float *>(sm + S::stat_at);
-    unsigned char *lut = sm + S::lut_at;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(at_address(raw, S::bars_at + 112));
+    volatile int *gone = reinterpret_cast<volatile int *>(at_address(raw, S::bars_at + 116));
+    Walk *work = reinterpret_cast<Walk *>(at_address(raw, S::work_at));
+    float *vn_s = reinterpret_cast<float *>(at_address(raw, S::vn_at));
+    float *kexp_s = reinterpret_cast<float *>(at_address(raw, S::kexp_at));
+    float *vmax_s = reinterpret_cast<float *>(at_address(raw, S::vmax_at));
+    uint32_t *bad_s = reinterpret_cast<uint32_t *>(at_address(raw, S::bad_at));
+    float *qs_s = reinterpret_cast<float *>(at_address(raw, S::qs_at));
+    unsigned long long *mask_s = reinterpret_cast<unsigned long long *>(at_address(raw, S::mask_at));
+    float *stat_s = reinterpret_cast<float *>(at_address(raw, S::stat_at));
 
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    fill_lut<BITS, false>(lut, p.lut);
+    fill_lut<BITS, PLACED>(at_address(raw, S::lut_at), p.lut);
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(B_K + i), kDecWarps / 2);
@@ -160,7 +166,7 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
             const int n = q.n, tile0 = q.tile0, nrows = q.nrows;
             // the rotation to K's first stage (the raw queries go to V's)
             for (int i = threadIdx.x; i < kTile / 16; i += 32 * kSoftWarps)
-                reinterpret_cast<uint4 *>(sm + S::k_at)[i] = __ldg(r_img + i);
+                reinterpret_cast<uint4 *>(at_address(raw, S::k_at))[i] = __ldg(r_img + i);
             if (threadIdx.x < kRows) {
                 const int node = (q.row_base + threadIdx.x) / p.group;
                 mask_s[threadIdx.x] =
@@ -196,7 +202,7 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
 #pragma unroll
                     for (int i = 0; i < 32; i += 8) {
                         auto f = [&](int j) { return __uint_as_float(z[i + j]) * down; };
-                        *reinterpret_cast<uint4 *>(sm + S::q_at +
+                        *reinterpret_cast<uint4 *>(at_address(raw, S::q_at) +
                                                    operand_at(threadIdx.x, 4 * k + i / 8)) =
                             make_uint4(half2_bits(f(0), f(1)), half2_bits(f(2), f(3)),
                                        half2_bits(f(4), f(5)), half2_bits(f(6), f(7)));
@@ -365,7 +371,7 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
             const float om = stat_s[(me ^ 1) * 384 + r], ol = stat_s[(me ^ 1) * 384 + 128 + r];
             const float mx = fmaxf(m, om);
             const float fac = ex2(m - mx) * vs * (1.0f / kWeightScale);
-            float *buf = reinterpret_cast<float *>(sm + S::k_at);        // [element][row]
+            float *buf = reinterpret_cast<float *>(at_address(raw, S::k_at));        // [element][row]
             if (me == 1 && mine > 0) {
 #pragma unroll 1
                 for (int k = 0; k < 4; ++k) {
@@ -425,14 +431,14 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                         static_cast<const E *>(p.q) + (q.s.row0 + node) * p.q_stride +
                         (kvh * p.group + e) * D + ch * 8);
                 }
-                *reinterpret_cast<uint4 *>(sm + S::v_at + operand_at(r, ch)) = v;
+                *reinterpret_cast<uint4 *>(at_address(raw, S::v_at) + operand_at(r, ch)) = v;
             }
             fence_async_smem();
             meet();
             meet();
             const int w = dt >> 8, part = (dt >> 7) & 1, row = dt & 127;
             const int *table = p.table + (long long)b * p.table_width;
-            const uint32_t col = lut_column<BITS>(lane);
+            const uint32_t col = lut_column<BITS, PLACED>(S::lut_at, lane);
             constexpr int words = 2 * BITS;               // 64 codes
             // One unit ahead in registers and two ahead on the way to the L2; a page's index is
             // known three ahead, so that no load waits for another.
@@ -495,7 +501,7 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                 // K's stage is free after S, V's and the norms' after P V
                 if (c > 0)
                     wait((w == 0 ? B_S : B_PV) + st, c - 1);
-                unsigned char *to = sm + (w == 0 ? S::k_at : S::v_at) + st * kTile;
+                unsigned char *to = at_address(raw, (w == 0 ? S::k_at : S::v_at) + st * kTile);
                 // four chunks of 8 elements at a time, so that their lookups are under way together
                 // (the compiler does not move a load over a store to the operand)
 #pragma unroll
@@ -503,8 +509,8 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                     uint4 v[4];
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
-                        quad<BITS, false>(lut, cur.codes, 2 * (k + h), col, v[h].x, v[h].y);
-                        quad<BITS, false>(lut, cur.codes, 2 * (k + h) + 1, col, v[h].z, v[h].w);
+                        quad<BITS, PLACED>(cur.codes, 2 * (k + h), col, v[h].x, v[h].y);
+                        quad<BITS, PLACED>(cur.codes, 2 * (k + h) + 1, col, v[h].z, v[h].w);
                     }
                     if (w == 0) {
 #pragma unroll
