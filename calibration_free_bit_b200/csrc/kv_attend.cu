@@ -11,6 +11,7 @@ namespace {
 __device__ unsigned int g_attend_err;
 
 constexpr int kJoinWarps = 4;
+constexpr int kManyRows = 4096;                       // rows of a call, for join_pieces
 // Tiles of 16 tokens, over all segments, up to which clusters take a call.
 constexpr long long kNearTiles = 16384;
 
@@ -52,17 +53,20 @@ __global__ void __launch_bounds__(32) list_work(const KvAttendParams p, const Kv
     list_units<Form>(p, ws);
 }
 
-// The sum of a row's pieces, and of their weights: WARPS warps take every WARPS-th piece and add up
-// in a fixed order.  One warp a row where there are many rows; four where there are few, which have
-// many pieces.
-template <class E, int D, class Form, int WARPS>
+// The sum of a row's pieces, and of their weights, in a fixed order.  Where there are few rows, each has
+// many pieces: four warps a row take every fourth.  Where there are many, a warp takes ROWS rows of one
+// tile in turn, for which the search for their pieces is the same.
+template <class E, int D, class Form, int WARPS, int ROWS>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 join_pieces(const KvAttendParams p, const KvAttendSpace ws) {
-    constexpr int N = D / 32, ROWS = kJoinWarps / WARPS;
+    static_assert(Form::rows % ROWS == 0, "a warp's rows are in one tile");
+    constexpr int N = D / 32, per = kJoinWarps / WARPS * ROWS;
     __shared__ float4 sums[kJoinWarps][D / 4];
     __shared__ float totals[kJoinWarps];
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
+    const int chunks = (p.max_nodes * p.group + per - 1) / per, kvh = blockIdx.x / chunks;
+    const int at = (blockIdx.x - kvh * chunks) * per + warp / WARPS * ROWS;
     uint32_t ent[N];
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -71,17 +75,18 @@ join_pieces(const KvAttendParams p, const KvAttendSpace ws) {
     Seq s;
     const long long U = ws.first[p.B], first = ws.first[b];
     const Units un = units_of<Form>(p, b, &s, false);
-    const int row = blockIdx.x * ROWS + warp / WARPS;        // node * q_heads + head
-    const int node = row / p.q_heads, head = row - node * p.q_heads;
-    const bool real = un.segments > 0 && node < s.nodes;
-    if (WARPS == 1 && !real)
+    const int rows = un.segments > 0 ? min(ROWS, s.nodes * p.group - at) : 0;
+    if (WARPS == 1 && rows <= 0)
         return;
-    float o[N], sum = 0.f;
+    float o[ROWS][N], sum[ROWS];
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        o[i] = 0.f;
-    const int kvh = head / p.group, at = node * p.group + head - kvh * p.group;
-    if (real) {
+    for (int j = 0; j < ROWS; ++j) {
+        sum[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            o[j][i] = 0.f;
+    }
+    if (rows > 0) {
         const int seg = kvh * (un.segments / p.c.kv_heads) + at / Form::rows, r = at % Form::rows;
         const long long W = workers_for(U, ws.most, ws.least);
         const long long start = first + (long long)seg * (un.tiles + Form::extra) + Form::extra;
@@ -89,56 +94,82 @@ join_pieces(const KvAttendParams p, const KvAttendSpace ws) {
         const int w0 = (int)(((start + 1) * W - 1) / U);
         const int w1 = (int)(((start + un.tiles) * W - 1) / U);
         const long long slot0 = (long long)b * ws.segments + seg;
-        float mx = kNone;
-        for (int w = w0 + lane; w <= w1; w += 32)
-            mx = fmaxf(mx, ws.stat[(slot0 + w) * 2 * ws.rows + r]);
+        float mx[ROWS];
 #pragma unroll
-        for (int k = 16; k; k >>= 1)
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-#pragma unroll 4
+        for (int j = 0; j < ROWS; ++j)
+            mx[j] = kNone;
+        if constexpr (WARPS > 1) {
+            for (int w = w0 + lane; w <= w1; w += 32)
+                mx[0] = fmaxf(mx[0], ws.stat[(slot0 + w) * 2 * ws.rows + r]);
+#pragma unroll
+            for (int k = 16; k; k >>= 1)
+                mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], k));
+        } else {
+            for (int w = w0; w <= w1; ++w)
+#pragma unroll
+                for (int j = 0; j < ROWS; ++j)
+                    if (j < rows)
+                        mx[j] = fmaxf(mx[j], ws.stat[(slot0 + w) * 2 * ws.rows + r + j]);
+        }
+#pragma unroll(WARPS > 1 ? 4 : 1)
         for (int w = w0 + warp % WARPS; w <= w1; w += WARPS) {
             const float *st = ws.stat + (slot0 + w) * 2 * ws.rows + r;
-            const float f = ex2(st[0] - mx);
-            sum += f * st[ws.rows];
             const float4 *src = reinterpret_cast<const float4 *>(
                 ws.part + ((slot0 + w) * ws.rows + r) * D + lane * N);
 #pragma unroll
-            for (int i = 0; i < N; i += 4) {
-                const float4 v = src[i / 4];
-                o[i] += f * v.x, o[i + 1] += f * v.y, o[i + 2] += f * v.z, o[i + 3] += f * v.w;
+            for (int j = 0; j < ROWS; ++j) {
+                if (j >= rows)
+                    continue;
+                const float f = ex2(st[j] - mx[j]);
+                sum[j] += f * st[ws.rows + j];
+#pragma unroll
+                for (int i = 0; i < N; i += 4) {
+                    const float4 v = src[j * (D / 4) + i / 4];
+                    o[j][i] += f * v.x, o[j][i + 1] += f * v.y;
+                    o[j][i + 2] += f * v.z, o[j][i + 3] += f * v.w;
+                }
             }
         }
     }
     if constexpr (WARPS > 1) {
 #pragma unroll
         for (int i = 0; i < N; i += 4)
-            sums[warp][lane * (N / 4) + i / 4] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            sums[warp][lane * (N / 4) + i / 4] =
+                make_float4(o[0][i], o[0][i + 1], o[0][i + 2], o[0][i + 3]);
         if (lane == 0)
-            totals[warp] = sum;
+            totals[warp] = sum[0];
         __syncthreads();
-        if (warp % WARPS > 0 || !real)
+        if (warp % WARPS > 0 || rows <= 0)
             return;
 #pragma unroll
         for (int w = 1; w < WARPS; ++w) {
-            sum += totals[warp + w];
+            sum[0] += totals[warp + w];
 #pragma unroll
             for (int i = 0; i < N; i += 4) {
                 const float4 v = sums[warp + w][lane * (N / 4) + i / 4];
-                o[i] += v.x, o[i + 1] += v.y, o[i + 2] += v.z, o[i + 3] += v.w;
+                o[0][i] += v.x, o[0][i + 1] += v.y, o[0][i + 2] += v.z, o[0][i + 3] += v.w;
             }
         }
     }
-    finish_row<E, D>(p, s, kvh, at, ent, reinterpret_cast<float *>(sums[warp]), o, sum);
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j)
+        if (j < rows)
+            finish_row<E, D>(p, s, kvh, at + j, ent, reinterpret_cast<float *>(sums[warp]), o[j],
+                             sum[j]);
 }
 
+template <class E, int D, class Form, int WARPS, int ROWS>
+cudaError_t join_with(const KvAttendParams &p, const KvAttendSpace &ws, cudaStream_t st) {
+    constexpr int per = kJoinWarps / WARPS * ROWS;
+    const int chunks = (p.max_nodes * p.group + per - 1) / per;
+    return launch_pdl(join_pieces<E, D, Form, WARPS, ROWS>, dim3(p.c.kv_heads * chunks, p.B),
+                      dim3(32 * kJoinWarps), 0, st, p, ws);
+}
 template <class E, int D, class Form>
 cudaError_t join_as(const KvAttendParams &p, const KvAttendSpace &ws, cudaStream_t st) {
-    const int rows = p.max_nodes * p.q_heads;
-    const dim3 block(32 * kJoinWarps);
-    if ((long long)rows * p.B >= 2048)
-        return launch_pdl(join_pieces<E, D, Form, 1>,
-                          dim3((rows + kJoinWarps - 1) / kJoinWarps, p.B), block, 0, st, p, ws);
-    return launch_pdl(join_pieces<E, D, Form, kJoinWarps>, dim3(rows, p.B), block, 0, st, p, ws);
+    if ((long long)p.max_nodes * p.q_heads * p.B >= kManyRows)
+        return join_with<E, D, Form, 1, 4>(p, ws, st);
+    return join_with<E, D, Form, kJoinWarps, 1>(p, ws, st);
 }
 
 template <int D, class Form>
