@@ -515,20 +515,21 @@ template <int D, int BITS, int NT, bool SPLIT> struct Near {
     static constexpr int warps = 8, rows = 8 * NT;
     using Q = Queries<D, NT, SPLIT>;
     using R = Ring<D, BITS, 2>;
-    static constexpr int part = (D / 16) * NT * 4 * 128 + NT * 4 * 128;      // a warp's sums
-    static constexpr int fin_stride = D + 4;                                 // floats
-    static constexpr int most(int a, int b) { return a > b ? a : b; }
+    static constexpr int stride = D + 4;                                     // floats
     static constexpr int q_at = kSharedStart;
     static constexpr int x_at = q_at + Q::words * 8;                         // [warps][D] floats
     static constexpr int mask_at = x_at + warps * D * 4;
     static constexpr int stat_at = mask_at + rows * 8;                       // factor, m, l: [rows]
+    static constexpr int warp_at = stat_at + rows * 12;                      // m, l: [warps][rows]
+    static constexpr int fin_at = warp_at + warps * rows * 8;                // [rows][stride] floats
     static constexpr int lut_at = 32768;
-    // the table, then the warps' sums, then the block's
-    static constexpr int big = most(most(Lut<BITS, PLACED>::bytes, warps / 2 * part),
-                                    rows * fin_stride * 4);
-    static constexpr int ring_at = (lut_at + big + 127) / 128 * 128;
-    static constexpr int bytes = ring_at + warps * R::bytes - kSharedStart;
-    static_assert(stat_at + rows * 12 <= lut_at && bytes <= 227 * 1024, "shared memory");
+    static constexpr int ring_at = lut_at + Lut<BITS, PLACED>::bytes;
+    // and over both, once the tokens are done with, the warps' sums: [warps][rows][stride] floats
+    static constexpr int most(int a, int b) { return a > b ? a : b; }
+    static constexpr int bytes =
+        lut_at + most(ring_at - lut_at + warps * R::bytes, warps * rows * stride * 4) - kSharedStart;
+    static_assert(fin_at + rows * stride * 4 <= lut_at && fin_at % 16 == 0 && bytes <= 227 * 1024,
+                  "shared memory");
 };
 
 template <class E, int D, int BITS, int NT, bool SPLIT>
@@ -599,68 +600,55 @@ attend_near(const KvAttendParams p, const int row_tiles) {
         });
     o.finish();
     // ---- the block's warps meet ----
+    float *parts = reinterpret_cast<float *>(at_address(raw, M::lut_at));
+    float *warp_m = reinterpret_cast<float *>(at_address(raw, M::warp_at));
+    float *warp_l = warp_m + M::warps * M::rows;
+    float *fin = reinterpret_cast<float *>(at_address(raw, M::fin_at));
+    __syncthreads();                                      // the table and the rings are done with
 #pragma unroll
-    for (int half = M::warps / 2; half >= 1; half >>= 1) {
-        __syncthreads();                                  // the table / the last round is done with
-        float *mine =
-            reinterpret_cast<float *>(at_address(raw, M::lut_at + (warp & (half - 1)) * M::part)) + lane;
-        if (warp >= half && warp < 2 * half) {
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
+        for (int i = 0; i < 2; ++i) {
+            const int r = warp * M::rows + 8 * n + 2 * c + i;
+            float4 *to = reinterpret_cast<float4 *>(parts + r * M::stride + g * (D / 8));
 #pragma unroll
-                for (int j = 0; j < KS; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mine[((n * KS + j) * 4 + i) * 32] = o.acc[n][j][i];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    mine[(NT * KS * 4 + n * 4 + i) * 32] = o.m[n][i];
-                    mine[(NT * KS * 4 + n * 4 + 2 + i) * 32] = o.l[n][i];
-                }
+            for (int j = 0; j < KS; j += 2)
+                to[j / 2] = make_float4(o.acc[n][j][i], o.acc[n][j][2 + i], o.acc[n][j + 1][i],
+                                        o.acc[n][j + 1][2 + i]);
+            if (g == 0) {
+                warp_m[r] = o.m[n][i];
+                warp_l[r] = o.l[n][i];
             }
         }
-        __syncthreads();
-        if (warp < half) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float f[2], h[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float om = mine[(NT * KS * 4 + n * 4 + i) * 32];
-                    const float ol = mine[(NT * KS * 4 + n * 4 + 2 + i) * 32];
-                    const float mn = fmaxf(o.m[n][i], om);
-                    f[i] = ex2(o.m[n][i] - mn);
-                    h[i] = ex2(om - mn);
-                    o.m[n][i] = mn;
-                    o.l[n][i] = o.l[n][i] * f[i] + ol * h[i];
-                }
-#pragma unroll
-                for (int j = 0; j < KS; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        o.acc[n][j][i] = o.acc[n][j][i] * f[i & 1] +
-                                         mine[((n * KS + j) * 4 + i) * 32] * h[i & 1];
-            }
-        }
-    }
     __syncthreads();
-    float *fin = reinterpret_cast<float *>(at_address(raw, M::lut_at));   // [rows][fin_stride]
-    if (warp == 0) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+    for (int r = warp; r < M::rows; r += M::warps) {
+        float mx = kNone, sum = 0.f, x[N];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = 8 * n + 2 * c + i;
+        for (int w = 0; w < M::warps; ++w)
+            mx = fmaxf(mx, warp_m[w * M::rows + r]);
 #pragma unroll
-                for (int j = 0; j < KS; ++j) {
-                    fin[r * M::fin_stride + g * (D / 8) + 2 * j] = o.acc[n][j][i];
-                    fin[r * M::fin_stride + g * (D / 8) + 2 * j + 1] = o.acc[n][j][2 + i];
-                }
-                if (g == 0) {
-                    row_m[r] = o.m[n][i];
-                    row_l[r] = o.l[n][i];
-                }
+        for (int i = 0; i < N; ++i)
+            x[i] = 0.f;
+#pragma unroll
+        for (int w = 0; w < M::warps; ++w) {
+            const float f = ex2(warp_m[w * M::rows + r] - mx);
+            sum += f * warp_l[w * M::rows + r];
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(parts + (w * M::rows + r) * M::stride +
+                                                                   lane * N + i);
+                x[i] += f * v.x, x[i + 1] += f * v.y, x[i + 2] += f * v.z, x[i + 3] += f * v.w;
             }
+        }
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            *reinterpret_cast<float4 *>(fin + r * M::stride + lane * N + i) =
+                make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        if (lane == 0) {
+            row_m[r] = mx;
+            row_l[r] = sum;
+        }
     }
     // ---- the cluster's blocks meet: rank k finishes rows k, k + splits, ... ----
     cg::cluster_group cl = cg::this_cluster();
@@ -668,12 +656,13 @@ attend_near(const KvAttendParams p, const int row_tiles) {
     for (int r = rank + splits * warp; r < nrows; r += splits * M::warps) {
         // a lane each of the ranks' references and sums, then their rows in turn
         const float mk = lane < splits ? *cl.map_shared_rank(row_m + r, lane) : kNone;
+        const float lk = lane < splits ? *cl.map_shared_rank(row_l + r, lane) : 0.f;
         float mx = mk;
 #pragma unroll
         for (int k = 16; k; k >>= 1)
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
         const float f = ex2(mk - mx);
-        float sum = lane < splits ? f * *cl.map_shared_rank(row_l + r, lane) : 0.f;
+        float sum = f * lk;
 #pragma unroll
         for (int k = 16; k; k >>= 1)
             sum += __shfl_xor_sync(0xffffffffu, sum, k);
@@ -681,11 +670,11 @@ attend_near(const KvAttendParams p, const int row_tiles) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
             x[i] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
         for (int k = 0; k < splits; ++k) {
             const float fk = __shfl_sync(0xffffffffu, f, k);
             const float4 *src = reinterpret_cast<const float4 *>(
-                cl.map_shared_rank(fin + r * M::fin_stride + lane * N, k));
+                cl.map_shared_rank(fin + r * M::stride + lane * N, k));
 #pragma unroll
             for (int i = 0; i < N; i += 4) {
                 const float4 v = src[i / 4];
