@@ -11,9 +11,19 @@ namespace {
 __device__ unsigned int g_attend_err;
 
 constexpr int kJoinWarps = 4;
-constexpr int kManyRows = 4096;                       // rows of a call, for join_pieces
-// Tiles of 16 tokens, over all segments, up to which clusters take a call.
-constexpr long long kNearTiles = 16384;
+// Rows of a call from which a joining warp takes four rows.  It and four warps a row, us: 64 sequences of
+// 2000 tokens, 2048 rows 58 and 54, 128 sequences 91 and 92, 512 of 500 tokens 113 and 131; 16 sequences
+// with 31 nodes, 15872 rows 63 and 84.
+constexpr int kManyRows = 4096;
+// Tiles of 16 tokens, over all segments, up to which clusters take a call: tiles of 8 rows of 128 (two
+// CTAs an SM), others.  Clusters and workers, us, bf16: 8 key heads, a sequence of 4096 tokens 11 and
+// 19, 32768 30 and 46, 65536 51 and 55, 131072 93 and 74, 16 of 4000 tokens 29 and 33; with 16 rows
+// 16000 tokens 27 and 32, 32000 44 and 37, 4 sequences of 4000 27 and 25.
+constexpr long long kNearTiles = 32768, kNearOther = 8192;
+// Rows of a key head from which a call is the tensor memory's (kv_wide.cuh).  It and the tiles of 16
+// rows, us, 8 key heads, 4 bits: 32 rows, 32 sequences of 4000 tokens 147 and 120, one of 4000 22 and
+// 19; 48 rows 149 and 169, and 23 and 20; 64 rows, 8 sequences 56 and 72; 128 rows 61 and 120.
+constexpr int kWideRows = 33;
 
 // Before the other two kernels of a call with few rows: its work list and the rotated queries, one
 // warp a row of a tile (rows that no query fills are zeros).
@@ -245,16 +255,19 @@ struct Plan {
 Plan plan_for(const KvAttendParams &p, int dtype, int num_sms) {
     Plan a = {};
     const int rows = p.max_nodes * p.group;
-    a.wide = p.c.d == 128 && rows > 16;
+    a.wide = p.c.d == 128 && rows >= kWideRows;
     a.tile = a.wide ? 128 : rows <= 8 || p.c.d == 256 ? 8 : 16;
     a.ws.rows = rows < a.tile ? rows : a.tile;
     a.ws.segments = p.c.kv_heads * ((rows + a.tile - 1) / a.tile);
     const long long all = (long long)p.B * a.ws.segments;
     const long long tokens = (long long)p.table_width << p.c.page_log2;
-    if (!a.wide && all <= num_sms && all * tokens <= 16ll * kNearTiles) {
-        // two CTAs an SM at most, and a tile for every warp
+    const bool two = a.tile == 8 && p.c.d == 128;        // CTAs an SM, of attend_near
+    if (!a.wide && all <= num_sms && all * tokens <= 16 * (two ? kNearTiles : kNearOther)) {
+        // all CTAs at once, and a tile for every warp (one CTA an SM: clusters do not fill every part
+        // of the GPU, and 128 CTAs in clusters of 8 took 21 us, 64 in clusters of 4 12)
+        const long long room = two ? 2 * num_sms : num_sms * 3 / 4;
         a.splits = 1;
-        while (a.splits < 16 && all * a.splits <= num_sms && tokens >= 256ll * a.splits)
+        while (a.splits < 16 && all * a.splits * 2 <= room && tokens >= 256ll * a.splits)
             a.splits *= 2;
         return a;
     }

@@ -185,8 +185,10 @@ cudaError_t error_word(unsigned **out) {
     return e;
 }
 
-// Rows (keys and values) from which the tensor cores' form is taken.
-constexpr long long kTensorRows = 512;
+// Rows (keys and values) from which the tensor cores' form is taken.  It and a warp a row, write (read),
+// us: d = 128, 4 bits, 4096 rows 6.5 and 5.9 (5.2 and 4.0), 16384 rows 7.3 and 11.5 (6.5 and 8.5); d =
+// 256, 2 bits, 4096 rows 7.2 and 6.9 (6.6 and 4.9), 16384 rows 8.7 and 15.8 (8.4 and 11.5).
+constexpr long long kTensorRows = 8192;
 
 }  // namespace
 

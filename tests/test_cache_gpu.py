@@ -802,3 +802,76 @@ def test_timing_names_the_new_kernels(oq):
     finally:
         oq.oq_timing_enable(False)
     assert names == ["rope", "kv_write", "kv_read", "kv_attend"]
+
+
+# ---------------------------------------------------------------------------------------
+# the forms of larger calls: rows on the tensor cores, row tiles of 16 side by side
+# ---------------------------------------------------------------------------------------
+@pytest.mark.parametrize("bits", [2, 3, 4, 6, 8])
+@pytest.mark.parametrize("T,H,d,h,dtype", [(1400, 3, 128, 16, F16), (4097, 1, 256, 256, F16),
+                                           (1371, 3, 256, 32, BF16)])
+def test_write_and_read_many_rows(oq, T, H, d, h, bits, dtype):
+    test_write_and_read_match_fp64(oq, T, H, d, h, bits, 32, dtype)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_padding_and_strides_of_many_rows(oq, d):
+    test_padding_bad_slots_and_special_rows(oq, BF16, 2100, d)
+    test_strided_rows_and_the_fused_projection(oq, 1400, d)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_small_large_and_misaligned_rows_of_a_large_call(oq, dtype):
+    """Rows of all sizes, in code arrays that are 16- but not 32-byte aligned."""
+    T, d, bits = 4200, 128, 4
+    r, c = oq.oq_build_rpbh(d, 64, 0), oq.oq_lloyd_max(d, bits)
+    a = oq.KVCache.empty(263, 1, 16, d, bits)
+    n = a.k_codes.numel()
+    buf = [torch.zeros(n + 16, dtype=torch.uint8, device="cuda")[16:].view(263, 1, 16, -1)
+           for _ in range(2)]
+    b = oq.KVCache(*buf, torch.zeros_like(a.k_norms), torch.zeros_like(a.k_norms), bits=bits)
+    x = make_rows(T, 1, d, F32, 5)
+    x[::3] *= 2.0 ** -15 if dtype == F16 else 2.0 ** -30
+    x[1::3] *= 100.0 if dtype == F16 else 2.0 ** 50
+    x = x.to(dtype)
+    slots = torch.arange(T).cuda()
+    for cache in (a, b):
+        oq.oq_kv_write(r, c, cache, x.cuda(), x.cuda(), slots)
+    oq.oq_check()
+    assert torch.equal(a.k_codes, b.k_codes) and torch.equal(a.v_codes, b.v_codes)
+    for u, v in zip(oq.oq_kv_read(r, c, a, slots), oq.oq_kv_read(r, c, b, slots)):
+        assert torch.equal(u.view(torch.int16), v.view(torch.int16))      # NaN of rows with infinities
+    fits = torch.isfinite(x).all(-1).view(-1).numpy()                     # fp16 has no 100 times some
+    assert fits.mean() > 0.9
+    codes = CO.unpack(a.k_codes.cpu().numpy().reshape(-1, d // 2)[:T], bits)
+    check_codes(codes[fits], f64(x).reshape(T, d)[fits], CO.rotation(d, 64), bits,
+                a.k_norms.cpu().double().numpy().reshape(-1)[:T][fits])
+
+
+@pytest.mark.parametrize("bits", [2, 3, 4, 6, 8])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("group,nodes", [(4, [7, 2, 8]), (1, [33, 9]), (3, [1, 11])])
+@pytest.mark.parametrize("roomy", [False, True])
+def test_row_tiles_side_by_side(oq, bits, dtype, group, nodes, roomy):
+    """17 to 33 rows a key head: two tiles of 16, the second partly filled, or one of 128."""
+    s = Serving(oq, [70, 0, 301][:len(nodes)], nodes, 2 * group, 2, 128, 64, bits, 16, dtype,
+                seed=60 + bits, columns=ROOMY // 16 if roomy else 0).trees(empty=0.1)
+    s.hide(float("nan"))
+    out = oq.oq_kv_attend(**s.gpu())
+    oq.oq_check()
+    close(out, s.want(), dtype)
+
+
+@pytest.mark.parametrize("bits,dtype", [(2, F16), (3, BF16), (4, F16), (6, F16), (8, BF16)])
+def test_many_rows_of_many_sequences(oq, bits, dtype):
+    """Enough rows that a joining warp takes several: ends of tiles, idle sequences between."""
+    nodes = [64, 0, 37, 1, 64, 5, 64, 63]
+    s = Serving(oq, [300, 5, 0, 77, 129, 1000, 64, 3], nodes, 18, 2, 128, 128, bits, 16, dtype,
+                seed=70 + bits, extra_rows=3).trees(empty=0.05)
+    s.hide(float("inf"))
+    a = s.gpu()
+    out = torch.full_like(a["q"], 42.0)
+    oq.oq_kv_attend(**a, out=out)
+    oq.oq_check()
+    assert torch.all(out[s.rows:] == 42.0)
+    close(out[:s.rows], s.want(), dtype)
