@@ -21,7 +21,7 @@ import numpy as np
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
-LIB_PATH = os.environ.get('OQ_SO', os.path.join(_PKG, "liboq.so"))
+LIB_PATH = os.path.join(_PKG, "liboq.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "oq.h")
 
 OQ_OK, OQ_EINVAL, OQ_EUNSUPPORTED, OQ_ECUDA, OQ_EDEVICE, OQ_ENOMEM = 0, -1, -2, -3, -4, -5
