@@ -81,20 +81,15 @@ template <bool BF16> __device__ __forceinline__ uint32_t idesc_q() {
     return idesc_f16(128, 128) | (BF16 ? (1u << 7) | (1u << 10) : 0u);
 }
 
-// 16 columns of tensor memory, in two steps (the registers are the load's until it is waited for).
-__device__ __forceinline__ void tmem_ld16_start(uint32_t at, uint32_t (&r)[16]) {
+// 16 columns of tensor memory (the wait is in the same statement: nothing may touch the registers, not
+// even a copy or a spill, while the load is on its way).
+__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-                 "%11, %12, %13, %14, %15}, [%16];"
+                 "%11, %12, %13, %14, %15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
                    "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
                    "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                 : "r"(at));
-}
-__device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
-                   "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+                 : "r"(at) : "memory");
 }
 __device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
@@ -292,18 +287,13 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                     // value norm that it sees
                     float top = -CUDART_INF_F, vtop, sum;
                     if (!edge) {
-                        // 16 tokens at a time, the next on their way meanwhile.  A group of 32 has
-                        // its norms over one power of two; that power, over the row's, enters with
-                        // the exponent (below 2^-60 fp16 has nothing of it).
-                        uint32_t z[2][16];
+                        // A group of 32 tokens has its norms over one power of two; that power, over
+                        // the row's, enters with the exponent (below 2^-60 fp16 has nothing of it).
                         sum = 0.f;
-                        tmem_ld16_start(tS, z[0]);
-                        tmem_ld16_wait(z[0]);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const uint32_t(&y)[16] = z[k & 1];
-                            if (k < 3)
-                                tmem_ld16_start(tS + 16 * (k + 1), z[(k + 1) & 1]);
+                            uint32_t y[16];
+                            tmem_ld16(tS + 16 * k, y);
                             const float f = qs * ke[k >> 1];
                             const float lf = fmaxf(vlog_s[4 * st + 2 * half + (k >> 1)] + vlog, -60.f);
                             const float2 ff = make_float2(f, f), mm = make_float2(lf - m, lf - m);
@@ -338,8 +328,6 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                             }
                             sum = fmaf((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y), ex2(-lf), sum);
                             tmem_st8(tP + 8 * k, w);
-                            if (k < 3)
-                                tmem_ld16_wait(z[(k + 1) & 1]);
                         }
                         vtop = fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w));
                     } else {
@@ -494,21 +482,25 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
             int page1 = page_of(1), page2 = page_of(2);
             load(cur, 0, page_of(0));
             fetch(1, page1);
-            // the raw queries, to V's first stage (the piece before is done with it)
-            if (done > 0)
-                wait(B_PV + ((done - 1) & 1u), (done - 1) >> 1);
-            const int ch = dt & 15;
+            // The raw queries go to V's first stage once the piece before is done with it: by V's
+            // decoders, which have followed P V unit by unit (a wait is for a barrier's next phase).
+            if (w == 1) {
+                const int t = dt - 128 * kParts, ch = t & 15;
+                if (done > 0)
+                    wait(B_PV + ((done - 1) & 1u), (done - 1) >> 1);
 #pragma unroll
-            for (int i = 0; i < 8 / kParts; ++i) {
-                const int r = i * 16 * kParts + (dt >> 4);
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (r < q.nrows) {
-                    const int node = (q.row_base + r) / p.group, e = q.row_base + r - node * p.group;
-                    v = *reinterpret_cast<const uint4 *>(
-                        static_cast<const E *>(p.q) + (q.s.row0 + node) * p.q_stride +
-                        (kvh * p.group + e) * D + ch * 8);
+                for (int i = 0; i < 16 / kParts; ++i) {
+                    const int r = i * 8 * kParts + (t >> 4);
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (r < q.nrows) {
+                        const int node = (q.row_base + r) / p.group;
+                        const int e = q.row_base + r - node * p.group;
+                        v = *reinterpret_cast<const uint4 *>(
+                            static_cast<const E *>(p.q) + (q.s.row0 + node) * p.q_stride +
+                            (kvh * p.group + e) * D + ch * 8);
+                    }
+                    *reinterpret_cast<uint4 *>(at_address(raw, S::v_at) + operand_at(r, ch)) = v;
                 }
-                *reinterpret_cast<uint4 *>(at_address(raw, S::v_at) + operand_at(r, ch)) = v;
             }
             fence_async_smem();
             meet();

@@ -875,3 +875,19 @@ def test_many_rows_of_many_sequences(oq, bits, dtype):
     oq.oq_check()
     assert torch.all(out[s.rows:] == 42.0)
     close(out[:s.rows], s.want(), dtype)
+
+
+@pytest.mark.parametrize("bits", [2, 3, 4, 6, 8])
+@pytest.mark.parametrize("length,nodes,dtype", [(500, 61, BF16), (130, 40, F16)])
+def test_several_pieces_of_many_rows_a_worker(oq, bits, length, nodes, dtype):
+    """Short segments of many rows: a worker goes from one to the next several times.  The same
+    bits every time, and (two key heads of them) the formula's values."""
+    s = Serving(oq, [length + 7 * b for b in range(16)], [nodes] * 16, 32, 8, 128, 128, bits, 64,
+                dtype, seed=80 + bits).trees()
+    s.hide(float("nan"))
+    a = s.gpu()
+    out = oq.oq_kv_attend(**a)
+    for _ in range(4):
+        assert torch.equal(oq.oq_kv_attend(**a), out)
+    oq.oq_check()
+    close(out, s.want(sample=[0, 7]), dtype)
