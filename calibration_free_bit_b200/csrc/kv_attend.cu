@@ -213,9 +213,8 @@ cudaError_t launch_narrow(const KvAttendParams &p, const KvAttendSpace &ws, int 
     OQ_BY_BITS(p.c.bits, OQ_CALL)
 #undef OQ_CALL
 }
-cudaError_t launch_wide(const KvAttendParams &p, const KvAttendSpace &ws, int dtype,
-                        cudaStream_t st) {
-#define OQ_CALL(B) launch_kv_wide_b##B(p, ws, dtype, st)
+cudaError_t launch_wide(const KvAttendParams &p, const KvAttendSpace &ws, cudaStream_t st) {
+#define OQ_CALL(B) launch_kv_wide_b##B(p, ws, st)
     OQ_BY_BITS(p.c.bits, OQ_CALL)
 #undef OQ_CALL
 }
@@ -234,16 +233,18 @@ cudaError_t run_narrow(const KvAttendParams &p, const KvAttendSpace &ws, int dty
     return e == cudaSuccess ? join<D, NarrowForm<NT>>(p, ws, dtype, st) : e;
 }
 
-cudaError_t run_wide(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, cudaStream_t st) {
+cudaError_t run_wide(const KvAttendParams &p, const KvAttendSpace &ws, cudaStream_t st) {
     cudaError_t e = launch_pdl(list_work<WideForm>, dim3(1), dim3(32), 0, st, p, ws);
     if (e == cudaSuccess)
-        e = launch_wide(p, ws, dtype, st);
-    return e == cudaSuccess ? join<128, WideForm>(p, ws, dtype, st) : e;
+        e = launch_wide(p, ws, st);
+    return e == cudaSuccess ? join_as<__nv_bfloat16, 128, WideForm>(p, ws, st) : e;
 }
 
-// How a call runs: tiles of 128 rows (kv_wide.cuh) for more than 16 rows a key head of 128, else
-// of 8 or, of heads of 128, 16 (kv_attend.cuh), the latter by clusters where all tokens that the page tables can hold
-// are little work; and where its workspace's arrays lie.
+// How a call runs: tiles of 128 rows (kv_wide.cuh) for many rows a key head of 128, else of 8 or, of
+// heads of 128, 16 (kv_attend.cuh), the latter by clusters where all tokens that the page tables can
+// hold are little work; and where its workspace's arrays lie.  fp16 stays with the small tiles: its
+// outputs are eight times as fine as bf16's, and a query and a key of one fp16 number an element, as
+// the large tiles have them, left an error of 1.2e-3 where the output's own rounding is 2.1e-4.
 struct Plan {
     bool wide;
     int tile;                     // rows of a tile
@@ -255,7 +256,7 @@ struct Plan {
 Plan plan_for(const KvAttendParams &p, int dtype, int num_sms) {
     Plan a = {};
     const int rows = p.max_nodes * p.group;
-    a.wide = p.c.d == 128 && rows >= kWideRows;
+    a.wide = p.c.d == 128 && dtype == OQ_BF16 && rows >= kWideRows;
     a.tile = a.wide ? 128 : rows <= 8 || p.c.d == 256 ? 8 : 16;
     a.ws.rows = rows < a.tile ? rows : a.tile;
     a.ws.segments = p.c.kv_heads * ((rows + a.tile - 1) / a.tile);
@@ -313,7 +314,7 @@ cudaError_t launch_kv_attend(const KvAttendParams &params, void *space, int dtyp
     a.ws.queries = reinterpret_cast<uint2 *>(w + a.queries_at);
     a.ws.factors = reinterpret_cast<float *>(w + a.factors_at);
     if (a.wide)
-        return attend::run_wide(p, a.ws, dtype, st);
+        return attend::run_wide(p, a.ws, st);
     if (a.splits > 0)
         return attend::launch_narrow(p, a.ws, dtype, a.splits, st);
     if (p.c.d == 128)

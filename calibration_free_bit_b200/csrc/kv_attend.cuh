@@ -28,7 +28,10 @@
 // (over a power of two of its own), the centroids (times alpha, see build_kv_lut) and the weights
 // p s_v, which are taken relative to a power of two above the row's largest s_v and times 2^6 to
 // 2^14: what a token adds is resolved down to 2^-31 of the largest.  With SPLIT (fp16 outputs) a
-// query enters as a sum of two fp16 numbers: its rounding is the one that scores multiply.
+// query enters as a sum of two fp16 numbers (its rounding is the one that scores multiply), and so do
+// the centroids of 6 and 8 bits, which are too many for alpha to help: errors of 2.6e-4 to 3.0e-4 of
+// an output's length, of which its own rounding is 2.1e-4 (without the second numbers 4.5e-4 and
+// 5.9e-4 at 6 and 8 bits).
 #pragma once
 
 #include <cooperative_groups.h>
@@ -233,6 +236,7 @@ __device__ __forceinline__ void walk_tiles(const KvAttendParams &p, uint32_t col
     using S = Shape<D, BITS>;
     using R = Ring<D, BITS, SLOTS>;
     constexpr int KS = D / 16;
+    constexpr bool RESTS = SPLIT && BITS >= 6;        // of the centroids
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int *table = p.table + (long long)b * p.table_width;
     const int in_page = (1 << p.c.page_log2) - 1;
@@ -276,14 +280,16 @@ __device__ __forceinline__ void walk_tiles(const KvAttendParams &p, uint32_t col
                 st[n][i] = s2[n][i] = 0.f;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-            uint32_t a[4];
-            quad<BITS, FORM>(kr[0], ks, col, a[0], a[2]);
-            quad<BITS, FORM>(kr[1], ks, col, a[1], a[3]);
+            uint32_t a[4], rest[4];
+            quad<BITS, FORM>(kr[0], ks, col, a[0], a[2], rest[0], rest[2]);
+            quad<BITS, FORM>(kr[1], ks, col, a[1], a[3], rest[1], rest[3]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 uint2 w = q(0, n, ks);
                 mma16816((ks & 1) ? s2[n] : st[n], a, w.x, w.y);
                 if constexpr (SPLIT) {
+                    if constexpr (RESTS)
+                        mma16816((ks & 1) ? s2[n] : st[n], rest, w.x, w.y);
                     w = q(1, n, ks);
                     mma16816((ks & 1) ? s2[n] : st[n], a, w.x, w.y);
                 }
@@ -389,15 +395,21 @@ __device__ __forceinline__ void walk_tiles(const KvAttendParams &p, uint32_t col
         mixed<BITS>(vw[2], vw[3]);
 #pragma unroll
         for (int j = 0; j < KS; j += 2) {
-            uint32_t x[4], y[4];
-            quad_of_two<BITS, FORM>(vw[0], vw[1], j / 2, col, x);
-            quad_of_two<BITS, FORM>(vw[2], vw[3], j / 2, col, y);
+            uint32_t x[4], y[4], rx[4], ry[4];
+            quad_of_two<BITS, FORM>(vw[0], vw[1], j / 2, col, x, rx);
+            quad_of_two<BITS, FORM>(vw[2], vw[3], j / 2, col, y, ry);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint32_t a[4] = {x[2 * h], x[2 * h + 1], y[2 * h], y[2 * h + 1]};
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     mma16816(o.acc[n][j + h], a, pb[n][0], pb[n][1]);
+                if constexpr (RESTS) {
+                    const uint32_t ra[4] = {rx[2 * h], rx[2 * h + 1], ry[2 * h], ry[2 * h + 1]};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        mma16816(o.acc[n][j + h], ra, pb[n][0], pb[n][1]);
+                }
             }
         }
     }

@@ -77,13 +77,18 @@ __global__ void __launch_bounds__(32 * kWarps) kv_write_rows(const KvWriteParams
         for (int s = 16; s; s >>= 1)
             sum += __shfl_xor_sync(0xffffffffu, sum, s);
         const float norm = sqrtf(sum / (float)p.h);
-        const float k = p.K / (norm + p.eps);
+        const float k = p.K / (norm + p.eps), unit = p.unit / (norm + p.eps);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const float a = fma_sat(z[i], k, 0.5f);
             const uint32_t q = __float_as_uint(__fadd_rd(a, 1.0f));
             const uint32_t word = p.tbl[((q - 0x3F800000u) >> p.F) * p.tbl_copies];
-            cs[warp][lane * N + i] = (uint8_t)((word + q * (uint32_t)p.G) >> 24);
+            const uint32_t at = word + q * (uint32_t)p.G;
+            uint32_t code = at >> 24;
+            if (distance_to_bound(at, p.G) < bound_width(p.G))
+                code = code_beside(code, z[i] * unit, __ldg(p.bounds + (code ? code - 1 : 0)),
+                                   __ldg(p.bounds + code), p.c.bits);
+            cs[warp][lane * N + i] = (uint8_t)code;
         }
         __syncwarp();
         const long long at = cache_row(p.c, slot, o.head);

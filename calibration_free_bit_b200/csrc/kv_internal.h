@@ -60,6 +60,8 @@ struct KvWriteParams {
     const uint16_t *ent;          // [d] perm | sign bit << 15
     const uint32_t *tbl;          // quantizer grid words (each `tbl_copies` times)
     int tbl_copies, tbl_words;
+    const float *bounds;          // the codes' 2^bits - 1 boundaries, of a row over its norm / unit
+    float unit;
     const void *r_img;            // R' as the tensor cores' operand in x's type (16-bit x)
     int wide;                     // code rows keep 32-byte stores aligned
     unsigned *err;                // device error word (set by launch_kv_write)
@@ -108,7 +110,7 @@ struct KvAttendParams {
     int h;
     float qk_scale;               // scale * log2(e) / (sqrt(d h) alpha)
     float o_scale;                // 1 / (sqrt(d h) alpha)
-    const void *r_img;            // R' as the tensor cores' operand in q's type (kv_wide.cuh)
+    const void *r_img;            // R' as the tensor cores' operand in bf16 (kv_wide.cuh)
     unsigned *err;                // device error word (set by launch_kv_attend)
 };
 // Workspace and work list of the forms that share out all tokens evenly (kv_attend_ops.cuh).
@@ -123,14 +125,12 @@ struct KvAttendSpace {
     int segments;                 // segments of a sequence with the most rows
     int most, least;              // workers, and units that one has at least
 };
-// Many rows a key head, heads of 128 (kv_wide.cuh).
-cudaError_t launch_kv_wide(const KvAttendParams &p, const KvAttendSpace &ws, int dtype,
-                           cudaStream_t st);
-cudaError_t launch_kv_wide_b2(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, cudaStream_t st);
-cudaError_t launch_kv_wide_b3(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, cudaStream_t st);
-cudaError_t launch_kv_wide_b4(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, cudaStream_t st);
-cudaError_t launch_kv_wide_b6(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, cudaStream_t st);
-cudaError_t launch_kv_wide_b8(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, cudaStream_t st);
+// Many rows a key head, heads of 128, bf16 (kv_wide.cuh).
+cudaError_t launch_kv_wide_b2(const KvAttendParams &p, const KvAttendSpace &ws, cudaStream_t st);
+cudaError_t launch_kv_wide_b3(const KvAttendParams &p, const KvAttendSpace &ws, cudaStream_t st);
+cudaError_t launch_kv_wide_b4(const KvAttendParams &p, const KvAttendSpace &ws, cudaStream_t st);
+cudaError_t launch_kv_wide_b6(const KvAttendParams &p, const KvAttendSpace &ws, cudaStream_t st);
+cudaError_t launch_kv_wide_b8(const KvAttendParams &p, const KvAttendSpace &ws, cudaStream_t st);
 // Few rows a key head, or heads of 256 (kv_attend.cuh): in one launch, a cluster of `splits` CTAs a
 // segment, or with splits = 0 by workers (their number on `sms` SMs) with a workspace.
 cudaError_t launch_kv_attend_b2(const KvAttendParams &p, const KvAttendSpace &ws, int dtype, int splits, cudaStream_t st);

@@ -93,10 +93,11 @@ __device__ __forceinline__ uint32_t word_at(const uint32_t (&w)[W], int at, int 
     return __funnelshift_r(w[i], w[i + 1 < W ? i + 1 : i], s);
 }
 
-// Codes 4 i .. 4 i + 3 of the packed words w as two fp16 pairs.
+// Codes 4 i .. 4 i + 3 of the packed words w as two fp16 pairs; of 6 and 8 bits, whose entries are one
+// centroid and what fp16 leaves of it, also the pairs of the rests.
 template <int BITS, LutForm FORM, int W>
-__device__ __forceinline__ void quad(const uint32_t (&w)[W], int i,
-                                     uint32_t col, uint32_t &lo, uint32_t &hi) {
+__device__ __forceinline__ void quad(const uint32_t (&w)[W], int i, uint32_t col, uint32_t &lo,
+                                     uint32_t &hi, uint32_t &lo_rest, uint32_t &hi_rest) {
     if constexpr (BITS == 2) {
         const uint2 e = look8<uint2, FORM>(w[i >> 2], i & 3, col);
         lo = e.x;
@@ -110,21 +111,30 @@ __device__ __forceinline__ void quad(const uint32_t (&w)[W], int i,
         hi = look6<FORM>(v, 6, col);
     } else if constexpr (BITS == 6) {
         const uint32_t v = word_at(w, 24 * i, 24);
-        lo = prmt(look6<FORM>(v, 0, col), look6<FORM>(v, 6, col), 0x5410);
-        hi = prmt(look6<FORM>(v, 12, col), look6<FORM>(v, 18, col), 0x5410);
+        const uint32_t e[4] = {look6<FORM>(v, 0, col), look6<FORM>(v, 6, col),
+                               look6<FORM>(v, 12, col), look6<FORM>(v, 18, col)};
+        lo = prmt(e[0], e[1], 0x5410), hi = prmt(e[2], e[3], 0x5410);
+        lo_rest = prmt(e[0], e[1], 0x7632), hi_rest = prmt(e[2], e[3], 0x7632);
     } else {
         const uint32_t v = w[i];
-        lo = prmt(look8<uint32_t, FORM>(v, 0, col), look8<uint32_t, FORM>(v, 1, col), 0x5410);
-        hi = prmt(look8<uint32_t, FORM>(v, 2, col), look8<uint32_t, FORM>(v, 3, col), 0x5410);
+        const uint32_t e[4] = {look8<uint32_t, FORM>(v, 0, col), look8<uint32_t, FORM>(v, 1, col),
+                               look8<uint32_t, FORM>(v, 2, col), look8<uint32_t, FORM>(v, 3, col)};
+        lo = prmt(e[0], e[1], 0x5410), hi = prmt(e[2], e[3], 0x5410);
+        lo_rest = prmt(e[0], e[1], 0x7632), hi_rest = prmt(e[2], e[3], 0x7632);
     }
+}
+template <int BITS, LutForm FORM, int W>
+__device__ __forceinline__ void quad(const uint32_t (&w)[W], int i, uint32_t col, uint32_t &lo,
+                                     uint32_t &hi) {
+    uint32_t a, b;
+    quad<BITS, FORM>(w, i, col, lo, hi, a, b);
 }
 
 // The same codes of two rows x and y (the packed words of each), transposed: o[k] = (code 4 i + k
 // of x, that of y).  4-bit codes are merged to bytes of one code of each row first (`mixed`).
 template <int BITS, LutForm FORM, int W>
-__device__ __forceinline__ void quad_of_two(const uint32_t (&x)[W],
-                                            const uint32_t (&y)[W], int i, uint32_t col,
-                                            uint32_t (&o)[4]) {
+__device__ __forceinline__ void quad_of_two(const uint32_t (&x)[W], const uint32_t (&y)[W], int i,
+                                            uint32_t col, uint32_t (&o)[4], uint32_t (&rest)[4]) {
     if constexpr (BITS == 4) {
         // x = even codes of both rows, y = odd ones
         const int k = 2 * (i & 1);
@@ -135,13 +145,19 @@ __device__ __forceinline__ void quad_of_two(const uint32_t (&x)[W],
     } else if constexpr (BITS == 6) {
         const uint32_t u = word_at(x, 24 * i, 24), v = word_at(y, 24 * i, 24);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            o[k] = prmt(look6<FORM>(u, 6 * k, col), look6<FORM>(v, 6 * k, col), 0x5410);
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t a = look6<FORM>(u, 6 * k, col), b = look6<FORM>(v, 6 * k, col);
+            o[k] = prmt(a, b, 0x5410);
+            rest[k] = prmt(a, b, 0x7632);
+        }
     } else if constexpr (BITS == 8) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            o[k] = prmt(look8<uint32_t, FORM>(x[i], k, col), look8<uint32_t, FORM>(y[i], k, col),
-                        0x5410);
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t a = look8<uint32_t, FORM>(x[i], k, col);
+            const uint32_t b = look8<uint32_t, FORM>(y[i], k, col);
+            o[k] = prmt(a, b, 0x5410);
+            rest[k] = prmt(a, b, 0x7632);
+        }
     } else {
         uint32_t a, b, c, d;
         quad<BITS, FORM>(x, i, col, a, b);

@@ -20,4 +20,22 @@ __device__ __forceinline__ bool slot_ok(const KvView &c, long long slot) {
     return slot >= 0 && slot < (c.pages << c.page_log2);
 }
 
+// ---- codes beside a boundary ----
+// The quantizer's grid (oq_host.cpp, build_grid) has a value in steps of 2^-23 of its span, rounded
+// twice on the way; `at`, whose top byte is the code, passes a boundary in steps of G.  A value within
+// four steps of one, or of a cell's end (of normal values 5, 15 and 26 in a million at 2, 3 and 4 bits),
+// is looked at again in fp32.
+__device__ __forceinline__ uint32_t distance_to_bound(uint32_t at, int G) {
+    return at * 256u + (uint32_t)G * 1024u;
+}
+__device__ __forceinline__ uint32_t bound_width(int G) { return (uint32_t)G * 2048u; }
+
+// The code of the value v, one of `code` and its neighbours, by the boundaries about it.
+__device__ __forceinline__ uint32_t code_beside(uint32_t code, float v, float below, float above,
+                                                int bits) {
+    if (code > 0 && v < below)
+        return code - 1;
+    return code + 1 < (1u << bits) && v >= above ? code + 1 : code;
+}
+
 }  // namespace oq

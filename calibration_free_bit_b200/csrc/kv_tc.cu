@@ -128,6 +128,16 @@ __device__ __forceinline__ void pack32(const uint32_t (&c)[32], uint32_t *w) {
     }
 }
 
+// One column of this thread's lane of tensor memory (warp-collective).
+__device__ __forceinline__ void tmem_ld1(uint32_t at, uint32_t &r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r) : "r"(at) : "memory");
+}
+
+// Few codes are far apart, so a wrong one beside a boundary shows in fp16 rows; with 6 and 8 bits it is
+// off by less than the centroids' own rounding there.
+template <int BITS> constexpr bool kLook = BITS <= 4;
+
 template <int D, int BITS, bool BF16>
 __global__ void __launch_bounds__(Geo<D>::threads, 1)
 kv_write_tc(const KvWriteParams p, const uint4 *r_img, const int tbl_words, const int tiles) {
@@ -185,6 +195,8 @@ kv_write_tc(const KvWriteParams p, const uint4 *r_img, const int tbl_words, cons
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
+    // lane j: boundary j
+    const float bound = kLook<BITS> && lane < (1 << BITS) - 1 ? __ldg(p.bounds + lane) : 0.f;
     bool dead = false;
     uint32_t phase = 0;
     const int stride = gridDim.x * G::groups;
@@ -236,8 +248,8 @@ kv_write_tc(const KvWriteParams p, const uint4 *r_img, const int tbl_words, cons
             sum = half_sum[row] + half_sum[row + 128];
         }
         const float norm = sqrtf(sum / (float)p.h);
-        const float kk = p.K / (norm + p.eps);
-        uint32_t out[4 * BITS];
+        const float kk = p.K / (norm + p.eps), unit = p.unit / (norm + p.eps);
+        uint32_t out[4 * BITS], beside[4], any = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             uint32_t z[32];
@@ -249,7 +261,53 @@ kv_write_tc(const KvWriteParams p, const uint4 *r_img, const int tbl_words, cons
                 z[i] = k1ops::lds32(my_tbl + (q.x >> p.F) * pitch) + q.x * (uint32_t)p.G;
                 z[i + 1] = k1ops::lds32(my_tbl + (q.y >> p.F) * pitch) + q.y * (uint32_t)p.G;
             }
+            if constexpr (kLook<BITS>) {
+                uint32_t least = ~0u;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    least = min(least, distance_to_bound(z[i], p.G));
+                beside[k] = 0;
+                // (all of an empty row is 0, on the middle one)
+                const bool look = dst >= 0 && norm > 0.f && least < bound_width(p.G);
+                if (__any_sync(0xffffffffu, look)) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (look && distance_to_bound(z[i], p.G) < bound_width(p.G))
+                            beside[k] |= 1u << i;
+                    any |= __reduce_or_sync(0xffffffffu, beside[k]) ? 1u << k : 0u;
+                }
+            }
             pack32<BITS>(z, out + k * BITS);
+        }
+        if constexpr (kLook<BITS>) {
+            // values beside a boundary, by all lanes a column at a time (a tile has a few of them, and
+            // this code for all columns at once would cost it more than they do)
+#pragma unroll 1
+            for (; any; any &= any - 1) {
+                const int k = __ffs(any) - 1;
+                const uint32_t mine = k < 2 ? (k ? beside[1] : beside[0]) : (k > 2 ? beside[3] : beside[2]);
+#pragma unroll 1
+                for (uint32_t cols = __reduce_or_sync(0xffffffffu, mine); cols; cols &= cols - 1) {
+                    const int b = __ffs(cols) - 1, bit = (32 * k + b) * BITS, s = bit & 31;
+                    uint32_t z;
+                    tmem_ld1(my_tmem + 32 * k + b, z);
+                    const float v = __uint_as_float(z) * unit;
+                    const uint32_t q = __float_as_uint(
+                        __fadd_rd(fma_sat(__uint_as_float(z), kk, 0.5f), 1.0f));
+                    const uint32_t was =
+                        (k1ops::lds32(my_tbl + (q >> p.F) * pitch) + q * (uint32_t)p.G) >> 24;
+                    const float below = __shfl_sync(0xffffffffu, bound, was - 1);
+                    const float above = __shfl_sync(0xffffffffu, bound, was);
+                    uint32_t x = was ^ code_beside(was, v, below, above, BITS);
+                    x = (mine >> b) & 1u ? x : 0u;
+#pragma unroll
+                    for (int i = 0; i < 4 * BITS; ++i) {
+                        out[i] ^= i == bit >> 5 ? x << s : 0u;
+                        if (32 % BITS)
+                            out[i] ^= i == (bit >> 5) + 1 && s + BITS > 32 ? x >> (32 - s) : 0u;
+                    }
+                }
+            }
         }
         if (dst >= 0) {
             uint8_t *to = pick(p.c.codes, w) + dst * (D * BITS / 8) + part * (16 * BITS);

@@ -18,8 +18,6 @@
 //     does not see (a NaN, an infinity) never reaches it.
 #pragma once
 
-#include <type_traits>
-
 #include "kv_attend_ops.cuh"
 #include "kv_internal.h"
 #include "kv_lut.cuh"
@@ -77,20 +75,10 @@ __device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
            ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-template <bool BF16> __device__ __forceinline__ uint32_t idesc_q() {
-    return idesc_f16(128, 128) | (BF16 ? (1u << 7) | (1u << 10) : 0u);
+__device__ __forceinline__ uint32_t idesc_q() {      // both operands bf16
+    return idesc_f16(128, 128) | (1u << 7) | (1u << 10);
 }
 
-// 16 columns of tensor memory (the wait is in the same statement: nothing may touch the registers, not
-// even a copy or a spill, while the load is on its way).
-__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-                 "%11, %12, %13, %14, %15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-                   "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-                   "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                 : "r"(at) : "memory");
-}
 __device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
                  ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
@@ -105,7 +93,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 }  // namespace wide
 
-template <class E, int BITS>
+template <int BITS>
 __global__ void __launch_bounds__(wide::Shape<BITS>::threads, 1)
 attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) {
     using namespace wide;
@@ -496,7 +484,7 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                         const int node = (q.row_base + r) / p.group;
                         const int e = q.row_base + r - node * p.group;
                         v = *reinterpret_cast<const uint4 *>(
-                            static_cast<const E *>(p.q) + (q.s.row0 + node) * p.q_stride +
+                            static_cast<const __nv_bfloat16 *>(p.q) + (q.s.row0 + node) * p.q_stride +
                             (kvh * p.group + e) * D + ch * 8);
                     }
                     *reinterpret_cast<uint4 *>(at_address(raw, S::v_at) + operand_at(r, ch)) = v;
@@ -583,7 +571,7 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                 for (int k = 0; k < 8; ++k)
                     mma_ss(tmem, sw128_desc(base + S::v_at + (k >> 2) * 16384) + 2 * (k & 3),
                            sw128_desc(base + S::k_at + (k >> 2) * 16384) + 2 * (k & 3),
-                           idesc_q<std::is_same<E, __nv_bfloat16>::value>(), k != 0);
+                           idesc_q(), k != 0);
                 mma_commit(bar(B_Q));
             }
             meet();
@@ -627,9 +615,9 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
-template <class E, int BITS>
+template <int BITS>
 cudaError_t launch_wide(const KvAttendParams &p, const KvAttendSpace &ws, cudaStream_t st) {
-    auto *kern = attend_wide<E, BITS>;
+    auto *kern = attend_wide<BITS>;
     static PerDevice ready;
     const cudaError_t e = ready.once([&] {
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -3,10 +3,8 @@
 
 namespace oq {
 
-cudaError_t launch_kv_wide_b6(const KvAttendParams &p, const KvAttendSpace &ws, int dtype,
-                              cudaStream_t st) {
-    return dtype == OQ_BF16 ? attend::launch_wide<__nv_bfloat16, 6>(p, ws, st)
-                            : attend::launch_wide<__half, 6>(p, ws, st);
+cudaError_t launch_kv_wide_b6(const KvAttendParams &p, const KvAttendSpace &ws, cudaStream_t st) {
+    return attend::launch_wide<6>(p, ws, st);
 }
 
 }  // namespace oq

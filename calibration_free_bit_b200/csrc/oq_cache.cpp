@@ -171,8 +171,8 @@ void build_kv_lut(oq_codebook *cb) {
                                      (uint32_t)lut[(e >> (4 * k + 2)) & 3] << 16);
         else if (b <= 4)
             cb->kv_lut.push_back(lut[e & (L - 1)] | (uint32_t)lut[e >> b] << 16);
-        else
-            cb->kv_lut.push_back(lut[e] | (uint32_t)lut[e] << 16);
+        else                                      // and what fp16 leaves of it
+            cb->kv_lut.push_back(lut[e] | (uint32_t)to_half_bits(cb->kv_alpha * cb->c[e] - value(lut[e])) << 16);
     }
 }
 
@@ -346,7 +346,8 @@ int oq_kv_write(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache
     oq_rpbh *rw = const_cast<oq_rpbh *>(r);
     oq_codebook *cw = const_cast<oq_codebook *>(c);
     if ((rc = upload_ent(rw, dev)) != OQ_OK ||
-        (rc = upload(cw->mu, &cw->dev_tbl[dev], cw->tbl_img, "upload quantizer table")) != OQ_OK)
+        (rc = upload(cw->mu, &cw->dev_tbl[dev], cw->tbl_img, "upload quantizer table")) != OQ_OK ||
+        (rc = upload(cw->mu, &cw->dev_cent32[dev], cw->cent32, "upload centroids")) != OQ_OK)
         return rc;
     if (dtype != OQ_F32 &&
         (rc = rotation_matrix(rw, dtype == OQ_BF16 ? RMAT_BF16 : RMAT_F16, dev, &p.r_img)) != OQ_OK)
@@ -362,6 +363,8 @@ int oq_kv_write(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache
     p.tbl = cw->dev_tbl[dev];
     p.tbl_copies = c->bits <= 4 ? 32 : 1;
     p.tbl_words = (int)cw->tbl_img.size();
+    p.bounds = reinterpret_cast<const float *>(cw->dev_cent32[dev]) + (1 << c->bits);
+    p.unit = (float)std::sqrt((double)r->d / r->h);
     p.wide = p.c.row_bytes % 32 == 0 &&
              ((reinterpret_cast<uintptr_t>(cache->k_codes) |
                reinterpret_cast<uintptr_t>(cache->v_codes)) & 31u) == 0;
@@ -499,8 +502,8 @@ int oq_kv_attend(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cach
     p.o_scale = (float)unit;
     cudaStream_t st = (cudaStream_t)stream;
     std::string why;
-    if (p.c.d == 128 &&
-        (rc = rotation_matrix(rw, dtype == OQ_BF16 ? RMAT_BF16 : RMAT_F16, dev, &p.r_img)) != OQ_OK)
+    if (p.c.d == 128 && dtype == OQ_BF16 &&
+        (rc = rotation_matrix(rw, RMAT_BF16, dev, &p.r_img)) != OQ_OK)
         return rc;
     void *space = nullptr;
     const size_t need = oq::kv_attend_space(p, dtype, di->sms);

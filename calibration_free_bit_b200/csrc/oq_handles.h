@@ -40,7 +40,7 @@ struct oq_codebook {
     std::mutex mu;
     uint32_t *dev_tbl[oq::kMaxDevices] = {};
     uint32_t *dev_dec[oq::kMaxDevices] = {};
-    std::vector<float> cent32;                    // unit centroids, fp32 (the cache's kernels)
+    std::vector<float> cent32;                    // unit centroids, then boundaries, fp32 (the cache)
     uint32_t *dev_cent32[oq::kMaxDevices] = {};
     // the cache's fp16 decode table (oq_cache.cpp, build_kv_lut): centroids times kv_alpha
     double kv_alpha = 1.0;
