@@ -243,8 +243,8 @@ cudaError_t run_wide(const KvAttendParams &p, const KvAttendSpace &ws, cudaStrea
 // How a call runs: tiles of 128 rows (kv_wide.cuh) for many rows a key head of 128, else of 8 or, of
 // heads of 128, 16 (kv_attend.cuh), the latter by clusters where all tokens that the page tables can
 // hold are little work; and where its workspace's arrays lie.  fp16 stays with the small tiles: its
-// outputs are eight times as fine as bf16's, and a query and a key of one fp16 number an element, as
-// the large tiles have them, left an error of 1.2e-3 where the output's own rounding is 2.1e-4.
+// outputs are eight times as fine as bf16's, and one fp16 number for each element of a query, a key and
+// a weight, as the large tiles have them, left an error of 1.2e-3 where the output's rounding is 2.1e-4.
 struct Plan {
     bool wide;
     int tile;                     // rows of a tile

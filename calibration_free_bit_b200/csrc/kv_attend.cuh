@@ -28,10 +28,9 @@
 // (over a power of two of its own), the centroids (times alpha, see build_kv_lut) and the weights
 // p s_v, which are taken relative to a power of two above the row's largest s_v and times 2^6 to
 // 2^14: what a token adds is resolved down to 2^-31 of the largest.  With SPLIT (fp16 outputs) a
-// query enters as a sum of two fp16 numbers (its rounding is the one that scores multiply), and so do
-// the centroids of 6 and 8 bits, which are too many for alpha to help: errors of 2.6e-4 to 3.0e-4 of
-// an output's length, of which its own rounding is 2.1e-4 (without the second numbers 4.5e-4 and
-// 5.9e-4 at 6 and 8 bits).
+// query and a weight enter as sums of two fp16 numbers, and so do the centroids of 6 and 8 bits, which
+// are too many for alpha to help: errors of 2.1e-4 to 2.5e-4 of an output's length, of which its own
+// rounding is 2.1e-4 (queries alone: 2.6e-4 at 2 bits, 3.1e-4 at 4, 5.9e-4 at 8).
 #pragma once
 
 #include <cooperative_groups.h>
@@ -362,7 +361,7 @@ __device__ __forceinline__ void walk_tiles(const KvAttendParams &p, uint32_t col
             }
         }
         // weights
-        uint32_t pb[NT][2];
+        uint32_t pb[NT][2], pr[NT][2];                // and what fp16 leaves of them
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float w[4];
@@ -379,8 +378,12 @@ __device__ __forceinline__ void walk_tiles(const KvAttendParams &p, uint32_t col
                         w[i] = 0.f;
             }
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-                pb[n][k] = transpose8x8(half2_bits(w[2 * k], w[2 * k + 1]));
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t hi = half2_bits(w[2 * k], w[2 * k + 1]);
+                pb[n][k] = transpose8x8(hi);
+                if constexpr (SPLIT)
+                    pr[n][k] = transpose8x8(half2_rest(w[2 * k], w[2 * k + 1], hi));
+            }
         }
         // O^T += V^T P^T: rows of tile j are elements g D/8 + 2j and 2j + 1
         uint32_t vw[4][S::vu];
@@ -402,8 +405,11 @@ __device__ __forceinline__ void walk_tiles(const KvAttendParams &p, uint32_t col
             for (int h = 0; h < 2; ++h) {
                 const uint32_t a[4] = {x[2 * h], x[2 * h + 1], y[2 * h], y[2 * h + 1]};
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n) {
                     mma16816(o.acc[n][j + h], a, pb[n][0], pb[n][1]);
+                    if constexpr (SPLIT)
+                        mma16816(o.acc[n][j + h], a, pr[n][0], pr[n][1]);
+                }
                 if constexpr (RESTS) {
                     const uint32_t ra[4] = {rx[2 * h], rx[2 * h + 1], ry[2 * h], ry[2 * h + 1]};
 #pragma unroll

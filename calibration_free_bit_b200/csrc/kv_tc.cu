@@ -57,11 +57,12 @@ __device__ __forceinline__ uint32_t operand_at(int r, int ch, int rows) {
 }
 
 template <int D, bool BF16>
-__device__ __forceinline__ void issue_mma(uint32_t tmem, uint32_t sA, uint32_t sR, uint32_t bar) {
+__device__ __forceinline__ void issue_mma(uint32_t tmem, uint32_t sA, uint32_t sR, uint32_t bar,
+                                          bool add = false) {
 #pragma unroll
     for (int k = 0; k < D / 16; ++k)
         mma_ss(tmem, sw128_desc(sA + (k >> 2) * (128 * 128)) + 2 * (k & 3),
-               sw128_desc(sR + (k >> 2) * (D * 128)) + 2 * (k & 3), idesc<D, BF16>(), k != 0);
+               sw128_desc(sR + (k >> 2) * (D * 128)) + 2 * (k & 3), idesc<D, BF16>(), add || k != 0);
     mma_commit(bar);
 }
 
@@ -379,6 +380,10 @@ kv_read_tc(const KvReadParams p, const uint4 *r_img, const int tiles) {
     const int heads = p.c.kv_heads, half_tiles = tiles / 2;
     const long long rows = (long long)p.T * heads;
     constexpr int words = 4 * BITS;                       // of this thread's 128 elements
+    // fp16 rows of 6 and 8 bits: a second product adds what fp16 leaves of the centroids (8000 rows of
+    // 256: errors of 2.3e-4 to 2.9e-4 of their length, a few other codes among them, and not of 2.9e-4
+    // to 3.1e-4; the output's rounding is 2.1e-4)
+    constexpr bool kRests = std::is_same<E, __half>::value && BITS >= 6;
 
     // the codes and norm of this thread's row (zeros and 0 where the slot names none)
     auto load = [&](int tile, uint32_t (&c)[words], float &norm, E *&to) {
@@ -419,37 +424,47 @@ kv_read_tc(const KvReadParams p, const uint4 *r_img, const int tiles) {
     for (; tile < tiles; tile += stride) {
         bulk_wait_read<0>();                              // the last tile's rows have left
         group_sync(1 + grp, G::group_threads);
-        // four chunks of 8 elements at a time, so that their lookups are under way together (the
-        // compiler does not move a load over a store to the operand)
-#pragma unroll
-        for (int k = 0; k < 16; k += 4) {
-            uint4 v[4];
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                quad<BITS, ANYWHERE>(codes, 2 * (k + h), col, v[h].x, v[h].y);
-                quad<BITS, ANYWHERE>(codes, 2 * (k + h) + 1, col, v[h].z, v[h].w);
+        auto done = [&] {
+            if (!dead && !mbar_wait(bar, phase)) {
+                dead = true;
+                atomicOr(p.err, KV_ERR_WAIT);
             }
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-                *reinterpret_cast<uint4 *>(a_sm + operand_at(row, part * 16 + k + h, 128)) = v[h];
-        }
-        fence_async_smem();
-        tc_fence_before();
-        group_sync(1 + grp, G::group_threads);
-        if (tid == 0) {
+            phase ^= 1;
             tc_fence_after();
-            issue_mma<D, false>(tmem, sA, sR, bar);
+        };
+#pragma unroll
+        for (int pass = 0; pass < (kRests ? 2 : 1); ++pass) {
+            if (pass)
+                done();
+            // four chunks of 8 elements at a time, so that their lookups are under way together (the
+            // compiler does not move a load over a store to the operand)
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+                uint4 v[4], rest[4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    quad<BITS, ANYWHERE>(codes, 2 * (k + h), col, v[h].x, v[h].y, rest[h].x, rest[h].y);
+                    quad<BITS, ANYWHERE>(codes, 2 * (k + h) + 1, col, v[h].z, v[h].w, rest[h].z,
+                                         rest[h].w);
+                }
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                    *reinterpret_cast<uint4 *>(a_sm + operand_at(row, part * 16 + k + h, 128)) =
+                        pass ? rest[h] : v[h];
+            }
+            fence_async_smem();
+            tc_fence_before();
+            group_sync(1 + grp, G::group_threads);
+            if (tid == 0) {
+                tc_fence_after();
+                issue_mma<D, false>(tmem, sA, sR, bar, pass > 0);
+            }
         }
         const float s = norm * p.scale;
         E *mine = to;
         if (tile + stride < tiles)
             load(tile + stride, codes, norm, to);
-        if (!dead && !mbar_wait(bar, phase)) {
-            dead = true;
-            atomicOr(p.err, KV_ERR_WAIT);
-        }
-        phase ^= 1;
-        tc_fence_after();
+        done();
         unsigned char *stage = a_sm + row * G::stage_stride + part * 256;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
