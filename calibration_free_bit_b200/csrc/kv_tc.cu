@@ -135,9 +135,9 @@ __device__ __forceinline__ void tmem_ld1(uint32_t at, uint32_t &r) {
                  : "=r"(r) : "r"(at) : "memory");
 }
 
-// Few codes are far apart, so a wrong one beside a boundary shows in fp16 rows; with 6 and 8 bits it is
-// off by less than the centroids' own rounding there.
-template <int BITS> constexpr bool kLook = BITS <= 4;
+// Few codes are far apart, so a wrong one beside a boundary shows in fp16 rows; with 8 bits it is off by
+// less than their rounding.
+template <int BITS> constexpr bool kLook = BITS <= 6;
 
 template <int D, int BITS, bool BF16>
 __global__ void __launch_bounds__(Geo<D>::threads, 1)
@@ -196,8 +196,9 @@ kv_write_tc(const KvWriteParams p, const uint4 *r_img, const int tbl_words, cons
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-    // lane j: boundary j
+    // lane j: boundaries j and, of 6 bits, 32 + j
     const float bound = kLook<BITS> && lane < (1 << BITS) - 1 ? __ldg(p.bounds + lane) : 0.f;
+    const float bound2 = BITS == 6 && lane < 31 ? __ldg(p.bounds + 32 + lane) : 0.f;
     bool dead = false;
     uint32_t phase = 0;
     const int stride = gridDim.x * G::groups;
@@ -297,8 +298,14 @@ kv_write_tc(const KvWriteParams p, const uint4 *r_img, const int tbl_words, cons
                         __fadd_rd(fma_sat(__uint_as_float(z), kk, 0.5f), 1.0f));
                     const uint32_t was =
                         (k1ops::lds32(my_tbl + (q >> p.F) * pitch) + q * (uint32_t)p.G) >> 24;
-                    const float below = __shfl_sync(0xffffffffu, bound, was - 1);
-                    const float above = __shfl_sync(0xffffffffu, bound, was);
+                    float below = __shfl_sync(0xffffffffu, bound, was - 1);
+                    float above = __shfl_sync(0xffffffffu, bound, was);
+                    if constexpr (BITS == 6) {
+                        const float b2 = __shfl_sync(0xffffffffu, bound2, was - 1);
+                        const float a2 = __shfl_sync(0xffffffffu, bound2, was);
+                        below = was > 32 ? b2 : below;
+                        above = was >= 32 ? a2 : above;
+                    }
                     uint32_t x = was ^ code_beside(was, v, below, above, BITS);
                     x = (mine >> b) & 1u ? x : 0u;
 #pragma unroll
