@@ -127,7 +127,8 @@ namespace host {
 
 // The fp16 decode table of the cache's kernels: 32-bit words of two centroids.
 //   bits 2: entry e (a byte, four codes) = two words; bits 3, 4: entry e (two codes) = one word,
-//   the lower code in the low half; bits 6, 8: entry e (one code) in both halves.
+//   the lower code in the low half; bits 6, 8: entry e (one code) in the low half, what fp16 leaves
+//   of it in the high one.
 // The centroids are multiplied by kv_alpha in [1, 2) before they are rounded to fp16, and the
 // kernels divide by it in fp32: of 4096 factors the one whose rounded centroids are nearest (cells
 // weighted by the mass that the quantizer gives them).  At 4 bits that takes the rounding from
@@ -146,8 +147,9 @@ void build_kv_lut(oq_codebook *cb) {
         mass[i] = std::exp(-0.5 * cb->c[i] * cb->c[i]) * (hi - lo);
     }
     double best = -1.0;
-    for (int k = 0; k < 4096; ++k) {
-        const double a = 1.0 + k / 4096.0;
+    const int tries = L <= 16 ? 4096 : 4096 / L;  // of many centroids all factors leave about the same
+    for (int k = 0; k < tries; ++k) {
+        const double a = 1.0 + (double)k / tries;
         double err = 0.0;
         for (int i = L / 2; i < L; ++i) {
             const double d = value(to_half_bits(a * cb->c[i])) / a - cb->c[i];
