@@ -455,8 +455,9 @@ int oq_kv_attend(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cach
     if (max_nodes < 1 || max_nodes > OQ_KV_MAX_NODES)
         return fail(OQ_EINVAL, "%s: max_nodes = %d not in [1, %d]", who, max_nodes,
                     OQ_KV_MAX_NODES);
-    if (table_width < 1 || ((long long)table_width << p.c.page_log2) > 0x7fffffffll)
-        return fail(OQ_EINVAL, "%s: table_width = %d must be positive, and hold fewer than 2^31 "
+    // (tiles of up to 128 tokens are counted in 32 bits)
+    if (table_width < 1 || ((long long)table_width << p.c.page_log2) > 0x7fffff00ll)
+        return fail(OQ_EINVAL, "%s: table_width = %d must be positive, and hold at most 2^31 - 256 "
                                "tokens", who, table_width);
     if (!(scale > 0.0) || !std::isfinite(scale))
         return fail(OQ_EINVAL, "%s: scale must be positive and finite", who);

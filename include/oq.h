@@ -272,9 +272,11 @@ int oq_debug_arm_wait_timeout(int kernel, long long limit_cycles);
  *
  * Rows are [tokens, heads, d] with the heads of a token contiguous; a token stride (in elements,
  * a multiple of 16 bytes) lets them be slices of a fused projection.  dtype is OQ_BF16, OQ_F16
- * or, where a call says so, OQ_F32.  Each call is one kernel on `stream`, keeps no workspace and
- * allocates nothing (after its handles' first use on the device), so calls on several streams
- * and captured graphs may run at the same time. */
+ * or, where a call says so, OQ_F32.  oq_apply_rope, oq_kv_write and oq_kv_read are one kernel each
+ * on `stream` and allocate nothing (after their handles' first use on the device); oq_kv_attend is
+ * one kernel where the page tables can hold little, else three, with a workspace that it takes
+ * from the device's stream-ordered pool and gives back on `stream`.  Nothing is kept from one call
+ * for the next, so calls on several streams and captured graphs may run at the same time. */
 typedef struct oq_rope oq_rope;
 
 #define OQ_KV_MAX_HEADS 1024  /* heads of a token                                          */
@@ -351,9 +353,12 @@ int oq_kv_read(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache,
  * order); with tree_mask = NULL the nodes up to its own, so one node a sequence is a plain
  * decoding step.  out = sum_t p_t v_hat_t, p the softmax of scale * q . k_hat_t over the tokens it
  * sees; a row that sees nothing gives zeros.  Query head i reads key head i / (q_heads/kv_heads).
- * q, out: device, [q_rows, q_heads, d] of dtype (OQ_BF16 or OQ_F16).  q_start: int32 [B+1];
+ * q, out: device, [q_rows, q_heads, d] of dtype (OQ_BF16 or OQ_F16); out = q with the same stride
+ * works in place, any other overlap is not allowed.  q_start: int32 [B+1];
  * prefix: int32 [B]; page_table: int32 [B, table_width] (entries past a sequence's last page are
- * not read); tree_mask: int64 [q_rows] or NULL; all device.  Rows of out outside every sequence
+ * not read; at most 2^31 - 256 tokens fit); tree_mask: int64 [q_rows] or NULL; all device.  The
+ * workspace has 4 to 8 bytes for each of B * max_nodes * q_heads * d elements, a key head's rows
+ * rounded up to tiles of 8, 16 or 128, and 10 MB more.  Rows of out outside every sequence
  * are left as they were.  What is not visible is never multiplied: masked tokens may hold
  * anything.  A sequence whose rows or lengths do not fit (q_start decreasing, past q_rows or over
  * max_nodes; prefix negative or past the table) is skipped, a token whose page is outside the

@@ -891,3 +891,14 @@ def test_several_pieces_of_many_rows_a_worker(oq, bits, length, nodes, dtype):
         assert torch.equal(oq.oq_kv_attend(**a), out)
     oq.oq_check()
     close(out, s.want(sample=[0, 7]), dtype)
+
+
+@pytest.mark.parametrize("nodes,roomy,dtype", [(1, False, BF16), (3, True, F16), (40, False, BF16)])
+def test_attention_in_place(oq, nodes, roomy, dtype):
+    s = Serving(oq, [300, 41], [nodes] * 2, 8, 2, 128, 128, 4, 16, dtype, seed=91,
+                columns=ROOMY // 16 if roomy else 0).trees()
+    a = s.gpu()
+    want = oq.oq_kv_attend(**a)
+    oq.oq_kv_attend(**a, out=a["q"])
+    oq.oq_check()
+    assert torch.equal(a["q"], want)

@@ -199,3 +199,8 @@ def test_oracle_rotation_and_packing():
         c = rng.integers(0, 1 << bits, (3, 128))
         assert np.array_equal(CO.unpack(CO.pack(c, bits), bits), c)
         assert np.array_equal(CO.pack(c, bits), O.pack(c.astype(np.uint8), bits))
+
+
+@pytest.mark.parametrize("page,width", [(16, (1 << 27) - 15), (1024, 1 << 21), (16, 1 << 27)])
+def test_attend_refuses_tables_of_too_many_tokens(page, width):
+    assert _attend(cache=dict(page=page), width=width) == oq.OQ_EINVAL
