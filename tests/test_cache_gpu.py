@@ -902,3 +902,14 @@ def test_attention_in_place(oq, nodes, roomy, dtype):
     oq.oq_kv_attend(**a, out=a["q"])
     oq.oq_check()
     assert torch.equal(a["q"], want)
+
+
+@pytest.mark.parametrize("hq,hk,nodes,dtype", [(1024, 1, 2, BF16), (1024, 1, 2, F16),
+                                               (1024, 1024, 1, BF16), (1024, 512, 20, BF16)])
+@pytest.mark.parametrize("roomy", [False, True])
+def test_the_most_heads(oq, hq, hk, nodes, dtype, roomy):
+    s = Serving(oq, [37], [nodes], hq, hk, 128, 128, 4, 16, dtype, seed=92,
+                columns=ROOMY // 16 if roomy else 0).trees()
+    out = oq.oq_kv_attend(**s.gpu())
+    oq.oq_check()
+    close(out, s.want(sample=sorted({0, hk // 2, hk - 1})), dtype)
