@@ -12,10 +12,10 @@
 // score on the way; only if a row of the two warps has passed it (kSlack) is a unit done again.
 // A unit needs about a thousand cycles each of shared memory (at 4 bits 16384 lookups of two codes, 64
 // KB of operands stored), of exponentials (16384) and of issue slots, and half of that of the tensor
-// cores; it takes 4400, since none of its steps (decode, S, softmax, P V) has warps enough to hide its
+// cores; it takes 4300, since none of its steps (decode, S, softmax, P V) has warps enough to hide its
 // latencies, and more warps have too few registers.  B200, 4 bits: 2 sequences of 131 000 tokens with 31
-// nodes, 8 key heads: 291 us in all (codes and norms at 0.98 TB/s); 8 bits: 16 sequences of 129 to 4095
-// tokens with 61 nodes 177 us, 52 of them set-up and joining of their 256 segments.
+// nodes, 8 key heads: 281 us in all (codes and norms at 1.02 TB/s); 8 bits: 16 sequences of 129 to 4095
+// tokens with 61 nodes 168 us, 50 of them set-up and joining of their 256 segments.
 //   - Key norms enter the operand (times 2^-e, e by 32 tokens, so that fp16 holds any norm): scores
 //     of a group of 32 tokens then share one factor, and the search for a new maximum is a maximum
 //     over raw products.  Value norms enter with the weights, a row at a time, so that what a row
@@ -201,16 +201,35 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
         for (uint32_t pieces = 0; next_piece<WideForm>(p, walk, q); ++pieces) {
             const Seq &s = q.s;
             const int n = q.n, tile0 = q.tile0, nrows = q.nrows;
-            // the rotation to K's first stage (the raw queries go to V's)
+            // the rotation to K's first stage, the raw queries to V's (these warps have seen the end of
+            // the last piece's products)
             {
-                uint4 v[kTile / 16 / (32 * kSoftWarps)];
+                constexpr int per = kTile / 16 / (32 * kSoftWarps);
+                uint4 v[per];
 #pragma unroll
-                for (int i = 0; i < kTile / 16 / (32 * kSoftWarps); ++i)
+                for (int i = 0; i < per; ++i)
                     v[i] = __ldg(r_img + i * 32 * kSoftWarps + threadIdx.x);
 #pragma unroll
-                for (int i = 0; i < kTile / 16 / (32 * kSoftWarps); ++i)
+                for (int i = 0; i < per; ++i)
                     reinterpret_cast<uint4 *>(at_address(raw, S::k_at))[i * 32 * kSoftWarps +
                                                                         threadIdx.x] = v[i];
+                const int ch = threadIdx.x & 15;
+#pragma unroll
+                for (int i = 0; i < per; ++i) {
+                    const int row = i * 16 + (threadIdx.x >> 4);
+                    v[i] = make_uint4(0, 0, 0, 0);
+                    if (row < nrows) {
+                        const int node = (q.row_base + row) / p.group;
+                        const int e = q.row_base + row - node * p.group;
+                        v[i] = *reinterpret_cast<const uint4 *>(
+                            static_cast<const __nv_bfloat16 *>(p.q) + (s.row0 + node) * p.q_stride +
+                            (q.kvh * p.group + e) * D + ch * 8);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < per; ++i)
+                    *reinterpret_cast<uint4 *>(at_address(raw, S::v_at) +
+                                               operand_at(i * 16 + (threadIdx.x >> 4), ch)) = v[i];
             }
             fence_async_smem();
             meet();
@@ -484,27 +503,6 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
             int page1 = page_of(1), page2 = page_of(2);
             load(cur, 0, page_of(0));
             fetch(1, page1);
-            // The raw queries go to V's first stage once the piece before is done with it: by V's
-            // decoders, which have followed P V unit by unit (a wait is for a barrier's next phase).
-            if (w == 1) {
-                const int t = dt - 128 * kParts, ch = t & 15;
-                if (done > 0)
-                    wait(B_PV + ((done - 1) & 1u), (done - 1) >> 1);
-#pragma unroll
-                for (int i = 0; i < 16 / kParts; ++i) {
-                    const int r = i * 8 * kParts + (t >> 4);
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (r < q.nrows) {
-                        const int node = (q.row_base + r) / p.group;
-                        const int e = q.row_base + r - node * p.group;
-                        v = *reinterpret_cast<const uint4 *>(
-                            static_cast<const __nv_bfloat16 *>(p.q) + (q.s.row0 + node) * p.q_stride +
-                            (kvh * p.group + e) * D + ch * 8);
-                    }
-                    *reinterpret_cast<uint4 *>(at_address(raw, S::v_at) + operand_at(r, ch)) = v;
-                }
-            }
-            fence_async_smem();
             meet();
             meet();
             for (int i = 0; i < n; ++i) {
