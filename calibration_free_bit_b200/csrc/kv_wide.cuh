@@ -352,31 +352,33 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                         }
                         vtop = fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w));
                     } else {
+                        // (selections, no branches: every lane sees other tokens)
                         sum = vtop = 0.f;
 #pragma unroll 1
-                        for (int k = 0; k < 2; ++k) {
-                            const uint32_t v = seen(k);
-                            const float f = qs * ke[k];
-                            uint32_t z[32], w[16];
-                            tmem_ld32(tS + 32 * k, z);
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t v = seen(k >> 1) >> (16 * (k & 1));
+                            const float f = qs * ke[k >> 1];
+                            uint32_t y[16], w[8];
+                            tmem_ld16(tS + 16 * k, y);
 #pragma unroll
-                            for (int j = 0; j < 32; j += 2) {
-                                float pw[2];
+                            for (int j = 0; j < 16; j += 4) {
+                                const float4 n4 = *reinterpret_cast<const float4 *>(vn + 16 * k + j);
+                                const float nv[4] = {n4.x, n4.y, n4.z, n4.w};
+                                float pw[4];
 #pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    pw[h] = 0.f;
-                                    if ((v >> (j + h)) & 1u) {
-                                        const float x = __uint_as_float(z[j + h]) * f;
-                                        const float nv = vn[32 * k + j + h], e = ex2(x - m);
-                                        top = fmaxf(top, x);
-                                        vtop = fmaxf(vtop, nv);
-                                        sum += e;
-                                        pw[h] = e * (nv * vinv);
-                                    }
+                                for (int h = 0; h < 4; ++h) {
+                                    const bool see = (v >> (j + h)) & 1u;
+                                    const float x = see ? __uint_as_float(y[j + h]) * f : -CUDART_INF_F;
+                                    const float n1 = see ? nv[h] : 0.f, e = ex2(x - m);
+                                    top = fmaxf(top, x);
+                                    vtop = fmaxf(vtop, n1);
+                                    sum += e;
+                                    pw[h] = e * (n1 * vinv);
                                 }
                                 w[j / 2] = half2_bits(pw[0], pw[1]);
+                                w[j / 2 + 1] = half2_bits(pw[2], pw[3]);
                             }
-                            tmem_st16(tP + 16 * k, w);
+                            tmem_st8(tP + 8 * k, w);
                         }
                     }
                     if (again || !any(top > m + kSlack || vtop > vs)) {
