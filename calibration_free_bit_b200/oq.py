@@ -391,19 +391,23 @@ def oq_apply_rope(rope: Rope, x: torch.Tensor, positions: torch.Tensor, k=None, 
     xs = _rows(x, "x")
     T, heads, d = x.shape
     if out is None:
-        out = _like(x)
-    ys = _rows(out, "out", heads, d, x.dtype)
-    if out.shape[0] != T:
-        _bad(f"out has {out.shape[0]} tokens, x {T}")
+        out, ys = _like(x), heads * d
+    else:
+        ys = _rows(out, "out", heads, d, x.dtype)
+        if out.shape[0] != T:
+            _bad(f"out has {out.shape[0]} tokens, x {T}")
     kp, ks, kyp, kys, k_heads = None, 0, None, 0, 0
     if k is not None:
         ks = _rows(k, "k", d=d, dtype=x.dtype)
+        kt, k_heads = k.shape[0], k.shape[1]
+        if kt != T:
+            _bad(f"k has {kt} tokens, x {T}")
         if k_out is None:
-            k_out = _like(k)
-        k_heads = k.shape[1]
-        kys = _rows(k_out, "k_out", k_heads, d, x.dtype)
-        if k.shape[0] != T or k_out.shape[0] != T:
-            _bad(f"k has {k.shape[0]} tokens, k_out {k_out.shape[0]}, x {T}")
+            k_out, kys = _like(k), k_heads * d
+        else:
+            kys = _rows(k_out, "k_out", k_heads, d, x.dtype)
+            if k_out.shape[0] != T:
+                _bad(f"k_out has {k_out.shape[0]} tokens, x {T}")
         kp, kyp = k.data_ptr(), k_out.data_ptr()
     pos = _ints(positions, "positions", torch.int64, (T,))
     _run(_device(x, positions, out, k, k_out), lib().oq_apply_rope,
@@ -475,12 +479,17 @@ def oq_kv_read(r: RPBH, c: Codebook, cache: KVCache, slots: torch.Tensor, k=None
     T = slots.shape[0] if slots.dim() == 1 else -1
     at = _ints(slots, "slots", torch.int64, (T,))
     shape = (T, cache.kv_heads, cache.d)
+    ks = vs = cache.kv_heads * cache.d
     if k is None:
+        if out_dtype not in _ROW_DTYPES:
+            _bad(f"out_dtype {out_dtype}: expected fp32, bf16 or fp16")
         k = slots.new_empty(shape, dtype=out_dtype)
+    else:
+        ks = _rows(k, "k", cache.kv_heads, cache.d)
     if v is None:
-        v = slots.new_empty(shape, dtype=k.dtype)
-    ks = _rows(k, "k", cache.kv_heads, cache.d)
-    vs = _rows(v, "v", cache.kv_heads, cache.d, k.dtype)
+        v = torch.empty_like(k) if ks == vs else slots.new_empty(shape, dtype=k.dtype)
+    else:
+        vs = _rows(v, "v", cache.kv_heads, cache.d, k.dtype)
     if k.shape[0] != T or v.shape[0] != T:
         _bad(f"k and v must have {T} tokens")
     _run(_device(cache.k_codes, k, v, slots), lib().oq_kv_read,
@@ -500,10 +509,11 @@ def oq_kv_attend(r: RPBH, c: Codebook, cache: KVCache, q: torch.Tensor, q_start:
     qs = _rows(q, "q", d=cache.d)
     rows, heads = q.shape[0], q.shape[1]
     if out is None:
-        out = _like(q)
-    os_ = _rows(out, "out", heads, cache.d, q.dtype)
-    if out.shape[0] != rows:
-        _bad(f"out has {out.shape[0]} rows, q {rows}")
+        out, os_ = _like(q), heads * cache.d
+    else:
+        os_ = _rows(out, "out", heads, cache.d, q.dtype)
+        if out.shape[0] != rows:
+            _bad(f"out has {out.shape[0]} rows, q {rows}")
     B = prefix.shape[0] if prefix.dim() == 1 else -1
     width = page_table.shape[1] if page_table.dim() == 2 else 0
     start_p = _ints(q_start, "q_start", torch.int32, (B + 1,))
