@@ -14,8 +14,8 @@
 // KB of operands stored), of exponentials (16384) and of issue slots, and half of that of the tensor
 // cores; it takes 4300, since none of its steps (decode, S, softmax, P V) has warps enough to hide its
 // latencies, and more warps have too few registers.  B200, 4 bits: 2 sequences of 131 000 tokens with 31
-// nodes, 8 key heads: 279 us in all (codes and norms at 1.03 TB/s); 8 bits: 16 sequences of 129 to 4095
-// tokens with 61 nodes 165 us, 43 of them set-up and joining of their 256 segments.
+// nodes, 8 key heads: 276 us in all (codes and norms at 1.04 TB/s); 8 bits: 16 sequences of 129 to 4095
+// tokens with 61 nodes 160 us, 43 of them set-up and joining of their 256 segments.
 //   - Key norms enter the operand (times 2^-e, e by 32 tokens, so that fp16 holds any norm): scores
 //     of a group of 32 tokens then share one factor, and the search for a new maximum is a maximum
 //     over raw products.  Value norms enter with the weights, a row at a time, so that what a row
