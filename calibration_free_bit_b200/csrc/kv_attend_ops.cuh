@@ -272,12 +272,13 @@ __device__ __forceinline__ bool next_piece(const KvAttendParams &p, Walk &w, Pie
 }
 
 // The forms: tiles of many rows (kv_wide.cuh) and of 8 NT (kv_attend.cuh).  `extra`, us: 16 sequences with
-// 61 nodes 165, 160 and 162 with 2, 3 and 4; 8 sequences, 40 key heads 45.8, 47.4 and 47.5 with 3, 4 and 6.
+// 61 nodes 165, 160 and 162 with 2, 3 and 4; 64 sequences of single tokens 87.3, 87.0 and 87.0 with 3, 4
+// and 6, 8 sequences of 40 key heads 45.8, 47.4 and 47.5.
 struct WideForm {
     static constexpr int tokens = 128, rows = 128, extra = 3;
 };
 template <int NT> struct NarrowForm {
-    static constexpr int tokens = 16, rows = 8 * NT, extra = 3;
+    static constexpr int tokens = 16, rows = 8 * NT, extra = 4;
 };
 
 }  // namespace attend

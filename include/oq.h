@@ -362,7 +362,8 @@ int oq_kv_read(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache,
  * are left as they were.  What is not visible is never multiplied: masked tokens may hold
  * anything.  A sequence whose rows or lengths do not fit (q_start decreasing, past q_rows or over
  * max_nodes; prefix negative or past the table) is skipped, a token whose page is outside the
- * cache is not seen, and oq_check reports both.
+ * cache is not seen, and oq_check reports both.  The same call gives the same bits; how a long row's
+ * sum is split depends on the whole call, so other sequences beside it may change its rounding.
  * Errors: as oq_kv_write. */
 int oq_kv_attend(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache, const void *q,
                  long long q_stride, void *out, long long out_stride, int dtype, int q_rows,
