@@ -14,12 +14,14 @@
 // KB of operands stored), of exponentials (16384) and of issue slots, and half of that of the tensor
 // cores; it takes 4300, since none of its steps (decode, S, softmax, P V) has warps enough to hide its
 // latencies, and more warps have too few registers.  B200, 4 bits: 2 sequences of 131 000 tokens with 31
-// nodes, 8 key heads: 276 us in all (codes and norms at 1.04 TB/s); 8 bits: 16 sequences of 129 to 4095
+// nodes, 8 key heads: 281 us in all (codes and norms at 1.02 TB/s); 8 bits: 16 sequences of 129 to 4095
 // tokens with 61 nodes 160 us, 43 of them set-up and joining of their 256 segments.
-//   - Key norms enter the operand (times 2^-e, e by 32 tokens, so that fp16 holds any norm): scores
-//     of a group of 32 tokens then share one factor, and the search for a new maximum is a maximum
-//     over raw products.  Value norms enter with the weights, a row at a time, so that what a row
-//     does not see (a NaN, an infinity) never reaches it.
+//   - A group of 32 tokens that all rows see, with key norms of one order (nearly all of a prefix), has
+//     them in the operand, times 2^-e: its scores share one factor, and the search for a new maximum is
+//     a maximum over raw products.  Of any other group (with nodes, a loud key, a NaN) the operand is
+//     bare centroids, and the norms multiply the products in fp32, token by token (a product is below
+//     2^12, and the cache's write stores no norm above 2^64).  Value norms enter with the weights, a row
+//     at a time.  So what a row does not see never reaches it, nor what stands beside it.
 #pragma once
 
 #include "kv_attend_ops.cuh"
@@ -52,11 +54,12 @@ constexpr int kTile = 128 * D * 2;                    // an operand: 32 KB
 struct Smem {
     static constexpr int vn_at = kSharedStart;        // [2][128] value norms
     static constexpr int vm_at = vn_at + 1024;        // [2][128] the same over their power of two
-    static constexpr int vlog_at = vm_at + 1024;      // [2][4] the powers' logarithms
-    static constexpr int kexp_at = vlog_at + 32;      // [2][4] powers of two of the key norms
-    static constexpr int vmax_at = kexp_at + 32;      // [2][4] largest value norms
+    static constexpr int kn_at = vm_at + 1024;        // [2][128] factors of the tokens' products
+    static constexpr int vlog_at = kn_at + 1024;      // [2][4] the powers' logarithms
+    static constexpr int vmax_at = vlog_at + 32;      // [2][4] largest value norms
     static constexpr int bad_at = vmax_at + 32;       // [2][4] tokens of missing pages
-    static constexpr int pair_at = bad_at + 32;       // [2][2][128]: what a row's two threads tell
+    static constexpr int bare_at = bad_at + 32;       // [2][4] whether a group's factors differ
+    static constexpr int pair_at = bare_at + 32;      // [2][2][128]: what a row's two threads tell
     static constexpr int work_at = pair_at + 2048;
     static constexpr int bars_at = work_at + 64;
     static constexpr int lut_at = 32768;
@@ -129,9 +132,10 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
     float *vn_s = reinterpret_cast<float *>(at_address(raw, S::vn_at));
     float *vm_s = reinterpret_cast<float *>(at_address(raw, S::vm_at));
     float *vlog_s = reinterpret_cast<float *>(at_address(raw, S::vlog_at));
-    float *kexp_s = reinterpret_cast<float *>(at_address(raw, S::kexp_at));
+    float *kn_s = reinterpret_cast<float *>(at_address(raw, S::kn_at));
     float *vmax_s = reinterpret_cast<float *>(at_address(raw, S::vmax_at));
     uint32_t *bad_s = reinterpret_cast<uint32_t *>(at_address(raw, S::bad_at));
+    uint32_t *bare_s = reinterpret_cast<uint32_t *>(at_address(raw, S::bare_at));
     float *pair_s = reinterpret_cast<float *>(at_address(raw, S::pair_at));
 
     pdl_trigger();
@@ -280,16 +284,18 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                 const uint32_t u = done + i, st = u & 1u, phase = u >> 1;
                 const uint32_t tS = lanes + 128 * st + 64 * half, tP = lanes + 384 + 64 * st + 32 * half;
                 const int tok = (tile0 + i) * kTokens;
-                wait(B_K + st, phase);                // exponents and lost tokens
+                wait(B_K + st, phase);                // factors and lost tokens
                 wait(B_V + st, phase);                // value norms
                 if (u >= 2)
                     wait(B_PV + st, phase - 1);       // the weights' place is free
                 wait(B_S + st, phase);
                 tc_fence_after();
-                const float *ke = kexp_s + 4 * st + 2 * half, *vn = vn_s + 128 * st + 64 * half;
+                const float *kn = kn_s + 128 * st + 64 * half, *vn = vn_s + 128 * st + 64 * half;
                 const float4 vm = *reinterpret_cast<const float4 *>(vmax_s + 4 * st);
                 const uint4 bad = *reinterpret_cast<const uint4 *>(bad_s + 4 * st);
-                const bool edge = tok + kTokens > s.prefix || (bad.x | bad.y | bad.z | bad.w);
+                const uint4 bare = *reinterpret_cast<const uint4 *>(bare_s + 4 * st);
+                const bool edge = tok + kTokens > s.prefix || (bad.x | bad.y | bad.z | bad.w) ||
+                                  (bare.x | bare.y | bare.z | bare.w);
                 // tokens of this half's group k that this row sees
                 auto seen = [&](int k) -> uint32_t {
                     const int first = tok + 64 * half + 32 * k - s.prefix;   // node of its first token
@@ -315,7 +321,7 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                         for (int k = 0; k < 4; ++k) {
                             uint32_t y[16];
                             tmem_ld16(tS + 16 * k, y);
-                            const float f = qs * ke[k >> 1];
+                            const float f = qs * kn[16 * k];
                             const float lf = fmaxf(vlog_s[4 * st + 2 * half + (k >> 1)] + vlog, -60.f);
                             const float2 ff = make_float2(f, f), mm = make_float2(lf - m, lf - m);
                             float4 nv[4];
@@ -357,18 +363,20 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
 #pragma unroll 1
                         for (int k = 0; k < 4; ++k) {
                             const uint32_t v = seen(k >> 1) >> (16 * (k & 1));
-                            const float f = qs * ke[k >> 1];
                             uint32_t y[16], w[8];
                             tmem_ld16(tS + 16 * k, y);
 #pragma unroll
                             for (int j = 0; j < 16; j += 4) {
                                 const float4 n4 = *reinterpret_cast<const float4 *>(vn + 16 * k + j);
+                                const float4 k4 = *reinterpret_cast<const float4 *>(kn + 16 * k + j);
                                 const float nv[4] = {n4.x, n4.y, n4.z, n4.w};
+                                const float nk[4] = {k4.x, k4.y, k4.z, k4.w};
                                 float pw[4];
 #pragma unroll
                                 for (int h = 0; h < 4; ++h) {
                                     const bool see = (v >> (j + h)) & 1u;
-                                    const float x = see ? __uint_as_float(y[j + h]) * f : -CUDART_INF_F;
+                                    const float x =
+                                        see ? __uint_as_float(y[j + h]) * nk[h] * qs : -CUDART_INF_F;
                                     const float n1 = see ? nv[h] : 0.f, e = ex2(x - m);
                                     top = fmaxf(top, x);
                                     vtop = fmaxf(vtop, n1);
@@ -514,14 +522,22 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                 const int page3 = page_of(i + 3);
                 const float norm = cur.norm;
                 const bool valid = cur.valid, missing = cur.missing;
-                // the largest norm of the warp's 32 tokens (they are one group of scores)
+                // the largest norm of the warp's 32 tokens (one group)
                 float top = valid && norm > 0.f && norm < CUDART_INF_F ? norm : 0.f;
                 top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
                 const uint32_t lost = __ballot_sync(0xffffffffu, missing);
                 uint32_t ex = (__float_as_uint(top) >> 23) & 255u;
                 ex = ex < 28u ? 28u : (ex > 253u ? 253u : ex);
-                const __half2 by = __float2half2_rn(norm * __uint_as_float((254u - ex) << 23));
-                // K's stage is free after S, its exponents after the softmax, V's and its norms after P V
+                // keys of a group of the prefix whose norms (0 apart) are within 2^6 of one another take
+                // them along, as sums of two fp16 numbers (one alone moved a row's scores by up to 2^-12)
+                const bool bare =
+                    w > 0 || (tile0 + i) * kTokens + (row | 31) >= q.s.prefix ||
+                    !__all_sync(0xffffffffu, norm == 0.f || (norm <= top && norm * 64.f >= top &&
+                                                             norm >= 0x1p-99f));
+                const float by = norm * __uint_as_float((254u - ex) << 23);
+                const __half2 by_hi = __float2half2_rn(by);
+                const __half2 by_lo = __float2half2_rn(by - __low2float(by_hi));
+                // K's stage is free after S, its factors after the softmax, V's and its norms after P V
                 if (u >= 2)
                     wait((w == 0 ? B_S : B_PV) + st, phase - 1);
                 unsigned char *to = at_address(raw, (w == 0 ? S::k_at : S::v_at) + st * kTile);
@@ -535,13 +551,13 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                         quad<BITS, PLACED>(cur.codes, 2 * (k + h), col, v[h].x, v[h].y);
                         quad<BITS, PLACED>(cur.codes, 2 * (k + h) + 1, col, v[h].z, v[h].w);
                     }
-                    if (w == 0) {
+                    if (!bare) {
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
                             __half2 *x = reinterpret_cast<__half2 *>(&v[h]);
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                x[j] = __hmul2(x[j], by);
+                                x[j] = __hfma2(x[j], by_hi, __hmul2(x[j], by_lo));
                         }
                     }
 #pragma unroll
@@ -552,13 +568,16 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                 page1 = page2;
                 page2 = page3;
                 if (w == 0) {
-                    if (part == 0 && lane == 0) {
+                    if (part == 0) {
                         if (u >= 2)
                             wait(B_P + st, phase - 1);
-                        kexp_s[4 * st + (warp & 3)] = __uint_as_float(ex << 23);
-                        bad_s[4 * st + (warp & 3)] = lost;
-                        if (lost)
-                            atomicOr(p.err, AT_ERR_PAGE);
+                        kn_s[128 * st + row] = bare ? norm : __uint_as_float(ex << 23);
+                        if (lane == 0) {
+                            bad_s[4 * st + (warp & 3)] = lost;
+                            bare_s[4 * st + (warp & 3)] = bare;
+                            if (lost)
+                                atomicOr(p.err, AT_ERR_PAGE);
+                        }
                     }
                 } else if (part == 0) {
                     vn_s[128 * st + row] = norm;

@@ -1,0 +1,66 @@
+"""Attention over the quantised cache where norms, scores and masks reach their ends.  Oracle and
+tolerances: test_cache_gpu.py."""
+import numpy as np
+import pytest
+import torch
+
+from test_cache_gpu import BF16, F16, ROOMY, Serving, close, oq  # noqa: F401  (oq: a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def first_node_only(s):
+    """Every row sees its prefix and node 0; the other nodes are hidden from all."""
+    s.mask = np.concatenate([np.full(n, 1) for n in s.nodes]).astype(np.int64)
+    return s
+
+
+@pytest.mark.parametrize("bits,nodes,dtype", [(2, 40, BF16), (3, 9, BF16), (4, 40, BF16),
+                                              (4, 2, F16), (6, 33, BF16), (8, 40, BF16)])
+@pytest.mark.parametrize("hidden", [1e6, 1e7, 1e30, 3e38])
+def test_hidden_norms_leave_their_neighbours_alone(oq, bits, nodes, dtype, hidden):  # noqa: F811
+    """Large finite norms of hidden nodes right behind the prefix, in the same tile and the same 32
+    tokens as visible ones."""
+    s = first_node_only(Serving(oq, [37, 250, 0], [nodes] * 3, 8, 2, 128, 128, bits, 16, dtype,
+                                seed=100 + bits))
+    s.hide(hidden)
+    out = oq.oq_kv_attend(**s.gpu())
+    oq.oq_check()
+    close(out, s.want(), dtype)
+
+
+@pytest.mark.parametrize("bits,nodes,dtype", [(2, 40, BF16), (4, 40, BF16), (4, 2, F16),
+                                              (8, 40, BF16), (8, 1, BF16)])
+@pytest.mark.parametrize("roomy", [False, True])
+def test_a_loud_key_leaves_its_neighbours_alone(oq, bits, nodes, dtype, roomy):  # noqa: F811
+    """One visible key 1e6 times as long as the others: rows that it points away from have the
+    softmax of the others, rows that it points to have its value."""
+    s = Serving(oq, [37, 250], [nodes] * 2, 8, 2, 128, 128, bits, 16, dtype, seed=110 + bits,
+                columns=ROOMY // 16 if roomy else 0)
+    for b in range(2):
+        s.norms[0][s.table[b][0], :, 5] *= 1e6
+    want = s.want()
+    out = oq.oq_kv_attend(**s.gpu())
+    oq.oq_check()
+    close(out, want, dtype)
+
+
+@pytest.mark.parametrize("bits,nodes", [(4, 40), (8, 40), (4, 3)])
+def test_keys_of_all_lengths(oq, bits, nodes):  # noqa: F811
+    """Key norms spread over four orders of magnitude within every 32 tokens."""
+    s = Serving(oq, [300, 77], [nodes] * 2, 8, 2, 128, 128, bits, 16, BF16, seed=120 + bits, size=0.5)
+    s.norms[0] *= np.exp(s.rng.uniform(-9.0, 1.0, s.norms[0].shape)).astype(np.float32)
+    out = oq.oq_kv_attend(**s.gpu())
+    oq.oq_check()
+    close(out, s.want(), BF16)
+
+
+@pytest.mark.parametrize("factor", [1e-34, 1e12])
+def test_groups_of_tiny_and_large_keys(oq, factor):  # noqa: F811
+    """All keys short or long, with queries that bring the scores back: the same softmax."""
+    s = Serving(oq, [300, 77], [40, 40], 8, 2, 128, 128, 4, 16, BF16, seed=130)
+    s.norms[0] = (s.norms[0] * factor).astype(np.float32)
+    s.q = (s.q.double() / factor).to(BF16)
+    out = oq.oq_kv_attend(**s.gpu())
+    oq.oq_check()
+    close(out, s.want(), BF16)
