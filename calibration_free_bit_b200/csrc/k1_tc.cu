@@ -94,16 +94,24 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_
         ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
 
-// 32x32b.x8: 8 consecutive TMEM columns of this thread's lane (no wait).
-__device__ __forceinline__ void tmem_ld8_nowait(uint32_t taddr, uint32_t (&r)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                   "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_ld_wait() {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+// 32x32b.x8, four times: 8 consecutive TMEM columns of this thread's lane from each address, and
+// their wait in the same statement (see tmem_ld32).
+__device__ __forceinline__ void tmem_ld8x4(const uint32_t (&at)[4], uint32_t (&r)[4][8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%33];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%34];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%24, %25, %26, %27, %28, %29, %30, %31}, [%35];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=&r"(r[0][0]), "=&r"(r[0][1]), "=&r"(r[0][2]), "=&r"(r[0][3]), "=&r"(r[0][4]),
+          "=&r"(r[0][5]), "=&r"(r[0][6]), "=&r"(r[0][7]), "=&r"(r[1][0]), "=&r"(r[1][1]),
+          "=&r"(r[1][2]), "=&r"(r[1][3]), "=&r"(r[1][4]), "=&r"(r[1][5]), "=&r"(r[1][6]),
+          "=&r"(r[1][7]), "=&r"(r[2][0]), "=&r"(r[2][1]), "=&r"(r[2][2]), "=&r"(r[2][3]),
+          "=&r"(r[2][4]), "=&r"(r[2][5]), "=&r"(r[2][6]), "=&r"(r[2][7]), "=&r"(r[3][0]),
+          "=&r"(r[3][1]), "=&r"(r[3][2]), "=&r"(r[3][3]), "=&r"(r[3][4]), "=&r"(r[3][5]),
+          "=&r"(r[3][6]), "=&r"(r[3][7])
+        : "r"(at[0]), "r"(at[1]), "r"(at[2]), "r"(at[3])
+        : "memory");
 }
 
 // Store BITS words of packed codes (32 codes) at dst; alignment 4 * (BITS & -BITS) bytes.
@@ -530,27 +538,24 @@ __global__ void __launch_bounds__(kThreads, 1) k1_tc(const K1TcParams p) {
                 const int cnt = seg_chunks(g);
                 const uint32_t t_base =
                     tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(H_COLS + s * SEG_N);
-                // this warp's chunks of the segment: j_i = par + 2 i (pairs: j_i = 2 par + 4 i,
-                // with partner j_i + 1); indices are compile-time so the values stay in registers
-                uint32_t acc[4][8], acc2[2][8];
+                // this warp's chunks of the segment: j_i = par + 2 i (pairs: j_i = 2 par + 4 (i / 2),
+                // with partner j_i + 1 in i + 1); those past its end read its first chunk again.
+                // Indices are compile-time so the values stay in registers.
+                uint32_t acc[4][8], at[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int j = pairs ? 2 * par + 4 * i : par + 2 * i;
-                    if ((!pairs || i < 2) && j < cnt) {               // warp-uniform
-                        tmem_ld8_nowait(t_base + (uint32_t)(8 * j), acc[i]);
-                        if (pairs && i < 2)
-                            tmem_ld8_nowait(t_base + (uint32_t)(8 * (j + 1)), acc2[i & 1]);
-                    }
+                    const int j = pairs ? 2 * par + 4 * (i / 2) + (i & 1) : par + 2 * i;
+                    at[i] = t_base + (uint32_t)(j < cnt ? 8 * j : 0);   // warp-uniform
                 }
-                tmem_ld_wait();
+                tmem_ld8x4(at, acc);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(tempty(s));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int j = pairs ? 2 * par + 4 * i : par + 2 * i;
-                    if (!((!pairs || i < 2) && j < cnt))
+                    const int j = pairs ? 2 * par + 2 * i : par + 2 * i;
+                    if ((pairs && (i & 1)) || j >= cnt)
                         continue;
                     const int c = g * SEG + j;
                     // code tile layout [position][token]: 8 bytes per rotated position, the
@@ -562,12 +567,12 @@ __global__ void __launch_bounds__(kThreads, 1) k1_tc(const K1TcParams p) {
                         for (int t = 0; t < NT; ++t)
                             z[t] = __uint_as_float(acc[i][t]);
                         dst[0] = codes8(z, m);
-                    } else if (i < 2) {
+                    } else {
                         float z2[NT];
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
                             const float u = __uint_as_float(acc[i][t]);
-                            const float v = __uint_as_float(acc2[i & 1][t]);
+                            const float v = __uint_as_float(acc[i | 1][t]);
                             z[t] = u + v;
                             z2[t] = u - v;
                         }
