@@ -499,7 +499,7 @@ __global__ void __maxnreg__(96) k1_rotquant(const K1Params p) {
 #pragma unroll
                 for (int j = 0; j < kU; ++j) {
                     const long long i = c0 + g + (long long)j * GTP;
-                    wv[j] = i < dcnt ? __ldg(wc + i) : 0u;
+                    wv[j] = i < dcnt ? wc[i] : 0u;
                 }
 #pragma unroll
                 for (int j = 0; j < kU; ++j) {

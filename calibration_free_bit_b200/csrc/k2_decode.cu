@@ -66,22 +66,23 @@ __device__ __forceinline__ uint4 decode_group(const uint32_t *tab32, uint64_t v)
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// Plain loads: the kernel that writes the codes may still run when this one starts (it waits, but
+// data behind the non-coherent path has to stay the same for a kernel's whole life).
 template <int BITS>
 __device__ __forceinline__ uint64_t load_group(const uint8_t *codes, long long g) {
     const uint8_t *src = codes + g * BITS;
     if constexpr (BITS == 2)
-        return __ldg(reinterpret_cast<const unsigned short *>(src));
+        return *reinterpret_cast<const unsigned short *>(src);
     else if constexpr (BITS == 4)
-        return __ldg(reinterpret_cast<const unsigned int *>(src));
+        return *reinterpret_cast<const unsigned int *>(src);
     else if constexpr (BITS == 8)
-        return __ldg(reinterpret_cast<const unsigned long long *>(src));
+        return *reinterpret_cast<const unsigned long long *>(src);
     else if constexpr (BITS == 6)                     // 6 bytes at an even address
-        return (uint64_t)__ldg(reinterpret_cast<const unsigned short *>(src)) |
-               ((uint64_t)__ldg(reinterpret_cast<const unsigned short *>(src + 2)) << 16) |
-               ((uint64_t)__ldg(reinterpret_cast<const unsigned short *>(src + 4)) << 32);
+        return (uint64_t)*reinterpret_cast<const unsigned short *>(src) |
+               ((uint64_t)*reinterpret_cast<const unsigned short *>(src + 2) << 16) |
+               ((uint64_t)*reinterpret_cast<const unsigned short *>(src + 4) << 32);
     else
-        return (uint64_t)__ldg(src) | ((uint64_t)__ldg(src + 1) << 8) |
-               ((uint64_t)__ldg(src + 2) << 16);
+        return (uint64_t)src[0] | ((uint64_t)src[1] << 8) | ((uint64_t)src[2] << 16);
 }
 
 // SYM (BITS == 4 only): decode with byte permutes instead of the shared table.

@@ -99,7 +99,7 @@ __device__ __forceinline__ void decode_weight_share(const FusedStepParams &p, in
 #pragma unroll
         for (int j = 0; j < kDecBatch; ++j) {
             const long long i = b + j * 32 + lane;
-            wv[j] = i < hi ? __ldg(p.wcodes + i) : 0u;
+            wv[j] = i < hi ? p.wcodes[i] : 0u;
         }
 #pragma unroll
         for (int j = 0; j < kDecBatch; ++j) {

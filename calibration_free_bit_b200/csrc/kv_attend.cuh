@@ -247,7 +247,7 @@ __device__ __forceinline__ void walk_tiles(const KvAttendParams &p, uint32_t col
     const uint32_t k_off = order(g) * S::row_bytes + c * S::k_bytes, n_off = R::kn_at + 4 * order(g);
     const uint32_t v_off = R::rows + c * S::row_bytes;
     auto place = [&](int t) -> int {              // a tile's page
-        return t < last ? __ldg(table + ((t << 4) >> p.c.page_log2)) : -1;
+        return t < last ? table[(t << 4) >> p.c.page_log2] : -1;
     };
     __syncwarp();
     for (int k = 0; k < SLOTS; ++k) {

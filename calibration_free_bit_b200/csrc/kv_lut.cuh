@@ -182,25 +182,27 @@ __device__ __forceinline__ void mixed(uint32_t (&x)[W], uint32_t (&y)[W]) {
     }
 }
 
-// W words from global memory, in the widest loads that the address allows (ALIGN bytes).
+// W words of a cache's codes, in the widest loads that the address allows (ALIGN bytes).  Plain loads:
+// the kernel that writes them may still run when the one that reads them starts (it waits, but data
+// behind the non-coherent path has to stay the same for a kernel's whole life).
 template <int W, int ALIGN>
 __device__ __forceinline__ void load_words(uint32_t (&w)[W], const uint8_t *p) {
     if constexpr (ALIGN % 16 == 0 && W % 4 == 0) {
 #pragma unroll
         for (int i = 0; i < W; i += 4) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p + 4 * i));
+            const uint4 v = *reinterpret_cast<const uint4 *>(p + 4 * i);
             w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
         }
     } else if constexpr (ALIGN % 8 == 0 && W % 2 == 0) {
 #pragma unroll
         for (int i = 0; i < W; i += 2) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p + 4 * i));
+            const uint2 v = *reinterpret_cast<const uint2 *>(p + 4 * i);
             w[i] = v.x, w[i + 1] = v.y;
         }
     } else {
 #pragma unroll
         for (int i = 0; i < W; ++i)
-            w[i] = __ldg(reinterpret_cast<const uint32_t *>(p + 4 * i));
+            w[i] = *reinterpret_cast<const uint32_t *>(p + 4 * i);
     }
 }
 

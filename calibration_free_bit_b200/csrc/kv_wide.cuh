@@ -481,7 +481,7 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
             };
             auto page_of = [&](int i) -> int {
                 const int tok = (tile0 + i) * kTokens + row;
-                return i < n && tok < total ? __ldg(table + (tok >> p.c.page_log2)) : -1;
+                return i < n && tok < total ? table[tok >> p.c.page_log2] : -1;
             };
             auto row_of = [&](int i, int page) -> long long {
                 return (((long long)page * p.c.kv_heads + kvh) << p.c.page_log2) +
@@ -502,7 +502,7 @@ attend_wide(const KvAttendParams p, const uint4 *r_img, const KvAttendSpace ws) 
                     const long long at = row_of(i, page);
                     load_words<words, own>(
                         to.codes, pick(p.c.codes, w) + at * (D * BITS / 8) + part * own);
-                    to.norm = __ldg(pick(p.c.norms, w) + at);
+                    to.norm = pick(p.c.norms, w)[at];
                 } else {
 #pragma unroll
                     for (int k = 0; k < words; ++k)

@@ -37,3 +37,18 @@ def test_a_load_of_tensor_memory_waits_in_its_own_statement(path):
         if "tcgen05.ld" in s:
             assert "tcgen05.wait::ld" in s, s[:80]
             assert '"memory"' in s, s[:80]
+
+
+# what a handle uploads before its first launch: tables, matrices, boundaries
+CONSTANT = ("reinterpret_cast<const uint2 *>(src) + (i >> 3)", "src + (i >> 3)", "r_img + ",
+            "reinterpret_cast<const uint4 *>(p.tbl) + ", "p.bounds + ", "p.wdec_tab + ")
+
+
+@pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
+def test_only_constant_tables_take_the_non_coherent_path(path):
+    """Kernels start while the one before them still runs, so codes, norms and page tables may
+    change during the life of a kernel that reads them (after its wait): plain loads."""
+    text = re.sub(r"//[^\n]*", "", open(path).read())
+    for m in re.finditer(r"__ldg\(\s*", text):
+        assert text[m.end():].startswith(CONSTANT), text[m.start():m.start() + 60]
+    assert not re.search(r"ld\.global(\.\w+)*\.nc|__restrict__|ldlu|__ldcv", text)
