@@ -467,6 +467,8 @@ int oq_kv_attend(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cach
         (rc = check_out_rows(who, "out", out, out_stride, dtype, (long long)q_heads * cache->d)) !=
             OQ_OK)
         return rc;
+    if (q == out && q_stride != out_stride)
+        return fail(OQ_EINVAL, "%s: in place, both strides must be the same", who);
     if (!q_start || !prefix || !page_table)
         return fail(OQ_EINVAL, "%s: null q_start, prefix or page_table", who);
     if (((reinterpret_cast<uintptr_t>(q_start) | reinterpret_cast<uintptr_t>(prefix) |

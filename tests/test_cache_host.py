@@ -204,3 +204,10 @@ def test_oracle_rotation_and_packing():
 @pytest.mark.parametrize("page,width", [(16, (1 << 27) - 15), (1024, 1 << 21), (16, 1 << 27)])
 def test_attend_refuses_tables_of_too_many_tokens(page, width):
     assert _attend(cache=dict(page=page), width=width) == oq.OQ_EINVAL
+
+
+def test_attend_in_place_wants_one_stride():
+    """With two strides a row of out lies on another row's query."""
+    assert _attend(qs=512, os=640) == oq.OQ_EINVAL
+    assert "in place" in oq.lib().oq_last_error().decode()
+    assert _attend(qs=640, os=512) == oq.OQ_EINVAL
