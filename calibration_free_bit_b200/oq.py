@@ -312,7 +312,7 @@ def _rows(t: torch.Tensor, what: str, heads=None, d=None, dtype=None):
         _bad(f"{what} has dtype {t.dtype}: expected {dtype}")
     n, h, e = t.shape
     sn, sh, se = t.stride()
-    if (e > 1 and se != 1) or (h > 1 and sh != e):
+    if n > 0 and ((e > 1 and se != 1) or (h > 1 and sh != e)):
         _bad(f"{what}: the heads of a token must be contiguous")
     return sn if n > 1 else h * e
 
@@ -386,8 +386,54 @@ def oq_build_rope(rot_dim: int, layout: str = "half", theta: float = 10000.0,
 def oq_apply_rope(rope: Rope, x: torch.Tensor, positions: torch.Tensor, k=None, out=None,
                   k_out=None, inverse: bool = False, stream=None):
     """Rotary positions of x [T, heads, d] and, in the same launch, of k [T, k_heads, d] (fp32,
-    bf16 or fp16; token stride free); positions int64 [T].  inverse=True applies the transpose
-    (gradients).  Returns out, or (out, k_out); out=x works in place."""
+    bf16 or fp16; token stride free); positions int64 [T].  inverse=True applies the transpose, which
+    is also what a gradient goes back through: inputs that require one give outputs that do.  Returns
+    out, or (out, k_out); out=x works in place (out and k_out only without gradients)."""
+    if torch.is_grad_enabled() and (
+            x.requires_grad or (k is not None and k.requires_grad) or
+            (out is not None and out.requires_grad) or (k_out is not None and k_out.requires_grad)):
+        if out is not None or k_out is not None:
+            _bad("oq_apply_rope: out and k_out do not go with tensors that require a gradient")
+        return _Turn.apply(rope, x, positions, k, inverse, stream)
+    return _turn(rope, x, positions, k, out, k_out, inverse, stream)
+
+
+class _Turn(torch.autograd.Function):
+    """oq_apply_rope with its transpose as the way back (itself differentiable)."""
+
+    @staticmethod
+    def forward(ctx, rope, x, positions, k, inverse, stream):
+        ctx.rope, ctx.inverse = rope, inverse
+        ctx.save_for_backward(positions)
+        ctx.set_materialize_grads(False)
+        y = _turn(rope, x, positions, k, None, None, inverse, stream)
+        if k is not None:
+            ctx.mark_non_differentiable(*(t for t, needs in zip(y, (x.requires_grad, k.requires_grad))
+                                          if not needs))
+        return y
+
+    @staticmethod
+    def backward(ctx, gy, gk=None):
+        g = [None if t is None else _dense(t) for t in (gy, gk)]
+        if g[0] is not None or g[1] is not None:
+            back = oq_apply_rope(ctx.rope, g[0] if g[0] is not None else g[1], ctx.saved_tensors[0],
+                                 g[1] if g[0] is not None else None, inverse=not ctx.inverse)
+            if g[0] is None:
+                g[1] = back
+            elif g[1] is None:
+                g[0] = back
+            else:
+                g = back
+        return None, g[0], None, g[1], None, None
+
+
+def _dense(t: torch.Tensor) -> torch.Tensor:
+    """t as a call takes it: contiguous, at a multiple of 16 bytes."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _turn(rope, x, positions, k, out, k_out, inverse, stream):
     xs = _rows(x, "x")
     T, heads, d = x.shape
     if out is None:
@@ -461,7 +507,7 @@ class KVCache:
 def oq_kv_write(r: RPBH, c: Codebook, cache: KVCache, k: torch.Tensor, v: torch.Tensor,
                 slots: torch.Tensor, stream=None):
     """Store k, v [T, kv_heads, d] (fp32, bf16 or fp16; token stride free) as codes in the slots
-    (int64 [T]; -1: skip; no other slot twice)."""
+    (int64 [T]; -1: skip; no other slot twice).  No gradient goes through the cache's calls."""
     ks = _rows(k, "k", cache.kv_heads, cache.d)
     vs = _rows(v, "v", cache.kv_heads, cache.d, k.dtype)
     T = k.shape[0]

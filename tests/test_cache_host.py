@@ -211,3 +211,15 @@ def test_attend_in_place_wants_one_stride():
     assert _attend(qs=512, os=640) == oq.OQ_EINVAL
     assert "in place" in oq.lib().oq_last_error().decode()
     assert _attend(qs=640, os=512) == oq.OQ_EINVAL
+
+
+def test_apply_rope_refuses_outputs_with_gradients():
+    """Written outputs would lose the gradient in silence."""
+    x, pos, rope = torch.zeros(4, 2, 128), torch.zeros(4, dtype=torch.int64), oq.oq_build_rope(128)
+    g = torch.zeros(4, 2, 128, requires_grad=True)
+    for kw in (dict(x=g, out=x), dict(x=x, k=g, out=x, k_out=x), dict(x=x, k=g, k_out=x),
+               dict(x=x, out=g)):
+        with pytest.raises(oq.OQError, match="gradient"):
+            oq.oq_apply_rope(rope, positions=pos, **kw)
+        with torch.no_grad(), pytest.raises(oq.OQError, match="CPU"):     # (and then needs a GPU)
+            oq.oq_apply_rope(rope, positions=pos, **kw)
