@@ -120,11 +120,6 @@ int upload_ent(oq_rpbh *r, int dev) {
     return upload(r->mu, &r->dev_ent16[dev], r->ent16, "upload rotation entries");
 }
 
-}  // namespace
-
-namespace oq {
-namespace host {
-
 // The fp16 decode table of the cache's kernels: 32-bit words of two centroids.
 //   bits 2: entry e (a byte, four codes) = two words; bits 3, 4: entry e (two codes) = one word,
 //   the lower code in the low half; bits 6, 8: entry e (one code) in the low half, what fp16 leaves
@@ -163,23 +158,34 @@ void build_kv_lut(oq_codebook *cb) {
     uint16_t lut[256];
     for (int i = 0; i < L; ++i)
         lut[i] = to_half_bits(cb->kv_alpha * cb->c[i]);
-    cb->kv_lut.clear();
+    std::vector<uint32_t> out;
     const int b = cb->bits;
     const int entries = b == 6 || b == 3 ? 64 : 256;
     for (int e = 0; e < entries; ++e) {
         if (b == 2)
             for (int k = 0; k < 2; ++k)
-                cb->kv_lut.push_back(lut[(e >> (4 * k)) & 3] |
-                                     (uint32_t)lut[(e >> (4 * k + 2)) & 3] << 16);
+                out.push_back(lut[(e >> (4 * k)) & 3] |
+                              (uint32_t)lut[(e >> (4 * k + 2)) & 3] << 16);
         else if (b <= 4)
-            cb->kv_lut.push_back(lut[e & (L - 1)] | (uint32_t)lut[e >> b] << 16);
+            out.push_back(lut[e & (L - 1)] | (uint32_t)lut[e >> b] << 16);
         else                                      // and what fp16 leaves of it
-            cb->kv_lut.push_back(lut[e] | (uint32_t)to_half_bits(cb->kv_alpha * cb->c[e] - value(lut[e])) << 16);
+            out.push_back(lut[e] | (uint32_t)to_half_bits(cb->kv_alpha * cb->c[e] - value(lut[e])) << 16);
     }
+    cb->kv_lut = std::move(out);
 }
 
-}  // namespace host
-}  // namespace oq
+// The decode table on the current device, made at a codebook's first use with a cache (most
+// codebooks never see one, and the search for kv_alpha takes longer than the rest of them).
+int decode_table(oq_codebook *cb, int dev) {
+    {
+        std::lock_guard<std::mutex> lk(cb->mu);
+        if (cb->kv_lut.empty())
+            build_kv_lut(cb);
+    }
+    return upload(cb->mu, &cb->dev_kv_lut[dev], cb->kv_lut, "upload decode table");
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -412,10 +418,10 @@ int oq_kv_read(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache,
         return rc;
     if (dtype != OQ_F32 &&
         ((rc = rotation_matrix(rw, RMAT_F16_T, dev, &p.r_img)) != OQ_OK ||
-         (rc = upload(cw->mu, &cw->dev_kv_lut[dev], cw->kv_lut, "upload decode table")) != OQ_OK))
+         (rc = decode_table(cw, dev)) != OQ_OK))
         return rc;
     p.lut = cw->dev_kv_lut[dev];
-    p.alpha_inv = (float)(1.0 / c->kv_alpha);
+    p.alpha_inv = dtype == OQ_F32 ? 1.f : (float)(1.0 / c->kv_alpha);   // (rows kernel: no table)
     p.y[0] = k;
     p.y[1] = v;
     p.y_stride[0] = k_stride;
@@ -483,7 +489,7 @@ int oq_kv_attend(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cach
     oq_rpbh *rw = const_cast<oq_rpbh *>(r);
     oq_codebook *cw = const_cast<oq_codebook *>(c);
     if ((rc = upload_ent(rw, dev)) != OQ_OK ||
-        (rc = upload(cw->mu, &cw->dev_kv_lut[dev], cw->kv_lut, "upload decode table")) != OQ_OK)
+        (rc = decode_table(cw, dev)) != OQ_OK)
         return rc;
     p.q = q;
     p.out = out;

@@ -42,7 +42,8 @@ struct oq_codebook {
     uint32_t *dev_dec[oq::kMaxDevices] = {};
     std::vector<float> cent32;                    // unit centroids, then boundaries, fp32 (the cache)
     uint32_t *dev_cent32[oq::kMaxDevices] = {};
-    // the cache's fp16 decode table (oq_cache.cpp, build_kv_lut): centroids times kv_alpha
+    // the cache's fp16 decode table (oq_cache.cpp, decode_table: made at its first use): centroids
+    // times kv_alpha
     double kv_alpha = 1.0;
     std::vector<uint32_t> kv_lut;
     uint32_t *dev_kv_lut[oq::kMaxDevices] = {};
@@ -74,7 +75,6 @@ struct DeviceInfo {
     uint32_t *gelu_tab = nullptr;     // the fused GELU's table (oq::gelu_table_image)
 };
 uint16_t to_half_bits(double x);        // IEEE binary16, to nearest even
-void build_kv_lut(oq_codebook *cb);      // oq_cache.cpp
 
 // The current device, checked once to be sm_100.
 int current_device(int *dev_out, DeviceInfo **info_out);

@@ -1044,7 +1044,6 @@ int oq_lloyd_max_marginal(int d, int bits, int marginal, oq_codebook **out) {
         if (i + 1 < L)                            // (the middle one is 0)
             cb->cent32[L + i] = std::fabs(cb->t[i]) < 1e-12 ? 0.f : (float)cb->t[i];
     }
-    build_kv_lut(cb);
     if (!build_grid(cb)) {
         delete cb;
         return fail(OQ_EINVAL, "%s: could not build the quantizer grid", who);
