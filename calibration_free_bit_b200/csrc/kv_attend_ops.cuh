@@ -64,7 +64,8 @@ __device__ __forceinline__ uint32_t half2_rest(float a, float b, uint32_t hi) {
 // A row's reference m is raised only when a score passes it by kSlack (in powers of two), so most
 // steps need no reduction over lanes; weights reach 2^kSlack kWeightScale = 2^14 in fp16.
 constexpr float kSlack = 8.0f, kWeightScale = 64.0f;
-constexpr float kNone = -1e30f;                      // reference of a row that has seen nothing
+constexpr float kNone = -3.402823466e38f;             // reference of a row that has seen nothing: no
+                                                     // finite score is below it
 
 // The power of two above a norm, with room for a quarter more, in [2^-100, 2^127].
 __device__ __forceinline__ float norm_scale(float v) {

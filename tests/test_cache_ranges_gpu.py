@@ -64,3 +64,16 @@ def test_groups_of_tiny_and_large_keys(oq, factor):  # noqa: F811
     out = oq.oq_kv_attend(**s.gpu())
     oq.oq_check()
     close(out, s.want(), BF16)
+
+
+@pytest.mark.parametrize("d,nodes", [(128, 1), (128, 3), (256, 2), (128, 40)])
+@pytest.mark.parametrize("roomy", [False, True])
+def test_scores_far_below_zero(oq, d, nodes, roomy):  # noqa: F811
+    """Rows that see one token have its value, however low its score (here down to -1e34)."""
+    s = Serving(oq, [0] * 5, [nodes] * 5, 8, 2, d, 128, 4, 16, BF16, seed=140, size=1e16,
+                columns=ROOMY // 16 if roomy else 0)
+    s.norms[0] = (s.norms[0] * 1e16).astype(np.float32)
+    s.mask = np.concatenate([1 << np.arange(n) for n in s.nodes]).astype(np.int64)
+    out = oq.oq_kv_attend(**s.gpu())
+    oq.oq_check()
+    close(out, s.want(), BF16)
