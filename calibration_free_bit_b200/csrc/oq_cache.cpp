@@ -13,6 +13,7 @@ using namespace oq::host;
 namespace {
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
+constexpr double kLog2e = 1.4426950408889634073599246810019;
 
 int elem_size(int dtype) { return dtype == OQ_F32 ? 4 : 2; }
 
@@ -465,8 +466,8 @@ int oq_kv_attend(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cach
     if (table_width < 1 || ((long long)table_width << p.c.page_log2) > 0x7fffff00ll)
         return fail(OQ_EINVAL, "%s: table_width = %d must be positive, and hold at most 2^31 - 256 "
                                "tokens", who, table_width);
-    if (!(scale > 0.0) || !std::isfinite(scale))
-        return fail(OQ_EINVAL, "%s: scale must be positive and finite", who);
+    if (!(scale > 0.0) || !std::isfinite((float)(scale * kLog2e)))
+        return fail(OQ_EINVAL, "%s: scale must be positive and, times log2(e), finite in fp32", who);
     if (q_rows == 0 || B == 0)
         return OQ_OK;
     if ((rc = check_rows(who, "q", q, q_stride, dtype)) != OQ_OK ||
@@ -509,7 +510,7 @@ int oq_kv_attend(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cach
     p.lut = cw->dev_kv_lut[dev];
     p.h = r->h;
     const double unit = 1.0 / (std::sqrt((double)r->d * r->h) * c->kv_alpha);
-    p.qk_scale = (float)(scale * 1.4426950408889634 * unit);
+    p.qk_scale = (float)(scale * kLog2e * unit);
     p.o_scale = (float)unit;
     cudaStream_t st = (cudaStream_t)stream;
     std::string why;

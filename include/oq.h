@@ -352,7 +352,7 @@ int oq_kv_read(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache,
  * prefix and the nodes j with bit j of tree_mask[row] set (its ancestors and itself, in any
  * order); with tree_mask = NULL the nodes up to its own, so one node a sequence is a plain
  * decoding step.  out = sum_t p_t v_hat_t, p the softmax of scale * q . k_hat_t over the tokens it
- * sees; a row that sees nothing gives zeros.  Query head i reads key head i / (q_heads/kv_heads).
+ * sees; a row that sees nothing gives zeros.  scale > 0, and scale * log2(e) finite in fp32.  Query head i reads key head i / (q_heads/kv_heads).
  * q, out: device, [q_rows, q_heads, d] of dtype (OQ_BF16 or OQ_F16); out = q with the same stride
  * works in place, any other overlap is not allowed.  q_start: int32 [B+1];
  * prefix: int32 [B]; page_table: int32 [B, table_width] (entries past a sequence's last page are

@@ -238,3 +238,8 @@ def test_a_codebook_costs_no_cache():
             times.append(time.perf_counter() - t)
         return min(times)
     assert best(4) <= 0.3 * best(6)
+
+
+@pytest.mark.parametrize("scale", [1e300, 3.4e38, float("inf"), -1.0])
+def test_attend_refuses_scales_past_fp32(scale):
+    assert _attend(scale=scale) == oq.OQ_EINVAL
