@@ -81,6 +81,14 @@ int check_cache(const char *who, const oq_rpbh *r, const oq_codebook *c, const o
     return OQ_OK;
 }
 
+// (tiles of 128 rows are counted in 32 bits; rows may be one row for all tokens, so memory is no limit)
+int check_tokens(const char *who, int T, int heads) {
+    if (T < 0 || (long long)T * heads > 1ll << 36)
+        return fail(OQ_EINVAL, "%s: T = %d tokens of %d heads: negative, or over 2^36 rows", who, T,
+                    heads);
+    return OQ_OK;
+}
+
 int check_slots(const char *who, const int64_t *slots) {
     if (!slots || (reinterpret_cast<uintptr_t>(slots) & 7u))
         return fail(OQ_EINVAL, "%s: slots must be a non-null, 8-byte aligned pointer", who);
@@ -340,8 +348,8 @@ int oq_kv_write(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache
         return rc;
     if (dtype != OQ_F32 && dtype != OQ_BF16 && dtype != OQ_F16)
         return fail(OQ_EINVAL, "%s: dtype must be OQ_F32, OQ_BF16 or OQ_F16", who);
-    if (T < 0)
-        return fail(OQ_EINVAL, "%s: negative row count %d", who, T);
+    if ((rc = check_tokens(who, T, cache->kv_heads)) != OQ_OK)
+        return rc;
     if (T == 0)
         return OQ_OK;
     if ((rc = check_rows(who, "k", k, k_stride, dtype)) != OQ_OK ||
@@ -399,8 +407,8 @@ int oq_kv_read(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache,
         return rc;
     if (dtype != OQ_F32 && dtype != OQ_BF16 && dtype != OQ_F16)
         return fail(OQ_EINVAL, "%s: dtype must be OQ_F32, OQ_BF16 or OQ_F16", who);
-    if (T < 0)
-        return fail(OQ_EINVAL, "%s: negative row count %d", who, T);
+    if ((rc = check_tokens(who, T, cache->kv_heads)) != OQ_OK)
+        return rc;
     if (T == 0)
         return OQ_OK;
     const long long row = (long long)cache->kv_heads * cache->d;

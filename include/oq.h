@@ -332,7 +332,7 @@ typedef struct {
  * token (padding); the others must differ from one another (a slot named twice ends up with
  * either token's rows or a mixture of them; no other slot is touched).  A slot outside the cache
  * is skipped and reported by oq_check.  A row with a NaN or infinity, or whose squares pass fp32,
- * gets a norm that is not finite; no other row feels it.  T = 0 is a no-op.
+ * gets a norm that is not finite; no other row feels it.  T = 0 is a no-op, T * kv_heads at most 2^36.
  * Errors: OQ_EINVAL, OQ_EUNSUPPORTED, OQ_ECUDA. */
 int oq_kv_write(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache, const void *k,
                 long long k_stride, const void *v, long long v_stride, int dtype, int T,

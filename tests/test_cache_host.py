@@ -243,3 +243,12 @@ def test_a_codebook_costs_no_cache():
 @pytest.mark.parametrize("scale", [1e300, 3.4e38, float("inf"), -1.0])
 def test_attend_refuses_scales_past_fp32(scale):
     assert _attend(scale=scale) == oq.OQ_EINVAL
+
+
+@pytest.mark.parametrize("T,heads", [((1 << 26) + 1, 1024), (1 << 30, 1024), ((1 << 31) - 1, 33)])
+@pytest.mark.parametrize("dtype", [oq.OQ_BF16, oq.OQ_F32])
+def test_cache_refuses_more_rows_than_it_counts(T, heads, dtype):
+    """(One row for all tokens, stride 0, makes such calls possible.)"""
+    row = heads * 128
+    assert _write(cache=dict(heads=heads), T=T, dtype=dtype, ks=0, vs=0) == oq.OQ_EINVAL
+    assert _read(cache=dict(heads=heads), T=T, dtype=dtype, ks=row, vs=row) == oq.OQ_EINVAL
