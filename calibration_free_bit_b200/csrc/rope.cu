@@ -164,7 +164,7 @@ cudaError_t run(const RopeParams &p, int layout, cudaStream_t st, int num_sms) {
         tokens = p.T / (2 * num_sms);
     if (tokens < 1)
         tokens = 1;
-    const dim3 grid((p.T + tokens - 1) / tokens);
+    const dim3 grid((p.T - 1) / tokens + 1);             // (T may be the largest int)
     const size_t smem = (size_t)tokens * half * sizeof(float2);
     constexpr int V = Vec<E>::n;
     const Divide turned((layout == OQ_ROPE_HALF ? half : p.rot) / V);

@@ -113,3 +113,22 @@ def test_gradients_on_a_stream_and_in_a_captured_graph(oq):  # noqa: F811
     torch.cuda.synchronize()
     assert torch.equal(got, want)
     oq.oq_check()
+
+
+def test_the_most_tokens(oq):  # noqa: F811
+    """2^31 - 1 tokens of one head of 16, one row for all of them (86 GB of outputs and positions)."""
+    T = 2 ** 31 - 1
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 100 * 2 ** 30:
+        pytest.skip("needs 100 GB of free memory")
+    rope = oq.oq_build_rope(16)
+    x = torch.randn(1, 1, 16, generator=gen(0)).bfloat16().cuda()
+    pos = torch.arange(T, device="cuda")
+    y = oq.oq_apply_rope(rope, x.expand(T, 1, 16), pos)
+    oq.oq_check()
+    for at in (0, 1, 12345, 2 ** 30, T - 3000):
+        n = min(3000, T - at)
+        want = oq.oq_apply_rope(rope, x.expand(n, 1, 16), pos[at:at + n].clone())
+        assert torch.equal(y[at:at + n], want)
+    del y, pos
+    torch.cuda.empty_cache()
