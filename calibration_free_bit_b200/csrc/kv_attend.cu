@@ -16,7 +16,9 @@ constexpr int kJoinWarps = 4;
 // with 31 nodes, 15872 rows 63 and 84.
 constexpr int kManyRows = 4096;
 // Tiles of 16 tokens, over all segments, up to which clusters take a call: tiles of 8 rows of 128 (two
-// CTAs an SM), others.  Clusters and workers, us, bf16: 8 key heads, a sequence of 4096 tokens 11 and
+// CTAs an SM), others.  They are counted by what the page tables can hold, since lengths are on the
+// device: the figures are of tables as wide as the lengths, and a sequence of 4096 tokens in a table for
+// 131072 is a call for workers (18.9 us).  Clusters and workers, us, bf16: 8 key heads, a sequence of 4096 tokens 11 and
 // 19, 32768 30 and 46, 65536 51 and 55, 131072 93 and 74, 16 of 4000 tokens 29 and 33; with 16 rows
 // 16000 tokens 27 and 32, 32000 44 and 37, 4 sequences of 4000 27 and 25.
 constexpr long long kNearTiles = 32768, kNearOther = 8192;

@@ -274,7 +274,10 @@ __device__ __forceinline__ bool next_piece(const KvAttendParams &p, Walk &w, Pie
 
 // The forms: tiles of many rows (kv_wide.cuh) and of 8 NT (kv_attend.cuh).  `extra`, us: 16 sequences with
 // 61 nodes 165, 160 and 162 with 2, 3 and 4; 64 sequences of single tokens 87.3, 87.0 and 87.0 with 3, 4
-// and 6, 8 sequences of 40 key heads 45.8, 47.4 and 47.5.
+// and 6, 8 sequences of 40 key heads 45.8, 47.4 and 47.5.  The small tiles' 4 is not the fastest there: it
+// is what a worker has at least (kv_attend.cu, `least`), and in a small call, where each worker has just
+// that, a sequence whose units are a multiple of 4 is then cut at the same places, and rounded alike,
+// whether or not another beside it is skipped.
 struct WideForm {
     static constexpr int tokens = 128, rows = 128, extra = 3;
 };

@@ -140,7 +140,8 @@ __device__ __forceinline__ void tmem_ld1(uint32_t at, uint32_t &r) {
 }
 
 // Few codes are far apart, so a wrong one beside a boundary shows in fp16 rows; with 8 bits it is off by
-// less than their rounding.
+// less than their rounding, and is left (a few of a million, which a smaller call, kv_cache.cu, may take
+// the other way).
 template <int BITS> constexpr bool kLook = BITS <= 6;
 
 template <int D, int BITS, bool BF16>

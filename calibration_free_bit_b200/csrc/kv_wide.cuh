@@ -5,11 +5,12 @@
 // One CTA per SM walks a contiguous range of units.  For a piece it rotates the 128 queries (one
 // tcgen05.mma with the rotation's dense operand) and keeps them as the A operand in shared memory;
 // then, per unit, decoder warps turn the codes of 128 tokens into the fp16 operands K (elements
-// contiguous, K-major) and V (the same layout, read as N-major), half a row a thread; S = Q K^T goes
-// to tensor memory, two units' in turn; two softmax threads own a row, one for either half of the
-// tokens, and put the weights, the A operand of O += P V, beside S, so that the next products do not
-// wait for the last.  They take the weights with the row's reference as it is and look for a larger
-// score on the way; only if a row of the two warps has passed it (kSlack) is a unit done again.
+// contiguous, K-major) and V (the same layout, read as N-major), a row a thread (of 6 and 8 bits half
+// a row); S = Q K^T goes to tensor memory, two units' in turn; two softmax threads own a row, one for
+// either half of the tokens, and put the weights, the A operand of O += P V, beside S, so that the next
+// products do not wait for the last.  They take the weights with the row's reference as it is and look
+// for a larger score on the way; only if a row of the two warps has passed it (kSlack) is a unit done
+// again.
 // A unit needs about a thousand cycles each of shared memory (at 4 bits 16384 lookups of two codes, 64
 // KB of operands stored), of exponentials (16384) and of issue slots, and half of that of the tensor
 // cores; it takes 4300, since none of its steps (decode, S, softmax, P V) has warps enough to hide its
@@ -21,7 +22,11 @@
 //     a maximum over raw products.  Of any other group (with nodes, a loud key, a NaN) the operand is
 //     bare centroids, and the norms multiply the products in fp32, token by token (a product is below
 //     2^12, and the cache's write stores no norm above 2^64).  Value norms enter with the weights, a row
-//     at a time.  So what a row does not see never reaches it, nor what stands beside it.
+//     at a time.  So what a row does not see never reaches it, nor what stands beside it.  (Trees of 31
+//     nodes as above take 416 us when all groups are bare, their norms spread over e^+-2 rms.)
+//   - Queries, products of centroid and norm, and weights are one fp16 number each: errors of 1.8e-3 to
+//     1.9e-3 of an output's length, of which its own rounding to bf16 is 1.65e-3.  A weight is resolved
+//     down to 2^-31 of the longest value that its row sees.
 #pragma once
 
 #include "kv_attend_ops.cuh"
@@ -39,8 +44,9 @@ using kvops::prmt;
 namespace wide {
 
 constexpr int kRows = 128, kTokens = 128, D = 128;
-// Warps: softmax, eight decoders each for keys and values, and one that issues the products.  (25 in
-// all leave 80 registers a thread.)
+// Warps: softmax, four or eight decoders each for keys and values, and one that issues the products.
+// (17 in all leave 96 registers a thread and 25 leave 72, since one scheduler has the odd warp: at 72,
+// with 6 and 8 bits, 76 bytes a thread are spilled.)
 constexpr int kSoftWarps = 8;
 template <int BITS> struct Shape {
     static constexpr int parts = BITS > 4 ? 2 : 1;    // decoder threads a row

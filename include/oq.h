@@ -273,10 +273,11 @@ int oq_debug_arm_wait_timeout(int kernel, long long limit_cycles);
  * Rows are [tokens, heads, d] with the heads of a token contiguous; a token stride (in elements,
  * a multiple of 16 bytes) lets them be slices of a fused projection.  dtype is OQ_BF16, OQ_F16
  * or, where a call says so, OQ_F32.  oq_apply_rope, oq_kv_write and oq_kv_read are one kernel each
- * on `stream` and allocate nothing (after their handles' first use on the device); oq_kv_attend is
+ * on `stream` and allocate nothing; oq_kv_attend is
  * one kernel where the page tables can hold little, else three, with a workspace that it takes
  * from the device's stream-ordered pool and gives back on `stream`.  Nothing is kept from one call
- * for the next, so calls on several streams and captured graphs may run at the same time. */
+ * for the next, so calls on several streams and captured graphs may run at the same time.  The first
+ * call of each kind and dtype with a handle on a device uploads tables: make it before a capture. */
 typedef struct oq_rope oq_rope;
 
 #define OQ_KV_MAX_HEADS 1024  /* heads of a token                                          */
@@ -330,7 +331,8 @@ typedef struct {
  * 1e-8), for every head's row, as oq_quantize_act does for a row of dimension d.  k, v: device,
  * [T, kv_heads, d] of dtype (OQ_F32, OQ_BF16, OQ_F16).  slots: device, int64 [T]; -1 skips the
  * token (padding); the others must differ from one another (a slot named twice ends up with
- * either token's rows or a mixture of them; no other slot is touched).  A slot outside the cache
+ * either token's rows or a mixture of them; no other slot is touched).  A coordinate within 1e-5 of a
+ * boundary (of the unit centroids) may take either code, in calls of other sizes another one.  A slot outside the cache
  * is skipped and reported by oq_check.  A row with a NaN or infinity, or whose squares pass fp32,
  * gets a norm that is not finite; no other row feels it.  T = 0 is a no-op, T * kv_heads at most 2^36.
  * Errors: OQ_EINVAL, OQ_EUNSUPPORTED, OQ_ECUDA. */
@@ -352,7 +354,8 @@ int oq_kv_read(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache,
  * prefix and the nodes j with bit j of tree_mask[row] set (its ancestors and itself, in any
  * order); with tree_mask = NULL the nodes up to its own, so one node a sequence is a plain
  * decoding step.  out = sum_t p_t v_hat_t, p the softmax of scale * q . k_hat_t over the tokens it
- * sees; a row that sees nothing gives zeros.  scale > 0, and scale * log2(e) finite in fp32.  Query head i reads key head i / (q_heads/kv_heads).
+ * sees; a row that sees nothing gives zeros.  scale > 0, and scale * log2(e) finite in fp32.  Query
+ * head i reads key head i / (q_heads/kv_heads).
  * q, out: device, [q_rows, q_heads, d] of dtype (OQ_BF16 or OQ_F16); out = q with the same stride
  * works in place, any other overlap is not allowed.  q_start: int32 [B+1];
  * prefix: int32 [B]; page_table: int32 [B, table_width] (entries past a sequence's last page are
@@ -360,7 +363,7 @@ int oq_kv_read(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache,
  * workspace has 4 to 8 bytes for each of B * max_nodes * q_heads * d elements, a key head's rows
  * rounded up to tiles of 8, 16 or 128, and 10 MB more.  Rows of out outside every sequence
  * are left as they were.  What is not visible is never multiplied: masked tokens may hold
- * anything.  A sequence whose rows or lengths do not fit (q_start decreasing, past q_rows or over
+ * anything.  Values are summed down to 2^-31 of the longest one that a row sees.  A sequence whose rows or lengths do not fit (q_start decreasing, past q_rows or over
  * max_nodes; prefix negative or past the table) is skipped, a token whose page is outside the
  * cache is not seen, and oq_check reports both.  The same call gives the same bits; how a long row's
  * sum is split depends on the whole call, so other sequences beside it may change its rounding.
