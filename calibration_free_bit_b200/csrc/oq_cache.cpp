@@ -150,13 +150,21 @@ void build_kv_lut(oq_codebook *cb) {
         const double hi = i + 1 < L ? cb->t[i] : 2.0 * cb->c[L - 1] - cb->t[L - 2];
         mass[i] = std::exp(-0.5 * cb->c[i] * cb->c[i]) * (hi - lo);
     }
+    // x to the 11 significant bits of fp16 (all of a c is in its normal range), to nearest even
+    auto rounded = [](double x) {
+        uint64_t u;
+        std::memcpy(&u, &x, 8);
+        u = (u + ((1ull << 41) - 1) + ((u >> 42) & 1)) & ~((1ull << 42) - 1);
+        std::memcpy(&x, &u, 8);
+        return x;
+    };
     double best = -1.0;
     const int tries = L <= 16 ? 4096 : 4096 / L;  // of many centroids all factors leave about the same
     for (int k = 0; k < tries; ++k) {
         const double a = 1.0 + (double)k / tries;
         double err = 0.0;
         for (int i = L / 2; i < L; ++i) {
-            const double d = value(to_half_bits(a * cb->c[i])) / a - cb->c[i];
+            const double d = rounded(a * cb->c[i]) / a - cb->c[i];
             err += mass[i] * d * d;
         }
         if (best < 0.0 || err < best) {
