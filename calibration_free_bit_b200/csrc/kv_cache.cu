@@ -79,7 +79,8 @@ __global__ void __launch_bounds__(32 * kWarps) kv_write_rows(const KvWriteParams
         for (int s = 16; s; s >>= 1)
             sum += __shfl_xor_sync(0xffffffffu, sum, s);
         const float norm = sqrtf(sum / (float)p.h);
-        const float k = p.K / (norm + p.eps), unit = p.unit / (norm + p.eps);
+        const float k = p.K / (norm + p.eps);
+        uint32_t beside = 0;                             // bit i: a second look
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const float a = fma_sat(z[i], k, 0.5f);
@@ -87,10 +88,38 @@ __global__ void __launch_bounds__(32 * kWarps) kv_write_rows(const KvWriteParams
             const uint32_t word = p.tbl[((q - 0x3F800000u) >> p.F) * p.tbl_copies];
             const uint32_t at = word + q * (uint32_t)p.G;
             uint32_t code = at >> 24;
-            if (distance_to_bound(at, p.G) < bound_width(p.G))
-                code = code_beside(code, z[i] * unit, __ldg(p.bounds + (code ? code - 1 : 0)),
-                                   __ldg(p.bounds + code), p.c.bits);
+            if (distance_to_bound(at, p.G) < bound_width(p.G)) {
+                if (z[i] == 0.f)
+                    code = code_of_zero(p.c.bits);
+                else
+                    beside |= 1u << i;
+            }
             cs[warp][lane * N + i] = (uint8_t)code;
+        }
+        beside = looks(norm) ? beside : 0u;
+        __syncwarp();
+#pragma unroll 1
+        for (uint32_t any = __reduce_or_sync(0xffffffffu, beside); any; any &= any - 1) {
+            const int i = __ffs(any) - 1;
+#pragma unroll 1
+            for (uint32_t lanes = __ballot_sync(0xffffffffu, (beside >> i) & 1u); lanes;
+                 lanes &= lanes - 1) {
+                const int at = (__ffs(lanes) - 1) * N + i;
+                double sum = 0.0, squares = 0.0;
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const int pos = lane * N + j;
+                    const double v = xs[warp][ent[j] & 0x7fffu];
+                    squares += v * v;
+                    if ((pos ^ at) < p.h)                // in one block
+                        sum += ((ent[j] >> 15) ^ __popc(pos & at & (p.h - 1))) & 1u ? -v : v;
+                }
+                const uint32_t code = code_beside(cs[warp][at], sum, squares, norm, p.unit, p.bounds,
+                                                  p.c.bits);
+                __syncwarp();
+                if (lane == 0)
+                    cs[warp][at] = (uint8_t)code;
+            }
         }
         __syncwarp();
         const long long at = cache_row(p.c, slot, o.head);
@@ -193,8 +222,9 @@ cudaError_t error_word(unsigned **out) {
 }
 
 // Rows (keys and values) from which the tensor cores' form is taken.  It and a warp a row, write (read),
-// us: d = 128, 4 bits, 4096 rows 6.5 and 5.9 (5.2 and 4.0), 16384 rows 7.3 and 11.5 (6.5 and 8.5); d =
-// 256, 2 bits, 4096 rows 7.2 and 6.9 (6.6 and 4.9), 16384 rows 8.7 and 15.8 (8.4 and 11.5).
+// us: d = 128, 4 bits, 4096 rows 7.2 and 6.0 (4.4 and 3.7), 8192 rows 7.3 and 8.5 (4.4 and 5.1), 16384
+// rows 8.0 and 13.2 (5.6 and 7.7); d = 256, 2 bits, 4096 rows 7.8 and 7.0 (5.7 and 4.5), 16384 rows 9.1
+// and 17.2 (7.6 and 11.0).
 constexpr long long kTensorRows = 8192;
 
 }  // namespace

@@ -60,8 +60,8 @@ struct KvWriteParams {
     const uint16_t *ent;          // [d] perm | sign bit << 15
     const uint32_t *tbl;          // quantizer grid words (each `tbl_copies` times)
     int tbl_copies, tbl_words;
-    const float *bounds;          // the codes' 2^bits - 1 boundaries, of a row over its norm / unit
-    float unit;
+    const float *bounds;          // the codes' 2^bits - 1 boundaries as fp32, and (2^bits on) the rests
+    double unit;                  // sqrt(d / h)
     const void *r_img;            // R' as the tensor cores' operand in x's type (16-bit x)
     int wide;                     // code rows keep 32-byte stores aligned
     unsigned *err;                // device error word (set by launch_kv_write)

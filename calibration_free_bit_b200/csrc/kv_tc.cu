@@ -13,8 +13,9 @@
 // work on tiles of their own; at d = 256 R' takes 128 KB and leaves room for one group of 256.
 // B200, bf16: 32760 tokens of 40 heads of 128 at 8 bits, write 317 us (3.2 TB/s), read 291 us (3.5 TB/s),
 // both bound by shared memory (the quantizer's table has one copy at 8 bits, so its lookups conflict;
-// lookups, operand and finished rows of a read); 2011 tokens of 8 heads at 4 bits, 8.6 and 6.9 us, of
-// which 5 are the set-up; fp16, 5003 tokens of 4 heads of 256 at 2 bits, 18.9 and 13.7 us.
+// lookups, operand and finished rows of a read); 2011 tokens of 8 heads at 4 bits, 9.3 and 7.0 us, of
+// which 5 are the set-up; fp16, 5003 tokens of 4 heads of 256 at 2 bits, 20.3 and 14.0 us (values beside
+// a boundary take 0.6 and 1.3 of the writes).
 #include "k1_ops.cuh"
 #include "kv_internal.h"
 #include "kv_lut.cuh"
@@ -140,14 +141,15 @@ __device__ __forceinline__ void tmem_ld1(uint32_t at, uint32_t &r) {
 }
 
 // Few codes are far apart, so a wrong one beside a boundary shows in fp16 rows; with 8 bits it is off by
-// less than their rounding, and is left (a few of a million, which a smaller call, kv_cache.cu, may take
-// the other way).
+// less than their rounding, and is left (300 of a million are beside one, and a second look at each would
+// take a tenth of the time; a few of them fall the other way in a smaller call, kv_cache.cu).
 template <int BITS> constexpr bool kLook = BITS <= 6;
 
 template <int D, int BITS, bool BF16>
 __global__ void __launch_bounds__(Geo<D>::threads, 1)
 kv_write_tc(const KvWriteParams p, const uint4 *r_img, const int tbl_words, const int tiles) {
     using G = Geo<D>;
+    using X = std::conditional_t<BF16, __nv_bfloat16, __half>;
     extern __shared__ unsigned char raw[];
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     unsigned char *sm = raw + (base - smem_u32(raw));
@@ -166,6 +168,7 @@ kv_write_tc(const KvWriteParams p, const uint4 *r_img, const int tbl_words, cons
     const int grp = threadIdx.x / G::group_threads, tid = threadIdx.x % G::group_threads;
     const int lane = threadIdx.x & 31, row = tid & 127, part = tid >> 7;
     const uint32_t sR = base, sA = base + G::r_bytes + grp * G::a_bytes, bar = bars + 8 * grp;
+    const unsigned char *a_sm = sm + G::r_bytes + grp * G::a_bytes;
     const uint32_t tmem = tmem0 + grp * D;
     const uint32_t my_tmem = tmem + ((uint32_t)(row & ~31) << 16) + part * 128;
     const int heads = p.c.kv_heads, half_tiles = tiles / 2;
@@ -201,9 +204,6 @@ kv_write_tc(const KvWriteParams p, const uint4 *r_img, const int tbl_words, cons
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-    // lane j: boundaries j and, of 6 bits, 32 + j
-    const float bound = kLook<BITS> && lane < (1 << BITS) - 1 ? __ldg(p.bounds + lane) : 0.f;
-    const float bound2 = BITS == 6 && lane < 31 ? __ldg(p.bounds + 32 + lane) : 0.f;
     bool dead = false;
     uint32_t phase = 0;
     const int stride = gridDim.x * G::groups;
@@ -255,7 +255,7 @@ kv_write_tc(const KvWriteParams p, const uint4 *r_img, const int tbl_words, cons
             sum = half_sum[row] + half_sum[row + 128];
         }
         const float norm = sqrtf(sum / (float)p.h);
-        const float kk = p.K / (norm + p.eps), unit = p.unit / (norm + p.eps);
+        const float kk = p.K / (norm + p.eps);
         uint32_t out[4 * BITS], beside[4], any = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -274,8 +274,7 @@ kv_write_tc(const KvWriteParams p, const uint4 *r_img, const int tbl_words, cons
                 for (int i = 0; i < 32; ++i)
                     least = min(least, distance_to_bound(z[i], p.G));
                 beside[k] = 0;
-                // (all of an empty row is 0, on the middle one)
-                const bool look = dst >= 0 && norm > 0.f && least < bound_width(p.G);
+                const bool look = dst >= 0 && looks(norm) && least < bound_width(p.G);
                 if (__any_sync(0xffffffffu, look)) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
@@ -287,8 +286,8 @@ kv_write_tc(const KvWriteParams p, const uint4 *r_img, const int tbl_words, cons
             pack32<BITS>(z, out + k * BITS);
         }
         if constexpr (kLook<BITS>) {
-            // values beside a boundary, by all lanes a column at a time (a tile has a few of them, and
-            // this code for all columns at once would cost it more than they do)
+            // values beside a boundary, by all lanes one at a time (a tile has few of them, and this code
+            // for all columns at once would cost it more than they do)
 #pragma unroll 1
             for (; any; any &= any - 1) {
                 const int k = __ffs(any) - 1;
@@ -298,21 +297,44 @@ kv_write_tc(const KvWriteParams p, const uint4 *r_img, const int tbl_words, cons
                     const int b = __ffs(cols) - 1, bit = (32 * k + b) * BITS, s = bit & 31;
                     uint32_t z;
                     tmem_ld1(my_tmem + 32 * k + b, z);
-                    const float v = __uint_as_float(z) * unit;
                     const uint32_t q = __float_as_uint(
                         __fadd_rd(fma_sat(__uint_as_float(z), kk, 0.5f), 1.0f));
                     const uint32_t was =
                         (k1ops::lds32(my_tbl + (q >> p.F) * pitch) + q * (uint32_t)p.G) >> 24;
-                    float below = __shfl_sync(0xffffffffu, bound, was - 1);
-                    float above = __shfl_sync(0xffffffffu, bound, was);
-                    if constexpr (BITS == 6) {
-                        const float b2 = __shfl_sync(0xffffffffu, bound2, was - 1);
-                        const float a2 = __shfl_sync(0xffffffffu, bound2, was);
-                        below = was > 32 ? b2 : below;
-                        above = was >= 32 ? a2 : above;
+                    const bool zero = __uint_as_float(z) == 0.f;
+                    uint32_t x = ((mine >> b) & 1u) && zero ? was ^ code_of_zero(BITS) : 0u;
+#pragma unroll 1
+                    for (uint32_t lanes = __ballot_sync(0xffffffffu, ((mine >> b) & 1u) && !zero); lanes;
+                         lanes &= lanes - 1) {
+                        // a lane's D / 32 elements of the row (which is still the operand, if this was
+                        // the group's last tile) and of the rotation's
+                        const int l = __ffs(lanes) - 1, r = (row & ~31) + l;
+                        constexpr int N = D / 32;
+                        const int ch = lane * N / 8, in = lane * N % 8 * 2;
+                        const X *from;
+                        if (tile + stride < tiles) {
+                            const long long at = (long long)(tile - w * half_tiles) * 128 + r;
+                            const long long tok = at / heads;
+                            from = static_cast<const X *>(pick(p.x, w)) + tok * pick(p.x_stride, w) +
+                                   (at - tok * heads) * D + lane * N;
+                        } else {
+                            from = reinterpret_cast<const X *>(a_sm + operand_at(r, ch, 128) + in);
+                        }
+                        const X *turn = reinterpret_cast<const X *>(
+                            sm + operand_at(part * 128 + 32 * k + b, ch, D) + in);
+                        double sum = 0.0, squares = 0.0;
+#pragma unroll
+                        for (int i = 0; i < N; ++i) {
+                            const double v = to_f32(from[i]);
+                            sum += v * (double)to_f32(turn[i]);
+                            squares += v * v;
+                        }
+                        const uint32_t code =
+                            code_beside(__shfl_sync(0xffffffffu, was, l), sum, squares,
+                                        __shfl_sync(0xffffffffu, norm, l), p.unit, p.bounds, BITS);
+                        if (lane == l)
+                            x = was ^ code;
                     }
-                    uint32_t x = was ^ code_beside(was, v, below, above, BITS);
-                    x = (mine >> b) & 1u ? x : 0u;
 #pragma unroll
                     for (int i = 0; i < 4 * BITS; ++i) {
                         out[i] ^= i == bit >> 5 ? x << s : 0u;

@@ -389,7 +389,7 @@ int oq_kv_write(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache
     p.tbl_copies = c->bits <= 4 ? 32 : 1;
     p.tbl_words = (int)cw->tbl_img.size();
     p.bounds = reinterpret_cast<const float *>(cw->dev_cent32[dev]) + (1 << c->bits);
-    p.unit = (float)std::sqrt((double)r->d / r->h);
+    p.unit = std::sqrt((double)r->d / r->h);
     p.wide = p.c.row_bytes % 32 == 0 &&
              ((reinterpret_cast<uintptr_t>(cache->k_codes) |
                reinterpret_cast<uintptr_t>(cache->v_codes)) & 31u) == 0;

@@ -40,7 +40,8 @@ struct oq_codebook {
     std::mutex mu;
     uint32_t *dev_tbl[oq::kMaxDevices] = {};
     uint32_t *dev_dec[oq::kMaxDevices] = {};
-    std::vector<float> cent32;                    // unit centroids, then boundaries, fp32 (the cache)
+    std::vector<float> cent32;                    // the cache: unit centroids, boundaries, and
+                                                  // what fp32 leaves of those
     uint32_t *dev_cent32[oq::kMaxDevices] = {};
     // the cache's fp16 decode table (oq_cache.cpp, decode_table: made at its first use): centroids
     // times kv_alpha

@@ -1037,12 +1037,14 @@ int oq_lloyd_max_marginal(int d, int bits, int marginal, oq_codebook **out) {
     cb->t.resize(L - 1);
     for (int j = 0; j < L - 1; ++j)
         cb->t[j] = 0.5 * (cb->c[j] + cb->c[j + 1]);
-    cb->cent32.resize(2 * (size_t)L);             // centroids, boundaries
+    cb->cent32.resize(3 * (size_t)L);             // centroids, boundaries, their rests
     for (int i = 0; i < L; ++i) {
         cb->lut[i] = to_half_bits(cb->c[i]);
         cb->cent32[i] = (float)cb->c[i];
-        if (i + 1 < L)                            // (the middle one is 0)
-            cb->cent32[L + i] = std::fabs(cb->t[i]) < 1e-12 ? 0.f : (float)cb->t[i];
+        if (i + 1 < L && std::fabs(cb->t[i]) >= 1e-12) {   // (the middle one is 0)
+            cb->cent32[L + i] = (float)cb->t[i];
+            cb->cent32[2 * L + i] = (float)(cb->t[i] - (double)cb->cent32[L + i]);
+        }
     }
     if (!build_grid(cb)) {
         delete cb;

@@ -331,8 +331,9 @@ typedef struct {
  * 1e-8), for every head's row, as oq_quantize_act does for a row of dimension d.  k, v: device,
  * [T, kv_heads, d] of dtype (OQ_F32, OQ_BF16, OQ_F16).  slots: device, int64 [T]; -1 skips the
  * token (padding); the others must differ from one another (a slot named twice ends up with
- * either token's rows or a mixture of them; no other slot is touched).  A coordinate within 1e-5 of a
- * boundary (of the unit centroids) may take either code, in calls of other sizes another one.  A slot outside the cache
+ * either token's rows or a mixture of them; no other slot is touched).  Codes are the
+ * formula's in fp64, in calls of any size, but for 8 bits in calls of 2 * T * kv_heads >= 8192 rows of
+ * 16 bits: there a coordinate within 1e-5 of a boundary may take either of its codes.  A slot outside the cache
  * is skipped and reported by oq_check.  A row with a NaN or infinity, or whose squares pass fp32,
  * gets a norm that is not finite; no other row feels it.  T = 0 is a no-op, T * kv_heads at most 2^36.
  * Errors: OQ_EINVAL, OQ_EUNSUPPORTED, OQ_ECUDA. */

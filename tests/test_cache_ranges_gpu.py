@@ -4,7 +4,10 @@ import numpy as np
 import pytest
 import torch
 
-from test_cache_gpu import BF16, F16, ROOMY, Serving, close, oq  # noqa: F401  (oq: a fixture)
+import _cache_oracle as CO
+import oracle as O
+from test_cache_gpu import (BF16, F16, ROOMY, Serving, close, f64,  # noqa: F401  (oq: a fixture)
+                            make_rows, oq)
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +80,50 @@ def test_scores_far_below_zero(oq, d, nodes, roomy):  # noqa: F811
     out = oq.oq_kv_attend(**s.gpu())
     oq.oq_check()
     close(out, s.want(), BF16)
+
+
+@pytest.mark.parametrize("T,H,d,h,bits,dtype", [
+    (20000, 4, 128, 128, 2, BF16), (12000, 4, 256, 128, 2, F16), (20000, 4, 128, 32, 3, F16),
+    (20000, 4, 128, 128, 4, BF16), (9000, 4, 256, 256, 4, BF16), (9000, 4, 128, 64, 6, BF16),
+    (5000, 4, 256, 128, 6, F16),                                  # the tensor cores' form
+    (1000, 4, 128, 128, 2, BF16), (500, 4, 256, 64, 4, F16), (1000, 4, 128, 128, 6, F16),
+    (1000, 4, 128, 128, 8, BF16), (500, 4, 256, 256, 8, BF16),    # a warp a row
+    (20000, 4, 128, 128, 4, torch.float32), (6000, 4, 256, 64, 8, torch.float32)])
+def test_codes_are_the_nearest_centroids(oq, T, H, d, h, bits, dtype):  # noqa: F811
+    """Every code is the fp64 oracle's, those beside a boundary too (of values more than 1e-13 from
+    one), and so the same in calls of any size.  (At 8 bits large calls of 16-bit rows have one code
+    more or less there.)"""
+    rows = make_rows(T, H, d, dtype, 7)
+    r, c = oq.oq_build_rpbh(d, h, 0), oq.oq_lloyd_max(d, bits)
+    cache = oq.KVCache.empty(-(-T // 16), H, 16, d, bits)
+    oq.oq_kv_write(r, c, cache, rows.cuda(), rows.cuda(), torch.arange(T).cuda())
+    oq.oq_check()
+    assert torch.equal(cache.k_codes, cache.v_codes)
+    packed = cache.k_codes.transpose(1, 2).reshape(-1, H, d * bits // 8)[:T].cpu().numpy()
+    R, t = CO.rotation(d, h), O.codebook(bits)[1]
+    for a in range(0, T, 1000):
+        want, _, u = CO.quantize(f64(rows[a:a + 1000]), R, bits)
+        got = CO.unpack(packed[a:a + 1000], bits)
+        for i in np.argwhere(got != want):
+            assert np.abs(t - u[tuple(i)]).min() <= 1e-13, (a, i, u[tuple(i)])
+
+
+@pytest.mark.parametrize("T", [50, 5000])
+def test_rows_of_few_distinct_values(oq, T):  # noqa: F811
+    """Rows whose rotation has exact zeros, on the middle boundary: the upper code, as the oracle's."""
+    d, bits = 128, 4
+    rows = torch.zeros(T, 1, d)
+    rows[torch.arange(T), 0, torch.arange(T) % d] = 3.0
+    rows[::3] = 1.0
+    r, c = oq.oq_build_rpbh(d, 64, 0), oq.oq_lloyd_max(d, bits)
+    cache = oq.KVCache.empty(-(-T // 16), 1, 16, d, bits)
+    x = rows.to(BF16).cuda()
+    oq.oq_kv_write(r, c, cache, x, x, torch.arange(T).cuda())
+    oq.oq_check()
+    got = CO.unpack(cache.k_codes.view(-1, d // 2)[:T].cpu().numpy(), bits)
+    z = f64(rows[:, 0]) @ CO.rotation(d, 64).T
+    z[np.abs(z) < 1e-12] = 0.0                                    # (fp64's own roundings)
+    u = z / np.linalg.norm(z, axis=-1, keepdims=True) * np.sqrt(d)
+    t = O.codebook(bits)[1].copy()
+    t[len(t) // 2] = 0.0
+    assert np.array_equal(got, np.searchsorted(t, u, side="right"))
