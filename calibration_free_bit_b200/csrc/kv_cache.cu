@@ -98,12 +98,13 @@ __global__ void __launch_bounds__(32 * kWarps) kv_write_rows(const KvWriteParams
         }
         beside = looks(norm) ? beside : 0u;
         __syncwarp();
+        int left = kLooks;
 #pragma unroll 1
         for (uint32_t any = __reduce_or_sync(0xffffffffu, beside); any; any &= any - 1) {
             const int i = __ffs(any) - 1;
 #pragma unroll 1
-            for (uint32_t lanes = __ballot_sync(0xffffffffu, (beside >> i) & 1u); lanes;
-                 lanes &= lanes - 1) {
+            for (uint32_t lanes = __ballot_sync(0xffffffffu, (beside >> i) & 1u); lanes && left > 0;
+                 lanes &= lanes - 1, --left) {
                 const int at = (__ffs(lanes) - 1) * N + i;
                 double sum = 0.0, squares = 0.0;
 #pragma unroll

@@ -26,11 +26,16 @@ __device__ __forceinline__ bool slot_ok(const KvView &c, long long slot) {
 // four steps of one, or of a cell's end (of normal values 5, 15 and 26 in a million at 2, 3 and 4 bits),
 // is looked at again: in fp64 from the row itself, so that neither the order of fp32 sums nor the form
 // that a call takes decides its code (one code off at 2 bits is an error of the value's own size).  An
-// exact 0, which rows of few distinct values have many of, needs no second look.
+// exact 0, which rows of few distinct values have many of, needs no second look, and a row has four at
+// most: normal values need a fifth in fewer than one row of 10 million, but one with an element a million
+// times the others would have all of its other blocks beside 0, and a call of such rows take 100 times
+// as long.
 __device__ __forceinline__ uint32_t distance_to_bound(uint32_t at, int G) {
     return at * 256u + (uint32_t)G * 1024u;
 }
 __device__ __forceinline__ uint32_t bound_width(int G) { return (uint32_t)G * 2048u; }
+
+constexpr int kLooks = 4;       // second looks of a row
 
 // Whether a row of this norm has second looks (all of an empty row is 0; fp32 has no codes for a norm
 // that is not finite, or lost in underflow).

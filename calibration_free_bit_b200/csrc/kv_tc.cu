@@ -288,6 +288,7 @@ kv_write_tc(const KvWriteParams p, const uint4 *r_img, const int tbl_words, cons
         if constexpr (kLook<BITS>) {
             // values beside a boundary, by all lanes one at a time (a tile has few of them, and this code
             // for all columns at once would cost it more than they do)
+            int left = kLooks;                         // of this lane's row
 #pragma unroll 1
             for (; any; any &= any - 1) {
                 const int k = __ffs(any) - 1;
@@ -304,8 +305,8 @@ kv_write_tc(const KvWriteParams p, const uint4 *r_img, const int tbl_words, cons
                     const bool zero = __uint_as_float(z) == 0.f;
                     uint32_t x = ((mine >> b) & 1u) && zero ? was ^ code_of_zero(BITS) : 0u;
 #pragma unroll 1
-                    for (uint32_t lanes = __ballot_sync(0xffffffffu, ((mine >> b) & 1u) && !zero); lanes;
-                         lanes &= lanes - 1) {
+                    for (uint32_t lanes = __ballot_sync(0xffffffffu, ((mine >> b) & 1u) && !zero && left > 0);
+                         lanes; lanes &= lanes - 1) {
                         // a lane's D / 32 elements of the row (which is still the operand, if this was
                         // the group's last tile) and of the rotation's
                         const int l = __ffs(lanes) - 1, r = (row & ~31) + l;
@@ -332,8 +333,10 @@ kv_write_tc(const KvWriteParams p, const uint4 *r_img, const int tbl_words, cons
                         const uint32_t code =
                             code_beside(__shfl_sync(0xffffffffu, was, l), sum, squares,
                                         __shfl_sync(0xffffffffu, norm, l), p.unit, p.bounds, BITS);
-                        if (lane == l)
+                        if (lane == l) {
                             x = was ^ code;
+                            --left;
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < 4 * BITS; ++i) {

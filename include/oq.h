@@ -331,11 +331,12 @@ typedef struct {
  * 1e-8), for every head's row, as oq_quantize_act does for a row of dimension d.  k, v: device,
  * [T, kv_heads, d] of dtype (OQ_F32, OQ_BF16, OQ_F16).  slots: device, int64 [T]; -1 skips the
  * token (padding); the others must differ from one another (a slot named twice ends up with
- * either token's rows or a mixture of them; no other slot is touched).  Codes are the
- * formula's in fp64, in calls of any size, but for 8 bits in calls of 2 * T * kv_heads >= 8192 rows of
- * 16 bits: there a coordinate within 1e-5 of a boundary may take either of its codes.  A slot outside the cache
- * is skipped and reported by oq_check.  A row with a NaN or infinity, or whose squares pass fp32,
- * gets a norm that is not finite; no other row feels it.  T = 0 is a no-op, T * kv_heads at most 2^36.
+ * either token's rows or a mixture of them; no other slot is touched).  Codes are the formula's in
+ * fp64, in calls of any size, with two exceptions, where a coordinate within 1e-5 of a boundary may take
+ * either of its codes: 8 bits in calls of 2 * T * kv_heads >= 8192 rows of 16-bit values, and rows with
+ * more than four such coordinates.  A slot outside the cache is skipped and reported by oq_check.  A row
+ * with a NaN or infinity, or whose squares pass fp32, gets a norm that is not finite; no other row feels
+ * it.  T = 0 is a no-op, T * kv_heads at most 2^36.
  * Errors: OQ_EINVAL, OQ_EUNSUPPORTED, OQ_ECUDA. */
 int oq_kv_write(const oq_rpbh *r, const oq_codebook *c, const oq_kv_cache *cache, const void *k,
                 long long k_stride, const void *v, long long v_stride, int dtype, int T,

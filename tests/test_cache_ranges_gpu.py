@@ -127,3 +127,23 @@ def test_rows_of_few_distinct_values(oq, T):  # noqa: F811
     t = O.codebook(bits)[1].copy()
     t[len(t) // 2] = 0.0
     assert np.array_equal(got, np.searchsorted(t, u, side="right"))
+
+
+@pytest.mark.parametrize("T,dtype", [(300, BF16), (300, torch.float32), (5000, BF16)])
+def test_rows_with_one_huge_element(oq, T, dtype):  # noqa: F811
+    """An element 1e7 times the others: its block has codes far from a boundary, the others' blocks lie
+    within 1e-5 of the middle one and have either of its codes."""
+    d, h, bits = 128, 32, 4
+    rows = torch.randn(T, 1, d, generator=torch.Generator().manual_seed(8))
+    rows[torch.arange(T), 0, torch.arange(T) % d] = 1e7
+    rows = rows.to(dtype)
+    r, c = oq.oq_build_rpbh(d, h, 0), oq.oq_lloyd_max(d, bits)
+    cache = oq.KVCache.empty(-(-T // 16), 1, 16, d, bits)
+    oq.oq_kv_write(r, c, cache, rows.cuda(), rows.cuda(), torch.arange(T).cuda())
+    oq.oq_check()
+    got = CO.unpack(cache.k_codes.view(-1, d // 2)[:T].cpu().numpy(), bits)
+    want, norm, u = CO.quantize(f64(rows[:, 0]), CO.rotation(d, h), bits)
+    np.testing.assert_allclose(cache.k_norms.view(-1)[:T].cpu().double().numpy(), norm, rtol=5e-6)
+    near = np.abs(u) <= 1e-5
+    assert near.mean() > 0.7 and np.array_equal(got[~near], want[~near])
+    assert np.all((got[near] == 7) | (got[near] == 8))
