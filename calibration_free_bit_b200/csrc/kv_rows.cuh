@@ -50,7 +50,7 @@ __device__ __forceinline__ uint32_t code_of_zero(int bits) { return 1u << (bits 
 __device__ __forceinline__ uint32_t code_beside(uint32_t code, double z, double n, float norm,
                                                 double unit, const float *bounds, int bits) {
     const uint32_t L = 1u << bits;
-    auto bound = [&](uint32_t j) { return (double)__ldg(bounds + j) + (double)__ldg(bounds + L + j); };
+    auto bound = [&](uint32_t j) { return (double)bounds[j] + (double)bounds[L + j]; };
     const double below = code > 0 ? bound(code - 1) : 0.0, above = code + 1 < L ? bound(code) : 0.0;
 #pragma unroll
     for (int k = 16; k; k >>= 1) {
